@@ -420,7 +420,7 @@ def _plan(s):
     held = (ctx - ql + BLOCK - 1) // BLOCK
     need = (ctx + BLOCK - 1) // BLOCK - held
     base = torch.cumsum(need, 0) - need
-    granted = base + need <= s["n_free"]
+    granted = (need == 0) | (base + need <= s["n_free"])
     need = torch.where(granted, need, 0)
     j = torch.arange(bt.shape[1], device="cuda") - held[:, None]
     new = (j >= 0) & (j < need[:, None])
