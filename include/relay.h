@@ -23,8 +23,12 @@
  * composing such a tree from the separate steps), relay_baseline_decode (the
  * non-relay formulation), and
  * the steps on either side of the path: relay_kv_append (cache write),
- * relay_rope (rotary positions offset by the system prompt) and
- * relay_sys_prefill (causal attention of the system prompt itself).
+ * relay_rope (rotary positions offset by the system prompt; relay_rope_axes
+ * for positions with several axes), relay_block_plan / relay_block_release
+ * (block tables and slot maps on the device) and relay_sys_prefill (causal
+ * attention of the system prompt itself).  relay_kv_append_q4,
+ * relay_ctx_attn_q4 and relay_attention_decode_q4 are the calls with the
+ * contexts in a 4-bit pool.
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -98,6 +102,10 @@ typedef enum {
 #define RELAY_FLAG_Q_TOTAL      8u  /* sum of q_lens above max_q_total */
 #define RELAY_FLAG_WAIT_TIMEOUT 16u  /* a bounded wait inside the tensor-core kernel gave up;
                                        that call's outputs are not valid */
+
+#define RELAY_FLAG_POOL         32u  /* relay_block_plan: the free list is too short for a request (or its
+                                       count is outside [0, num_blocks]); relay_block_release: more blocks
+                                       than the pool has */
 
 /* Opaque CUDA stream (binary-compatible with cudaStream_t); NULL = legacy stream. */
 typedef struct CUstream_st *relay_stream_t;
@@ -300,6 +308,118 @@ relay_status_t relay_sys_prefill(const relay_dims_t *dims, const void *q_sys, co
 relay_status_t relay_rope(const relay_dims_t *dims, void *q, void *k_new, const int32_t *ctx_lens,
                           const int32_t *q_lens, float base, void *ws, size_t ws_bytes,
                           relay_stream_t stream);
+
+/* Rotary position embedding with several position axes (time, height and
+ * width of images and video beside the position of text), with the
+ * system-prompt offset of relay_rope.  Token (b, i), i < q_lens[b], has one
+ * position per axis, positions[a][b][i] ([n_axes, B, Lq] int32, any value);
+ * pair j < D/2 of every head (x[j], x[j + D/2]) turns by the angle
+ *     (Ls + positions[pair_axis[j]][b][i]) * base^(-2j/D)
+ * in the rotate-half form of relay_rope, or by its negative when `inverse` is
+ * not 0 (which undoes the rotation, and is also its gradient).  pair_axis:
+ * HOST array of D/2 axis numbers below n_axes <= RELAY_MAX_ROPE_AXES, in any
+ * arrangement (runs of pairs per axis, or the axes in turn).  Equal positions
+ * on every axis give relay_rope's angles.  Angles are formed as 64-bit
+ * fixed-point fractions of a turn, the rotation in fp32, results rounded to
+ * fp16.  q -> q_out: [B, Lq, H, D]; k_new -> k_out: [B, Lq, Hkv, D] fp16, both
+ * NULL or neither; an output may be its input (in place) but not overlap it
+ * otherwise.  Rows i >= q_lens[b] of the outputs are left untouched; a request
+ * with q_len outside [0, Lq] is skipped and flagged.  ws: at least 256 bytes
+ * (flag word). */
+#define RELAY_MAX_ROPE_AXES 4
+relay_status_t relay_rope_axes(const relay_dims_t *dims, const void *q, const void *k_new, const int32_t *positions,
+                               int n_axes, const uint8_t *pair_axis, const int32_t *q_lens, float base, int inverse,
+                               void *q_out, void *k_out, void *ws, size_t ws_bytes, relay_stream_t stream);
+
+/* The step's block bookkeeping on the device: block tables and slot maps
+ * from the request lengths, with no host round trip (the call can sit in a
+ * CUDA graph in front of the append and the attention).  ctx_lens already
+ * counts the step's q_lens[b] new tokens, as everywhere.  Request b holds
+ * ceil((ctx_lens[b] - q_lens[b]) / 16) blocks, named by the front of its
+ * block-table row, and needs ceil(ctx_lens[b] / 16); the missing ones are
+ * taken from the end of the free list in request order:
+ *     block_tables[b][held + j] = free_blocks[n_free - 1 - (base_b + j)],
+ * base_b the blocks that requests before b need.  A request whose blocks do
+ * not all fit gets none, and neither does any later one that needs some
+ * (RELAY_FLAG_POOL).  n_free_out[0] = n_free[0] minus the blocks handed out;
+ * it may be n_free itself.  Other table entries and the list are left as they
+ * are.  slot_map (nullable): [B, Lq], block * 16 + row of the pool of token
+ * (b, i), and -1 where there is none: rows i >= q_lens[b], and all rows of a
+ * request that is refused its blocks or has a length out of range (flagged,
+ * as in relay_kv_append).  An id outside [0, num_blocks) in the list or the
+ * table gives slot -1 and RELAY_FLAG_BAD_BLOCK.
+ *  - free_blocks: [num_blocks] int32, the first n_free[0] in use; n_free,
+ *    n_free_out: device int32.  Uses dims->B, Lq, num_blocks,
+ *    max_blocks_per_seq; 16 * num_blocks must be below 2^31.
+ *  - ws: at least 256 bytes, zero before its first use (flag word and a
+ *    counter that every call leaves at zero). */
+relay_status_t relay_block_plan(const relay_dims_t *dims, const int32_t *ctx_lens, const int32_t *q_lens,
+                                const int32_t *free_blocks, const int32_t *n_free, int32_t *block_tables,
+                                int32_t *slot_map, int32_t *n_free_out, void *ws, size_t ws_bytes,
+                                relay_stream_t stream);
+
+/* The return of blocks: for every request with done[b] != 0, in request
+ * order, the ceil(ctx_lens[b] / 16) ids at the front of its block-table row
+ * are appended to the free list, and n_free_out[0] = n_free[0] plus their
+ * number (it may be n_free itself).  The tables are left as they are: the
+ * caller gives the row a length of 0 before the next plan.  A request whose
+ * blocks would take the list past num_blocks (a second return) is skipped,
+ * and so is every later one that has some (RELAY_FLAG_POOL); one with a
+ * length outside [0, 16*max_blocks_per_seq] is skipped and flagged; an id
+ * outside [0, num_blocks) is flagged and listed as -1.  ws as for
+ * relay_block_plan. */
+relay_status_t relay_block_release(const relay_dims_t *dims, const int32_t *done, const int32_t *ctx_lens,
+                                   const int32_t *block_tables, int32_t *free_blocks, const int32_t *n_free,
+                                   int32_t *n_free_out, void *ws, size_t ws_bytes, relay_stream_t stream);
+
+/* A paged context pool held in 4 bits: a token of a KV head is D codes in
+ * groups of `group` dimensions, each group with an fp16 pair (s, z); a code c
+ * stands for the value s * c + z.
+ *      k_codes, v_codes  [num_blocks, Hkv, 16, D/2]         uint8, dimension
+ *                        2j in the low and 2j + 1 in the high half of byte j
+ *      k_sz, v_sz        [num_blocks, Hkv, 16, D/group, 2]  fp16 (s, z)
+ * All 16-byte aligned; group 32, 64 or 128, at most D (other sizes return
+ * RELAY_ERR_UNSUPPORTED).  Blocks, block tables and lengths are those of the
+ * fp16 pool; the system cache stays fp16.  At group = 128 a token takes 136
+ * bytes per KV head where the fp16 pool takes 512.  The struct is a HOST
+ * struct, read during the call only. */
+typedef struct {
+    void *k_codes, *k_sz, *v_codes, *v_sz;
+    int32_t group;
+} relay_q4_cache_t;
+
+/* relay_kv_append into a 4-bit pool: each group of the new rows is stored as
+ *     z = min, s = fp16((max - min) / 15), c = rint((x - z) / s) in 0..15
+ * (divisions in fp32; ties to even; s = 0 stores c = 0), so a stored value is
+ * off by at most s / 2, and by the rounding of s at most 15 * s * 2^-11 more.
+ * A group that holds a NaN or an infinity is stored as s = z = NaN.  Rows and
+ * their places are those of relay_kv_append; with slot_map ([B, Lq], as
+ * relay_block_plan writes it) row (b, i), i < q_lens[b], goes to slot
+ * slot_map[b][i] instead, a negative slot is skipped, and block_tables and
+ * ctx_lens are not read and may be NULL.  Two rows of one call must not have
+ * one place. */
+relay_status_t relay_kv_append_q4(const relay_dims_t *dims, const void *k_new, const void *v_new,
+                                  const int32_t *block_tables, const int32_t *ctx_lens, const int32_t *q_lens,
+                                  const int32_t *slot_map, const relay_q4_cache_t *cache, void *ws, size_t ws_bytes,
+                                  relay_stream_t stream);
+
+/* Bytes of workspace relay_attention_decode_q4 and relay_ctx_attn_q4 need for
+ * `dims` (0 if invalid); sized for the current device, initialised and shared
+ * as the workspace of relay_attention_decode. */
+size_t relay_workspace_size_q4(const relay_dims_t *dims);
+
+/* relay_attention_decode and relay_ctx_attn with the contexts in a 4-bit
+ * pool.  Scores and sums are held in fp32 and the codes enter the products
+ * exactly; the softmax weights times the value scales are rounded to fp16
+ * (the fp16 path rounds the weights).  A key that a row does not see has no
+ * part in it even where its scales are NaN. */
+relay_status_t relay_attention_decode_q4(const relay_dims_t *dims, const void *q, const void *sys_k, const void *sys_v,
+                                         const relay_q4_cache_t *cache, const int32_t *block_tables,
+                                         const int32_t *ctx_lens, const int32_t *q_lens, void *out, float *lse_out,
+                                         void *ws, size_t ws_bytes, relay_stream_t stream);
+relay_status_t relay_ctx_attn_q4(const relay_dims_t *dims, const void *q, const relay_q4_cache_t *cache,
+                                 const int32_t *block_tables, const int32_t *ctx_lens, const int32_t *q_lens,
+                                 float *o_ctx, float *lse_ctx, void *ws, size_t ws_bytes, relay_stream_t stream);
 
 /* The non-relay formulation, as a paged-attention system with prefix sharing
  * runs it (atyun.com RelayAttention article, section "RelayAttention": the

@@ -18,6 +18,12 @@ Entry points (same names as the C ABI in include/relay.h):
     relay_kv_append(...)          the step's new K/V rows into the paged pool
     relay_sys_prefill(...)        causal self-attention of the system prompt (filling its cache)
     relay_rope(...)               rotary positions of the new rows, offset by the system prompt
+    relay_rope_axes(...)          the same with several position axes (time, height, width)
+    relay_block_plan(...)         block tables and slot maps from the request lengths, on the device
+    relay_block_release(...)      the blocks of finished requests back to the free list
+    relay_kv_append_q4(...)       the step's new K/V rows quantised into a 4-bit pool (Q4Cache)
+    relay_attention_decode_q4(...), relay_ctx_attn_q4(...)
+                                  the relay step, and its context step, over a 4-bit pool
     workspace_size(dims), make_workspace(dims), device_status(ws)
 """
 from __future__ import annotations
@@ -34,7 +40,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "librelay.so")
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_CHECK, ERR_TIMEOUT = range(7)
-FLAG_BAD_Q_LEN, FLAG_BAD_CTX_LEN, FLAG_BAD_BLOCK, FLAG_Q_TOTAL, FLAG_WAIT_TIMEOUT = 1, 2, 4, 8, 16
+FLAG_BAD_Q_LEN, FLAG_BAD_CTX_LEN, FLAG_BAD_BLOCK, FLAG_Q_TOTAL, FLAG_WAIT_TIMEOUT, FLAG_POOL = 1, 2, 4, 8, 16, 32
 
 
 class RelayError(RuntimeError):
@@ -52,6 +58,11 @@ class Dims(ctypes.Structure):
 
     def __repr__(self):
         return "Dims(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class Q4Struct(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_sz", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_sz", ctypes.c_void_p), ("group", ctypes.c_int32)]
 
 
 _lib = None
@@ -76,6 +87,18 @@ _SIGS = {
     "relay_workspace_size_prefixes": (ctypes.c_size_t, [ctypes.POINTER(Dims), ctypes.c_int, _VP]),
     "relay_attention_decode_prefixes": (ctypes.c_int, [ctypes.POINTER(Dims), _VP, ctypes.c_int, _VP, _VP, _VP, _VP]
                                         + [_VP] * 8 + [ctypes.c_size_t, _VP]),
+    "relay_rope_axes": (ctypes.c_int, [ctypes.POINTER(Dims)] + [_VP] * 3 + [ctypes.c_int, _VP, _VP, ctypes.c_float,
+                                                                         ctypes.c_int, _VP, _VP, _VP, ctypes.c_size_t,
+                                                                         _VP]),
+    "relay_block_plan": (ctypes.c_int, [ctypes.POINTER(Dims)] + [_VP] * 8 + [ctypes.c_size_t, _VP]),
+    "relay_block_release": (ctypes.c_int, [ctypes.POINTER(Dims)] + [_VP] * 7 + [ctypes.c_size_t, _VP]),
+    "relay_workspace_size_q4": (ctypes.c_size_t, [ctypes.POINTER(Dims)]),
+    "relay_kv_append_q4": (ctypes.c_int, [ctypes.POINTER(Dims)] + [_VP] * 6 + [ctypes.POINTER(Q4Struct), _VP,
+                                                                            ctypes.c_size_t, _VP]),
+    "relay_ctx_attn_q4": (ctypes.c_int, [ctypes.POINTER(Dims), _VP, ctypes.POINTER(Q4Struct)] + [_VP] * 6
+                          + [ctypes.c_size_t, _VP]),
+    "relay_attention_decode_q4": (ctypes.c_int, [ctypes.POINTER(Dims), _VP, _VP, _VP, ctypes.POINTER(Q4Struct)]
+                                  + [_VP] * 6 + [ctypes.c_size_t, _VP]),
 }
 
 
@@ -525,6 +548,304 @@ def relay_rope(q, ctx_lens, Ls, k_new=None, q_lens=None, base=10000.0, workspace
                           _ptr(workspace), workspace.numel(), _stream(stream))
     _check(rc, "relay_rope")
     return workspace
+
+
+# ----------------------------------------------------------------------------- steps around the cache
+def _current(dev):
+    """The library launches on the current device: tensors of another one are refused, not reached from here."""
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _on_stream(stream, make, *args, **kw):
+    """make(*args, **kw) with its memory, and a fill it queues, belonging to the stream of the call."""
+    if stream is None:
+        return make(*args, **kw)
+    with torch.cuda.stream(stream):
+        return make(*args, **kw)
+
+
+def _small_workspace(workspace, dev, stream):
+    if workspace is None:
+        workspace = _on_stream(stream, torch.zeros, 256, dtype=torch.uint8, device=dev)
+    return workspace
+
+
+MAX_ROPE_AXES = 4
+
+
+def rope_axis_map(sections, D, interleaved=False) -> bytes:
+    """The axis of each of the D / 2 pairs of relay_rope_axes.  sections: pairs per axis, together D / 2; in runs
+    (axis 0's pairs first), or interleaved: pair a + n k belongs to axis a (of n) for k < sections[a], a > 0, and
+    every other pair to axis 0."""
+    sections = [int(x) for x in sections]
+    half, n = D // 2, len(sections)
+    if not 1 <= n <= MAX_ROPE_AXES or min(sections) < 0 or sum(sections) != half:
+        raise ValueError(f"sections {sections} must be 1..{MAX_ROPE_AXES} counts that add up to {half}")
+    if not interleaved:
+        return b"".join(bytes([a]) * c for a, c in enumerate(sections))
+    axis = bytearray(half)
+    for a in range(1, n):
+        if sections[a] and a + n * (sections[a] - 1) >= half:
+            raise ValueError(f"axis {a} of interleaved sections {sections} runs past the {half} pairs")
+        for k in range(sections[a]):
+            axis[a + n * k] = a
+    return bytes(axis)
+
+
+def relay_rope_axes(q, positions, Ls, sections, k_new=None, q_lens=None, base=10000.0, interleaved=False, inverse=False,
+                    q_out=None, k_out=None, workspace=None, stream=None):
+    """Rotary embedding with one position per axis: q [B, Lq, H, D] (and k_new [B, Lq, Hkv, D]) at positions Ls +
+    positions[a][b][i] ([n_axes, B, Lq] int32) for the pairs that `sections` (rope_axis_map) gives to axis a;
+    `inverse` turns back.  In place, or into q_out / k_out.  Returns q_out, k_out."""
+    dev = q.device
+    B, Lq, H, D = q.shape
+    q_out = q if q_out is None else q_out
+    k_out = k_new if k_out is None else k_out
+    if k_new is None and k_out is not None:
+        raise ValueError("k_out without k_new")
+    Hkv = H
+    if k_new is not None:
+        Hkv = k_new.shape[2] if k_new.dim() == 4 else 0
+        _shape(k_new, "k_new", (B, Lq, Hkv, D))
+        _same(k_out, k_new, ("k_out", "k_new"))
+    _shape(positions, "positions", (len(sections), B, Lq))
+    _shape(q_lens, "q_lens", (B,))
+    _same(q_out, q, ("q_out", "q"))
+    axis = rope_axis_map(sections, D, interleaved)
+    _need(q, "q", torch.float16)
+    _current(dev)
+    _need(q_out, "q_out", torch.float16, dev)
+    _need(positions, "positions", torch.int32, dev)
+    _opt(k_new, "k_new", torch.float16, dev)
+    _opt(k_out, "k_out", torch.float16, dev)
+    _opt(q_lens, "q_lens", torch.int32, dev)
+    dims = Dims(B, Lq, H, D, int(Ls), 16, 0, 0, 0, 0, 0, 0.0, Hkv)
+    workspace = _small_workspace(workspace, dev, stream)
+    rc = lib().relay_rope_axes(ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(positions), len(sections), axis,
+                               _ptr(q_lens), float(base), int(inverse), _ptr(q_out), _ptr(k_out), _ptr(workspace),
+                               workspace.numel(), _stream(stream))
+    _check(rc, "relay_rope_axes")
+    return q_out, k_out
+
+
+def _free_list(free_blocks, n_free, n_free_out, dev):
+    if free_blocks.dim() != 1:
+        raise ValueError(f"free_blocks {tuple(free_blocks.shape)} must be [num_blocks]")
+    _shape(n_free, "n_free", (1,))
+    _shape(n_free_out, "n_free_out", (1,))
+    _need(free_blocks, "free_blocks", torch.int32, dev)
+    _need(n_free, "n_free", torch.int32, dev)
+    _need(n_free_out, "n_free_out", torch.int32, dev)
+
+
+def relay_block_plan(ctx_lens, block_tables, free_blocks, n_free, q_lens=None, Lq=1, slot_map=None, n_free_out=None,
+                     workspace=None, stream=None):
+    """Block tables (in place) and slot map ([B, Lq] int32, returned) of a step in which request b grows by q_lens[b]
+    (or Lq) tokens to ctx_lens[b], the new blocks taken from the end of free_blocks ([num_blocks], the first n_free[0]
+    in use).  n_free_out: where the new count goes (None: into n_free)."""
+    dev = ctx_lens.device
+    if ctx_lens.dim() != 1:
+        raise ValueError(f"ctx_lens {tuple(ctx_lens.shape)} must be [B]")
+    B = ctx_lens.shape[0]
+    n_free_out = n_free if n_free_out is None else n_free_out
+    _table_shapes(B, block_tables, ctx_lens, q_lens)
+    _shape(slot_map, "slot_map", (B, Lq))
+    _need(ctx_lens, "ctx_lens", torch.int32)
+    _current(dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _opt(q_lens, "q_lens", torch.int32, dev)
+    _free_list(free_blocks, n_free, n_free_out, dev)
+    if slot_map is None:
+        slot_map = _on_stream(stream, torch.empty, (B, Lq), dtype=torch.int32, device=dev)
+    _need(slot_map, "slot_map", torch.int32, dev)
+    dims = Dims(B, Lq, 1, 64, 0, 16, free_blocks.shape[0], block_tables.shape[1], 0, 0, 0, 0.0, 0)
+    workspace = _small_workspace(workspace, dev, stream)
+    rc = lib().relay_block_plan(ctypes.byref(dims), _ptr(ctx_lens), _ptr(q_lens), _ptr(free_blocks), _ptr(n_free),
+                                _ptr(block_tables), _ptr(slot_map), _ptr(n_free_out), _ptr(workspace),
+                                workspace.numel(), _stream(stream))
+    _check(rc, "relay_block_plan")
+    return slot_map
+
+
+def relay_block_release(done, ctx_lens, block_tables, free_blocks, n_free, n_free_out=None, workspace=None, stream=None):
+    """Append the blocks of the requests with done[b] != 0 ([B] int32) to free_blocks (in place); the new count goes
+    to n_free_out (None: into n_free).  Returns n_free_out."""
+    dev = done.device
+    if done.dim() != 1:
+        raise ValueError(f"done {tuple(done.shape)} must be [B]")
+    B = done.shape[0]
+    n_free_out = n_free if n_free_out is None else n_free_out
+    _table_shapes(B, block_tables, ctx_lens, None)
+    _need(done, "done", torch.int32)
+    _current(dev)
+    _need(ctx_lens, "ctx_lens", torch.int32, dev)
+    _need(block_tables, "block_tables", torch.int32, dev)
+    _free_list(free_blocks, n_free, n_free_out, dev)
+    dims = Dims(B, 1, 1, 64, 0, 16, free_blocks.shape[0], block_tables.shape[1], 0, 0, 0, 0.0, 0)
+    workspace = _small_workspace(workspace, dev, stream)
+    rc = lib().relay_block_release(ctypes.byref(dims), _ptr(done), _ptr(ctx_lens), _ptr(block_tables), _ptr(free_blocks),
+                                   _ptr(n_free), _ptr(n_free_out), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "relay_block_release")
+    return n_free_out
+
+
+# ----------------------------------------------------------------------------- 4-bit context pool
+class Q4Cache:
+    """A paged context pool held in 4 bits, over four tensors that it keeps: codes [num_blocks, Hkv, 16, D / 2] uint8
+    and (scale, zero) pairs [num_blocks, Hkv, 16, D / group, 2] fp16, of K and of V."""
+
+    def __init__(self, k_codes, k_sz, v_codes, v_sz):
+        _same(k_codes, v_codes, ("k_codes", "v_codes"))
+        _same(k_sz, v_sz, ("k_sz", "v_sz"))
+        if k_codes.dim() != 4 or k_codes.shape[2] != 16:
+            raise ValueError(f"k_codes {tuple(k_codes.shape)} must be [num_blocks, Hkv, 16, D / 2]")
+        self.num_blocks, self.Hkv, _, half = k_codes.shape
+        self.D = 2 * half
+        groups = k_sz.shape[3] if k_sz.dim() == 5 else 0
+        if groups < 1 or self.D % groups or                 tuple(k_sz.shape) != (self.num_blocks, self.Hkv, 16, groups, 2):
+            raise ValueError(f"k_sz {tuple(k_sz.shape)} must be [{self.num_blocks}, {self.Hkv}, 16, D / group, 2]")
+        self.group = self.D // groups
+        for name, t, dtype in (("k_codes", k_codes, torch.uint8), ("k_sz", k_sz, torch.float16),
+                               ("v_codes", v_codes, torch.uint8), ("v_sz", v_sz, torch.float16)):
+            _need(t, name, dtype, k_codes.device)
+        self.k_codes, self.k_sz, self.v_codes, self.v_sz = k_codes, k_sz, v_codes, v_sz
+        self.device = k_codes.device
+        self._struct = Q4Struct(k_codes.data_ptr(), k_sz.data_ptr(), v_codes.data_ptr(), v_sz.data_ptr(), self.group)
+
+
+def make_q4_cache(num_blocks, Hkv, D, group=128, device=None) -> Q4Cache:
+    """An empty (zero) 4-bit pool; group 32, 64 or 128, at most D."""
+    if group not in (32, 64, 128) or D % group:
+        raise ValueError(f"group {group} must be 32, 64 or 128 and divide D = {D}")
+    z = lambda *shape, dtype: torch.zeros(num_blocks, Hkv, 16, *shape, dtype=dtype, device=device or "cuda")
+    return Q4Cache(z(D // 2, dtype=torch.uint8), z(D // group, 2, dtype=torch.float16),
+                   z(D // 2, dtype=torch.uint8), z(D // group, 2, dtype=torch.float16))
+
+
+def workspace_size_q4(dims: Dims) -> int:
+    return int(lib().relay_workspace_size_q4(ctypes.byref(dims)))
+
+
+def make_workspace_q4(dims: Dims, device=None) -> torch.Tensor:
+    """Zero-filled workspace of relay_attention_decode_q4 / relay_ctx_attn_q4 for `dims`."""
+    n = workspace_size_q4(dims)
+    if n == 0:
+        raise ValueError(f"invalid dims {dims}")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def _check_cache(cache: Q4Cache, D, dev):
+    if cache.D != D:
+        raise ValueError(f"the 4-bit pool has D = {cache.D}, expected {D}")
+    if cache.device != dev:
+        raise ValueError(f"the 4-bit pool is on {cache.device}, expected {dev}")
+
+
+def relay_kv_append_q4(k_new, v_new, block_tables, ctx_lens, cache: Q4Cache, q_lens=None, slot_map=None, workspace=None,
+                       stream=None):
+    """Quantise the step's new K/V rows ([B, Lq, Hkv, D] fp16) into the 4-bit pool in place, at each request's last
+    q_lens[b] context positions, or at slot_map ([B, Lq] int32, from relay_block_plan; block_tables and ctx_lens may
+    then be None).  Device-side problems are flagged in `workspace` (device_status), which is returned."""
+    dev = k_new.device
+    B, Lq, Hkv, D = k_new.shape
+    _same(k_new, v_new, ("k_new", "v_new"))
+    if cache.Hkv != Hkv:
+        raise ValueError(f"k_new has {Hkv} KV heads, the 4-bit pool {cache.Hkv}")
+    max_blocks = 0
+    if slot_map is None:
+        _table_shapes(B, block_tables, ctx_lens, q_lens)
+        max_blocks = block_tables.shape[1]
+    _shape(q_lens, "q_lens", (B,))
+    _shape(slot_map, "slot_map", (B, Lq))
+    _need(k_new, "k_new", torch.float16)
+    _current(dev)
+    _need(v_new, "v_new", torch.float16, dev)
+    _check_cache(cache, D, dev)
+    if slot_map is None:
+        _need(block_tables, "block_tables", torch.int32, dev)
+        _need(ctx_lens, "ctx_lens", torch.int32, dev)
+    else:
+        block_tables = ctx_lens = None
+        _need(slot_map, "slot_map", torch.int32, dev)
+    _opt(q_lens, "q_lens", torch.int32, dev)
+    dims = Dims(B, Lq, Hkv, D, 0, 16, cache.num_blocks, max_blocks, 0, 0, 0, 0.0, Hkv)
+    workspace = _small_workspace(workspace, dev, stream)
+    rc = lib().relay_kv_append_q4(ctypes.byref(dims), _ptr(k_new), _ptr(v_new), _ptr(block_tables), _ptr(ctx_lens),
+                                  _ptr(q_lens), _ptr(slot_map), ctypes.byref(cache._struct), _ptr(workspace),
+                                  workspace.numel(), _stream(stream))
+    _check(rc, "relay_kv_append_q4")
+    return workspace
+
+
+def _q4_dims(q, Ls, cache, block_tables, ctx_lens, q_lens, dims, scale, max_q_total, ctx_split, sys_range):
+    """The checks and dims that the two calls over a 4-bit pool share."""
+    B, Lq, H, D = q.shape
+    _check_cache(cache, D, q.device)
+    if H % cache.Hkv:
+        raise ValueError(f"{H} query heads over the 4-bit pool's {cache.Hkv} KV heads")
+    _table_shapes(B, block_tables, ctx_lens, q_lens)
+    _need(q, "q", torch.float16)
+    _current(q.device)
+    _need(block_tables, "block_tables", torch.int32, q.device)
+    _need(ctx_lens, "ctx_lens", torch.int32, q.device)
+    _opt(q_lens, "q_lens", torch.int32, q.device)
+    if dims is None:
+        dims = make_dims(q, Ls, cache.num_blocks, block_tables.shape[1], scale, max_q_total, ctx_split, sys_range,
+                         cache.Hkv)
+    _check_dims(dims, q, Ls, cache.k_codes, block_tables)
+    _check_kv(dims, cache.k_codes, "the 4-bit pool")
+    return dims
+
+
+def relay_attention_decode_q4(q, sys_k, sys_v, cache: Q4Cache, block_tables, ctx_lens, q_lens=None, out=None,
+                              lse_out=None, workspace=None, scale=None, max_q_total=0, ctx_split=0, sys_range=0,
+                              stream=None, dims=None):
+    """relay_attention_decode with the contexts in a 4-bit pool.  Returns out [B, Lq, H, D] fp16."""
+    dev = q.device
+    B, Lq, H, D = q.shape
+    _same(sys_k, sys_v, ("sys_k", "sys_v"))
+    _shape(sys_k, "sys_k", (sys_k.shape[0], cache.Hkv, D))
+    _shape(out, "out", q.shape)
+    _shape(lse_out, "lse_out", (B, Lq, H))
+    dims = _q4_dims(q, sys_k.shape[0], cache, block_tables, ctx_lens, q_lens, dims, scale, max_q_total, ctx_split,
+                    sys_range)
+    _need(sys_k, "sys_k", torch.float16, dev)
+    _need(sys_v, "sys_v", torch.float16, dev)
+    if out is None:
+        out = _on_stream(stream, torch.empty_like, q)
+    _need(out, "out", torch.float16, dev)
+    _opt(lse_out, "lse_out", torch.float32, dev)
+    if workspace is None:
+        workspace = _on_stream(stream, make_workspace_q4, dims, dev)
+    rc = lib().relay_attention_decode_q4(ctypes.byref(dims), _ptr(q), _ptr(sys_k), _ptr(sys_v),
+                                         ctypes.byref(cache._struct), _ptr(block_tables), _ptr(ctx_lens), _ptr(q_lens),
+                                         _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.numel(), _stream(stream))
+    _check(rc, "relay_attention_decode_q4")
+    return out
+
+
+def relay_ctx_attn_q4(q, cache: Q4Cache, block_tables, ctx_lens, q_lens=None, o_ctx=None, lse_ctx=None, workspace=None,
+                      scale=None, max_q_total=0, ctx_split=0, stream=None, dims=None):
+    """relay_ctx_attn with the contexts in a 4-bit pool.  Returns o_ctx [B, Lq, H, D], lse_ctx [B, Lq, H] fp32."""
+    dev = q.device
+    B, Lq, H, D = q.shape
+    _shape(o_ctx, "o_ctx", q.shape)
+    _shape(lse_ctx, "lse_ctx", (B, Lq, H))
+    dims = _q4_dims(q, 0, cache, block_tables, ctx_lens, q_lens, dims, scale, max_q_total, ctx_split, 0)
+    if o_ctx is None:
+        o_ctx = _on_stream(stream, torch.empty, (B, Lq, H, D), dtype=torch.float32, device=dev)
+    if lse_ctx is None:
+        lse_ctx = _on_stream(stream, torch.empty, (B, Lq, H), dtype=torch.float32, device=dev)
+    _need(o_ctx, "o_ctx", torch.float32, dev)
+    _need(lse_ctx, "lse_ctx", torch.float32, dev)
+    if workspace is None:
+        workspace = _on_stream(stream, make_workspace_q4, dims, dev)
+    rc = lib().relay_ctx_attn_q4(ctypes.byref(dims), _ptr(q), ctypes.byref(cache._struct), _ptr(block_tables),
+                                 _ptr(ctx_lens), _ptr(q_lens), _ptr(o_ctx), _ptr(lse_ctx), _ptr(workspace),
+                                 workspace.numel(), _stream(stream))
+    _check(rc, "relay_ctx_attn_q4")
+    return o_ctx, lse_ctx
 
 
 def device_status(workspace: torch.Tensor, stream=None) -> int:

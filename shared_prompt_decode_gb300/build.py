@@ -12,8 +12,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "librelay.so")
 SOURCES = [os.path.join(CSRC, "relay.cu")]
-DEPS = SOURCES + [os.path.join(CSRC, "relay_kernels.cuh"), os.path.join(CSRC, "sys_tc.cuh"),
-                  os.path.join(INCLUDE, "relay.h")]
+DEPS = SOURCES + [os.path.join(CSRC, name) for name in ("relay_kernels.cuh", "sys_tc.cuh", "q4_kernels.cuh",
+                                                        "step_kernels.cuh")] + [os.path.join(INCLUDE, "relay.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
@@ -34,7 +34,7 @@ def build(force: bool = False, verbose: bool = False, variant: str = "", defines
         if all(os.path.getmtime(f) <= t for f in DEPS):
             return lib
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), ARCH, "-O3", "--split-compile=0", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-o", tmp] + [f"-D{d}" for d in defines] + SOURCES
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -14,7 +14,9 @@
 #include <mutex>
 
 #include "relay.h"
+#include "q4_kernels.cuh"
 #include "relay_kernels.cuh"
+#include "step_kernels.cuh"
 #include "sys_tc.cuh"
 
 namespace {
@@ -27,6 +29,7 @@ constexpr int kMaxMqParts = 8;         // context splits of a multi-row request,
 static_assert(RELAY_MAX_SEGMENTS == kMaxSegments, "segment limit of the header and the kernels");
 static_assert(tc::kPageTC == kBlock, "page size of the tensor-core context path");
 static_assert(tc::kMaxBatchTC == kMaxB, "batch limit of the tensor-core kernel");
+static_assert(RELAY_FLAG_POOL == FLAG_POOL, "flag of the header and the kernels");
 
 struct DevInfo {
     bool ready = false;
@@ -78,6 +81,35 @@ cudaError_t prepare_kernel(int *occ)
 }
 
 
+// The 4-bit streaming kernel of a shape, its shared memory, and the instances
+// for D, the group size and whether a request may bring more than 8 columns
+// (query rows times query heads of a KV head).
+using Q4Kernel = void (*)(const Params, const q4::Pool);
+Q4Kernel q4_kernel_for(int D, int group, bool wide)
+{
+    if (D == 128) {
+        if (group == 128) return wide ? q4::q4_kernel<128, 128, 2> : q4::q4_kernel<128, 128, 1>;
+        if (group == 64) return wide ? q4::q4_kernel<128, 64, 2> : q4::q4_kernel<128, 64, 1>;
+        return wide ? q4::q4_kernel<128, 32, 2> : q4::q4_kernel<128, 32, 1>;
+    }
+    if (group == 64) return wide ? q4::q4_kernel<64, 64, 2> : q4::q4_kernel<64, 64, 1>;
+    return wide ? q4::q4_kernel<64, 32, 2> : q4::q4_kernel<64, 32, 1>;
+}
+size_t q4_smem(int D) { return D == 128 ? sizeof(q4::SmemQ<128>) : sizeof(q4::SmemQ<64>); }
+
+cudaError_t prepare_q4()
+{
+    for (int D : {64, 128})
+        for (int group : {32, 64, 128})
+            for (bool wide : {false, true}) {
+                if (group > D) continue;
+                const cudaError_t e = cudaFuncSetAttribute(q4_kernel_for(D, group, wide),
+                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q4_smem(D));
+                if (e != cudaSuccess) return e;
+            }
+    return cudaSuccess;
+}
+
 relay_status_t device_info(const DevInfo **out)
 {
     int dev = 0;
@@ -89,7 +121,8 @@ relay_status_t device_info(const DevInfo **out)
     DevInfo &d = g_dev[dev];
     if (!d.ready) {
         if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-            prepare_kernel<64>(&d.occ64) != cudaSuccess || prepare_kernel<128>(&d.occ128) != cudaSuccess) {
+            prepare_kernel<64>(&d.occ64) != cudaSuccess || prepare_kernel<128>(&d.occ128) != cudaSuccess ||
+            prepare_q4() != cudaSuccess) {
             cudaGetLastError();
             return RELAY_ERR_CUDA;
         }
@@ -248,8 +281,9 @@ int round_up(int x, int m) { return (x + m - 1) / m * m; }
 // Work-item sizes and workspace layout for one mode, for a GPU of `sms` SMs
 // (one streaming CTA per SM; the number of system key ranges depends on it).
 // `seg`: several shared prefix segments (never on the tensor-core kernel);
-// null: the one system prompt of dims->Ls tokens.
-Plan make_plan(const relay_dims_t *d, int mode, int sms, const Segments *seg = nullptr)
+// null: the one system prompt of dims->Ls tokens.  `q4`: the contexts are in
+// a 4-bit pool.
+Plan make_plan(const relay_dims_t *d, int mode, int sms, const Segments *seg = nullptr, bool q4 = false)
 {
     Plan pl;
     pl.Mtot = d->max_q_total > 0 ? d->max_q_total : d->B * d->Lq;
@@ -336,12 +370,27 @@ Plan make_plan(const relay_dims_t *d, int mode, int sms, const Segments *seg = n
         pl.tps_min = d->ctx_split > 0 ? pl.tps_max
                                       : std::min(pl.tps_max, std::max(2, (max_pages + kMaxCtxParts - 1) / kMaxCtxParts));
         pl.c_dec = std::max(1, (max_pages + pl.tps_min - 1) / pl.tps_min);
+        int mq_parts = kMaxMqParts;
+        if (q4) {
+            // 4-bit pages are a quarter of the bytes, so items hold more of
+            // them (at least 8, where the context has them); a batch too
+            // small to give every warp an item that way is cut finer, into up
+            // to 256 parts a request
+            const long long warps = (long long)sms * kWarps;
+            const long long per_part = std::max<long long>(1, (long long)d->B * kv_heads(d));
+            const int parts = (int)std::max(64ll, std::min(256ll, 2 * warps / per_part));
+            pl.tps_max = d->ctx_split > 0 ? pl.ctx_split / kBlock : std::max(64, (max_pages + parts - 1) / parts);
+            pl.tps_min = d->ctx_split > 0 ? pl.tps_max : std::max(8, (max_pages + parts - 1) / parts);
+            pl.c_dec = std::max(1, (max_pages + pl.tps_min - 1) / pl.tps_min);
+            const long long tiles = ((long long)d->Lq * G + 15) / 16;
+            mq_parts = (int)std::max(8ll, std::min(64ll, 2 * warps / (per_part * tiles)));
+        }
         const long long max_keys = (long long)pl.n_prefix + (long long)d->max_blocks_per_seq * kBlock;
-        pl.mq_split_min = (int)((max_keys + kMaxMqParts - 1) / kMaxMqParts);
+        pl.mq_split_min = (int)((max_keys + mq_parts - 1) / mq_parts);
         // Requests of at least kTcCtxMinRows virtual rows per KV head take
         // their own context on the tensor cores, one split over all of it,
         // in the same grid as the system step (after its CTAs).
-        pl.ctx_tc = d->D == 128 && pl.n_prefix == 0 && d->Lq > 1 && (long long)d->Lq * G >= kTcCtxMinRows &&
+        pl.ctx_tc = !q4 && d->D == 128 && pl.n_prefix == 0 && d->Lq > 1 && (long long)d->Lq * G >= kTcCtxMinRows &&
                     d->num_blocks > 0 && d->max_blocks_per_seq > 0 && d->max_blocks_per_seq <= tc::kMaxPagesTC;
         if (pl.ctx_tc) {
             pl.mq_split_min = (int)max_keys;
@@ -430,8 +479,10 @@ relay_status_t make_segments(int n_seg, const void *const *k, const void *const 
     return RELAY_OK;
 }
 
+// `q4`: the contexts are in this 4-bit pool (groups of `group` dimensions).
 relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws, size_t ws_bytes,
-                            relay_stream_t stream, const Segments *seg = nullptr)
+                            relay_stream_t stream, const Segments *seg = nullptr, const q4::Pool *q4 = nullptr,
+                            int group = 0)
 {
     if (!ws) return RELAY_ERR_WORKSPACE;
     if (!aligned(ws, 256)) return RELAY_ERR_INVALID_ARG;
@@ -439,12 +490,13 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
     // q_lens every request has Lq rows, and the partial slots are laid out
     // for max_q_total rows) a bound below B * Lq; with q_lens the kernel
     // checks their sum on the device
-    if (ws_bytes < make_plan(d, mode, 1, seg).total) return RELAY_ERR_WORKSPACE;
-    if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1, seg).Mtot) return RELAY_ERR_INVALID_ARG;
+    const bool is_q4 = q4 != nullptr;
+    if (ws_bytes < make_plan(d, mode, 1, seg, is_q4).total) return RELAY_ERR_WORKSPACE;
+    if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1, seg, is_q4).Mtot) return RELAY_ERR_INVALID_ARG;
     const DevInfo *dev = nullptr;
     relay_status_t st = device_info(&dev);
     if (st != RELAY_OK) return st;
-    Plan pl = make_plan(d, mode, dev->sms, seg);
+    Plan pl = make_plan(d, mode, dev->sms, seg, is_q4);
     if (ws_bytes < pl.total) return RELAY_ERR_WORKSPACE;
 
     unsigned char *base = static_cast<unsigned char *>(ws);
@@ -546,7 +598,10 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
         unsigned grid = 0;
         size_t smem = 0;
         const bool grp = p.G > 1;
-        if (d->D == 128) {
+        if (q4) {
+            grid = dev->sms;
+            smem = q4_smem(d->D);
+        } else if (d->D == 128) {
             grid = dev->sms * dev->occ128;
             smem = sizeof(Smem<128>);
             switch (row_class(d, pl, mode, p.G, p.q_lens != nullptr)) {
@@ -575,7 +630,10 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
             cfg.attrs = attr;
             cfg.numAttrs = 1;
         }
-        if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
+        const cudaError_t e =
+            q4 ? cudaLaunchKernelEx(&cfg, q4_kernel_for(d->D, group, (long long)d->Lq * p.G > 8), p, *q4)
+               : cudaLaunchKernelEx(&cfg, fn, p);
+        if (e != cudaSuccess) {
             cudaGetLastError();
             return RELAY_ERR_CUDA;
         }
@@ -964,6 +1022,269 @@ relay_status_t relay_rope(const relay_dims_t *dims, void *q, void *k_new, const 
     a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
     const long long warps = (long long)a.B * a.Lq * (a.H + (k_new ? a.Hkv : 0));
     rope_kernel<<<(unsigned)((warps + 7) / 8), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
+}
+
+// ----------------------------------------------------------------------------- 4-bit context pool
+}  // extern "C"
+
+namespace {
+
+// A pool that holds something (num_blocks > 0) has all four arrays, 16-byte
+// aligned; the group divides D.
+relay_status_t check_q4(const relay_dims_t *d, const relay_q4_cache_t *c)
+{
+    if (!c) return RELAY_ERR_INVALID_ARG;
+    if (c->group != 32 && c->group != 64 && c->group != 128) return RELAY_ERR_UNSUPPORTED;
+    if (c->group > d->D) return RELAY_ERR_UNSUPPORTED;
+    if (d->num_blocks > 0 && (!c->k_codes || !c->v_codes || !c->k_sz || !c->v_sz)) return RELAY_ERR_INVALID_ARG;
+    if (!aligned(c->k_codes, 16) || !aligned(c->v_codes, 16) || !aligned(c->k_sz, 16) || !aligned(c->v_sz, 16))
+        return RELAY_ERR_INVALID_ARG;
+    return RELAY_OK;
+}
+
+q4::Pool q4_pool(const relay_q4_cache_t *c)
+{
+    return {static_cast<const unsigned char *>(c->k_codes), static_cast<const unsigned char *>(c->v_codes),
+            static_cast<const __half2 *>(c->k_sz), static_cast<const __half2 *>(c->v_sz)};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t relay_workspace_size_q4(const relay_dims_t *dims)
+{
+    if (check_dims(dims) != RELAY_OK) return 0;
+    const DevInfo *dev = nullptr;
+    const int sms = device_info(&dev) == RELAY_OK ? dev->sms : INT_MAX / 4;
+    return std::max(make_plan(dims, MODE_FUSED, sms, nullptr, true).total,
+                    make_plan(dims, MODE_CTX, sms, nullptr, true).total);
+}
+
+relay_status_t relay_kv_append_q4(const relay_dims_t *dims, const void *k_new, const void *v_new,
+                                  const int32_t *block_tables, const int32_t *ctx_lens, const int32_t *q_lens,
+                                  const int32_t *slot_map, const relay_q4_cache_t *cache, void *ws, size_t ws_bytes,
+                                  relay_stream_t stream)
+{
+    relay_status_t st = check_dims(dims);
+    if (st == RELAY_OK) st = check_q4(dims, cache);
+    if (st != RELAY_OK) return st;
+    if (!ws || ws_bytes < 256) return RELAY_ERR_WORKSPACE;
+    if (dims->B == 0) return RELAY_OK;
+    if (!k_new || !v_new || dims->num_blocks < 1) return RELAY_ERR_INVALID_ARG;
+    if (!slot_map && (!block_tables || !ctx_lens || dims->max_blocks_per_seq < 1)) return RELAY_ERR_INVALID_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(block_tables, 4) || !aligned(ctx_lens, 4) ||
+        !aligned(q_lens, 4) || !aligned(slot_map, 4) || !aligned(ws, 256))
+        return RELAY_ERR_INVALID_ARG;
+    if ((int64_t)dims->num_blocks * kBlock > INT_MAX) return RELAY_ERR_UNSUPPORTED;      // 32-bit slots
+    q4::Append a{};
+    a.B = dims->B;
+    a.Lq = dims->Lq;
+    a.Hkv = kv_heads(dims);
+    a.num_blocks = dims->num_blocks;
+    a.max_blocks = dims->max_blocks_per_seq;
+    a.k_new = static_cast<const __half *>(k_new);
+    a.v_new = static_cast<const __half *>(v_new);
+    a.block_tables = block_tables;
+    a.ctx_lens = ctx_lens;
+    a.q_lens = q_lens;
+    a.slot_map = slot_map;
+    a.k = static_cast<unsigned char *>(cache->k_codes);
+    a.v = static_cast<unsigned char *>(cache->v_codes);
+    a.ksz = static_cast<__half2 *>(cache->k_sz);
+    a.vsz = static_cast<__half2 *>(cache->v_sz);
+    a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
+    const long long threads = (long long)a.B * a.Lq * a.Hkv * 2 * (dims->D / 8), grid = (threads + 255) / 256;
+    if (grid > INT_MAX) return RELAY_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dims->D == 128) {
+        if (cache->group == 128) q4::append_kernel<128, 128><<<(unsigned)grid, 256, 0, s>>>(a);
+        else if (cache->group == 64) q4::append_kernel<128, 64><<<(unsigned)grid, 256, 0, s>>>(a);
+        else q4::append_kernel<128, 32><<<(unsigned)grid, 256, 0, s>>>(a);
+    } else {
+        if (cache->group == 64) q4::append_kernel<64, 64><<<(unsigned)grid, 256, 0, s>>>(a);
+        else q4::append_kernel<64, 32><<<(unsigned)grid, 256, 0, s>>>(a);
+    }
+    return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
+}
+
+relay_status_t relay_ctx_attn_q4(const relay_dims_t *dims, const void *q, const relay_q4_cache_t *cache,
+                                 const int32_t *block_tables, const int32_t *ctx_lens, const int32_t *q_lens,
+                                 float *o_ctx, float *lse_ctx, void *ws, size_t ws_bytes, relay_stream_t stream)
+{
+    relay_status_t st = check_dims(dims);
+    if (st == RELAY_OK) st = check_q4(dims, cache);
+    if (st != RELAY_OK) return st;
+    if (!q || !o_ctx || !lse_ctx || !ctx_lens || (dims->max_blocks_per_seq > 0 && !block_tables))
+        return RELAY_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o_ctx, 16) || !aligned(lse_ctx, 4) || !aligned(block_tables, 4) ||
+        !aligned(ctx_lens, 4) || !aligned(q_lens, 4))
+        return RELAY_ERR_INVALID_ARG;
+    if (dims->B == 0) return RELAY_OK;
+    Params p = blank_params();
+    p.q = static_cast<const __half *>(q);
+    p.block_tables = block_tables;
+    p.ctx_lens = ctx_lens;
+    p.q_lens = q_lens;
+    p.o_f32 = o_ctx;
+    p.lse_f32 = lse_ctx;
+    const q4::Pool pool = q4_pool(cache);
+    return launch_relay(dims, MODE_CTX, p, ws, ws_bytes, stream, nullptr, &pool, cache->group);
+}
+
+relay_status_t relay_attention_decode_q4(const relay_dims_t *dims, const void *q, const void *sys_k, const void *sys_v,
+                                         const relay_q4_cache_t *cache, const int32_t *block_tables,
+                                         const int32_t *ctx_lens, const int32_t *q_lens, void *out, float *lse_out,
+                                         void *ws, size_t ws_bytes, relay_stream_t stream)
+{
+    relay_status_t st = check_dims(dims);
+    if (st == RELAY_OK) st = check_q4(dims, cache);
+    if (st != RELAY_OK) return st;
+    if (!q || !out || !ctx_lens || (dims->Ls > 0 && (!sys_k || !sys_v)) ||
+        (dims->max_blocks_per_seq > 0 && !block_tables))
+        return RELAY_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(sys_k, 16) || !aligned(sys_v, 16) || !aligned(out, 16) || !aligned(lse_out, 4) ||
+        !aligned(block_tables, 4) || !aligned(ctx_lens, 4) || !aligned(q_lens, 4))
+        return RELAY_ERR_INVALID_ARG;
+    if (dims->B == 0) return RELAY_OK;
+    Params p = blank_params();
+    p.q = static_cast<const __half *>(q);
+    p.sys_k = static_cast<const __half *>(sys_k);
+    p.sys_v = static_cast<const __half *>(sys_v);
+    p.block_tables = block_tables;
+    p.ctx_lens = ctx_lens;
+    p.q_lens = q_lens;
+    p.out = static_cast<__half *>(out);
+    p.lse_out = lse_out;
+    const q4::Pool pool = q4_pool(cache);
+    return launch_relay(dims, MODE_FUSED, p, ws, ws_bytes, stream, nullptr, &pool, cache->group);
+}
+
+// ----------------------------------------------------------------------------- steps around the cache
+relay_status_t relay_block_plan(const relay_dims_t *dims, const int32_t *ctx_lens, const int32_t *q_lens,
+                                const int32_t *free_blocks, const int32_t *n_free, int32_t *block_tables,
+                                int32_t *slot_map, int32_t *n_free_out, void *ws, size_t ws_bytes,
+                                relay_stream_t stream)
+{
+    relay_status_t st = check_dims(dims);
+    if (st != RELAY_OK) return st;
+    if (!ws || ws_bytes < 256) return RELAY_ERR_WORKSPACE;
+    if ((int64_t)dims->num_blocks * kBlock > INT_MAX) return RELAY_ERR_UNSUPPORTED;      // 32-bit slots
+    if (dims->B == 0) return RELAY_OK;
+    if (!ctx_lens || !n_free || !n_free_out || (dims->num_blocks > 0 && !free_blocks) ||
+        (dims->max_blocks_per_seq > 0 && !block_tables))
+        return RELAY_ERR_INVALID_ARG;
+    if (!aligned(ctx_lens, 4) || !aligned(q_lens, 4) || !aligned(free_blocks, 4) || !aligned(n_free, 4) ||
+        !aligned(block_tables, 4) || !aligned(slot_map, 4) || !aligned(n_free_out, 4) || !aligned(ws, 256))
+        return RELAY_ERR_INVALID_ARG;
+    const DevInfo *dev = nullptr;
+    st = device_info(&dev);
+    if (st != RELAY_OK) return st;
+    BlockPlan a{};
+    a.B = dims->B;
+    a.Lq = dims->Lq;
+    a.max_blocks = dims->max_blocks_per_seq;
+    a.num_blocks = dims->num_blocks;
+    a.ctx_lens = ctx_lens;
+    a.q_lens = q_lens;
+    a.free_blocks = free_blocks;
+    a.n_free = n_free;
+    a.block_tables = block_tables;
+    a.slot_map = slot_map;
+    a.n_free_out = n_free_out;
+    a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
+    a.ticket = static_cast<unsigned *>(ws) + CTRL_STEP_TICKET;
+    const long long slots = (long long)a.B * a.Lq;
+    const int grid = (int)std::min<long long>((slots + kStepThreads - 1) / kStepThreads, 2 * dev->sms);
+    block_plan_kernel<<<grid, kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
+}
+
+relay_status_t relay_block_release(const relay_dims_t *dims, const int32_t *done, const int32_t *ctx_lens,
+                                   const int32_t *block_tables, int32_t *free_blocks, const int32_t *n_free,
+                                   int32_t *n_free_out, void *ws, size_t ws_bytes, relay_stream_t stream)
+{
+    relay_status_t st = check_dims(dims);
+    if (st != RELAY_OK) return st;
+    if (!ws || ws_bytes < 256) return RELAY_ERR_WORKSPACE;
+    if (dims->B == 0) return RELAY_OK;
+    if (!done || !ctx_lens || !n_free || !n_free_out || (dims->num_blocks > 0 && !free_blocks) ||
+        (dims->max_blocks_per_seq > 0 && !block_tables))
+        return RELAY_ERR_INVALID_ARG;
+    if (!aligned(done, 4) || !aligned(ctx_lens, 4) || !aligned(block_tables, 4) || !aligned(free_blocks, 4) ||
+        !aligned(n_free, 4) || !aligned(n_free_out, 4) || !aligned(ws, 256))
+        return RELAY_ERR_INVALID_ARG;
+    const DevInfo *dev = nullptr;
+    st = device_info(&dev);
+    if (st != RELAY_OK) return st;
+    BlockRelease a{};
+    a.B = dims->B;
+    a.max_blocks = dims->max_blocks_per_seq;
+    a.num_blocks = dims->num_blocks;
+    a.done = done;
+    a.ctx_lens = ctx_lens;
+    a.block_tables = block_tables;
+    a.n_free = n_free;
+    a.free_blocks = free_blocks;
+    a.n_free_out = n_free_out;
+    a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
+    a.ticket = static_cast<unsigned *>(ws) + CTRL_STEP_TICKET;
+    const long long units = (long long)a.B * ((a.max_blocks + kReleaseChunk - 1) / kReleaseChunk);
+    const int grid = (int)std::max<long long>(
+        1, std::min<long long>((units + kStepThreads / 32 - 1) / (kStepThreads / 32), 2 * dev->sms));
+    block_release_kernel<<<grid, kStepThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+    return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
+}
+
+relay_status_t relay_rope_axes(const relay_dims_t *dims, const void *q, const void *k_new, const int32_t *positions,
+                               int n_axes, const uint8_t *pair_axis, const int32_t *q_lens, float base, int inverse,
+                               void *q_out, void *k_out, void *ws, size_t ws_bytes, relay_stream_t stream)
+{
+    relay_status_t st = check_dims(dims);
+    if (st != RELAY_OK) return st;
+    if (!ws || ws_bytes < 256) return RELAY_ERR_WORKSPACE;
+    if (!(base > 1.f) || !(base < 1e30f) || n_axes < 1 || n_axes > RELAY_MAX_ROPE_AXES || !pair_axis)
+        return RELAY_ERR_INVALID_ARG;
+    const int half = dims->D / 2;
+    static_assert(kMaxRopePairs == 64, "pairs of D = 128");
+    for (int j = 0; j < half; j++)
+        if (pair_axis[j] >= n_axes) return RELAY_ERR_INVALID_ARG;
+    if (dims->B == 0) return RELAY_OK;
+    if (!q || !q_out || !positions || !k_new != !k_out) return RELAY_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(positions, 4) ||
+        !aligned(q_lens, 4) || !aligned(ws, 256))
+        return RELAY_ERR_INVALID_ARG;
+    const DevInfo *dev = nullptr;
+    st = device_info(&dev);
+    if (st != RELAY_OK) return st;
+    RopeAxes a{};
+    a.B = dims->B;
+    a.Lq = dims->Lq;
+    a.H = dims->H;
+    a.Hkv = k_new ? kv_heads(dims) : 0;
+    a.Ls = dims->Ls;
+    for (int j = 0; j < half; j++) {
+        // below a sixth of a turn per position, so the fraction fits 64 bits
+        const double turns = std::pow((double)base, -2.0 * j / dims->D) / 6.283185307179586476925286766559;
+        a.turn[j] = (unsigned long long)std::ldexp(turns, 64);
+        a.axis[j] = pair_axis[j];
+    }
+    a.q = static_cast<const __half *>(q);
+    a.k = static_cast<const __half *>(k_new);
+    a.q_out = static_cast<__half *>(q_out);
+    a.k_out = static_cast<__half *>(k_out);
+    a.pos = positions;
+    a.q_lens = q_lens;
+    a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
+    a.inverse = inverse != 0;
+    const int nh = a.H + a.Hkv, pass = 32 / (dims->D / 16);
+    a.hpw = pass;
+    const long long warps = (long long)a.B * a.Lq * ((nh + a.hpw - 1) / a.hpw), grid = (warps + 7) / 8;
+    if (grid > INT_MAX) return RELAY_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (dims->D == 128) rope_axes_kernel<128><<<(unsigned)grid, 256, 0, s>>>(a);
+    else rope_axes_kernel<64><<<(unsigned)grid, 256, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
 }
 
