@@ -25,6 +25,7 @@
 #include <stdint.h>
 
 #include "relay_kernels.cuh"
+#include "step_kernels.cuh"
 
 namespace relay {
 namespace q4 {
@@ -37,10 +38,19 @@ struct Pool {
 // ----------------------------------------------------------------------------- append
 // s = fp16((max - min) / 15), z = min, code = rint((x - z) / s) clamped to
 // 0..15, in fp32 with IEEE divisions; s = 0 has code 0, and a group with a NaN
-// or an infinity stores s = z = NaN.  D / 8 lanes take one row of one KV head,
-// K or V, eight elements each.
+// or an infinity stores s = z = NaN.  D / 32 lanes take one row of one KV
+// head, K or V: with the instructions of a row's address, group and scale
+// spread over 32 elements the kernel is [APPEND].
+//
+// The quotient's code comes from a product with 1 / s: t = (x - z) * (1 / s)
+// is off by less than 1e-5 (15 times a few roundings of 2^-24), so unless t
+// is that near to a half its nearest whole number c is the quotient's too.
+// Exact halves are common (x - z and s are short fractions): there x - z - c
+// s is s / 2 to the bit, and c goes to the even side.  Only what is near a
+// half without being one is divided.
 struct Append {
     int B, Lq, Hkv, num_blocks, max_blocks;
+    unsigned magic;                   // (2^32 - 1) / Lq
     const __half *k_new, *v_new;      // [B, Lq, Hkv, D]
     const int *block_tables, *ctx_lens, *q_lens;
     const int *slot_map;              // [B, Lq] or null: the slots from the block tables
@@ -48,98 +58,139 @@ struct Append {
     __half2 *ksz, *vsz;
     unsigned *flags;
 };
+constexpr int kAppendDims = 32;       // elements of a lane: 64 bytes in, 16 bytes of codes out
+
+// Codes of eight elements.  r: 1 / s; clamp: a code may come out above 15.
+__device__ __forceinline__ unsigned codes_of(uint4 x, float lo, float s, float r, bool clamp)
+{
+    constexpr float kMagic = 12582912.f;      // 1.5 * 2^23: t + kMagic has rint(t) in its low bits
+    const unsigned xs[4] = {x.x, x.y, x.z, x.w};
+    float2 t[4], m[4];
+    float far = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&xs[e]));
+        t[e] = mul2(add2(f, make_float2(-lo, -lo)), make_float2(r, r));
+        m[e] = add2(t[e], make_float2(kMagic, kMagic));
+        const float2 d = fma2(add2(m[e], make_float2(-kMagic, -kMagic)), make_float2(-1.f, -1.f), t[e]);
+        far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+    }
+    if (far > 0.49999f) {
+        const float half = 0.5f * s;
+        auto settle = [&](float d, float t1, float &m1) {
+            const float c1 = m1 - kMagic, rest = fmaf(-c1, s, d);
+            if (fabsf(rest) == half) {
+                if (__float_as_uint(m1) & 1u) m1 += copysignf(1.f, rest);
+            } else if (fabsf(t1 - c1) > 0.49999f) {
+                m1 = __fdiv_rn(d, s) + kMagic;
+            }
+        };
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&xs[e]));
+            settle(f.x - lo, t[e].x, m[e].x);
+            settle(f.y - lo, t[e].y, m[e].y);
+        }
+    }
+    if (clamp) {
+#pragma unroll
+        for (int e = 0; e < 4; e++) m[e] = make_float2(fminf(m[e].x, kMagic + 15.f), fminf(m[e].y, kMagic + 15.f));
+    }
+    // the codes are the low bits of eight equal words plus 0..15: shifted
+    // together, less what the eight words come to (x - z >= 0: none below 0)
+    unsigned word = 0;
+#pragma unroll
+    for (int e = 3; e >= 0; e--) word = (((word << 4) + __float_as_uint(m[e].y)) << 4) + __float_as_uint(m[e].x);
+    return word - 0x4b400000u * 0x11111111u;
+}
 
 template <int D, int GROUP>
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ Append a)
 {
-    constexpr int kLanes = D / 8, kGroupLanes = GROUP / 8;
-    const long long t = (long long)blockIdx.x * 256 + threadIdx.x;
-    const int c = (int)(t % kLanes);
-    const long long unit = t / kLanes;
-    const bool is_v = unit & 1;
-    const long long rh = unit >> 1, bi = rh / a.Hkv;
-    const int hk = (int)(rh - bi * a.Hkv);
-    const int b = (int)(bi / a.Lq), i = (int)(bi - (long long)b * a.Lq);
-    // all lanes of a row take the same way out of here, and rows do not
-    // straddle warps: the shuffles below name the row's own lanes
-    if (b >= a.B) return;
-    const bool first = hk == 0 && c == 0 && !is_v;      // the row's one reporter
-    int slot;
+    constexpr int kLanes = D / kAppendDims, kGroupLanes = GROUP / kAppendDims, kRows = 256 / kLanes;
+    const int b = blockIdx.y, c = threadIdx.x % kLanes;
+    const unsigned unit = blockIdx.x * kRows + threadIdx.x / kLanes;
+    // rows do not straddle warps and all lanes of one take the same way: the
+    // shuffles below name the row's own lanes
+    const unsigned lanes = ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
+    const int ql = a.q_lens ? a.q_lens[b] : a.Lq;
+    const bool first = blockIdx.x == 0 && threadIdx.x == 0;
+    if (ql < 0 || ql > a.Lq) {
+        if (first) atomicOr(a.flags, FLAG_BAD_Q_LEN);
+        return;
+    }
+    // consecutive rows of one head are neighbours, as they are in their page.
+    // unit / Lq: the product with the rounded-down reciprocal is the quotient
+    // or one less
+    int hv = (int)__umulhi(unit, a.magic), i = (int)unit - hv * a.Lq;
+    if (i >= a.Lq) {
+        hv++;
+        i -= a.Lq;
+    }
+    if (hv >= 2 * a.Hkv || i >= ql) return;
+    const bool is_v = hv & 1;
+    const int hk = hv >> 1;
+    const size_t row = (size_t)b * a.Lq + i;
+    const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) + (row * a.Hkv + hk) * D) + 4 * c;
+    uint4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; k++) x[k] = __ldg(src + k);
+    int blk, at;
     if (a.slot_map) {
-        if (a.q_lens) {
-            const int ql = a.q_lens[b];
-            if (ql < 0 || ql > a.Lq) {
-                if (first && i == 0) atomicOr(a.flags, FLAG_BAD_Q_LEN);
-                return;
-            }
-            if (i >= ql) return;
-        }
-        slot = a.slot_map[bi];
+        const int slot = a.slot_map[row];
         if (slot < 0) return;
-        if (slot / kBlock >= a.num_blocks) {
-            if (first) atomicOr(a.flags, FLAG_BAD_BLOCK);
-            return;
-        }
+        blk = slot / kBlock;
+        at = slot % kBlock;
     } else {
-        const int ql = a.q_lens ? a.q_lens[b] : a.Lq, n = a.ctx_lens[b];
-        if (ql < 0 || ql > a.Lq) {
-            if (first && i == 0) atomicOr(a.flags, FLAG_BAD_Q_LEN);
-            return;
-        }
-        if (i >= ql) return;
+        const int n = a.ctx_lens[b];
         if (n < ql || n > (long long)a.max_blocks * kBlock) {
-            if (first && i == 0) atomicOr(a.flags, FLAG_BAD_CTX_LEN);
+            if (first) atomicOr(a.flags, FLAG_BAD_CTX_LEN);
             return;
         }
         const int pos = n - ql + i;
-        const int blk = a.block_tables[(size_t)b * a.max_blocks + pos / kBlock];
-        if (blk < 0 || blk >= a.num_blocks) {
-            if (first) atomicOr(a.flags, FLAG_BAD_BLOCK);
-            return;
+        blk = a.block_tables[(size_t)b * a.max_blocks + pos / kBlock];
+        at = pos % kBlock;
+    }
+    if (blk < 0 || blk >= a.num_blocks) {
+        if (hv == 0 && c == 0) atomicOr(a.flags, FLAG_BAD_BLOCK);
+        return;
+    }
+    // (lowest, minus the highest) of the group: two minima in one, which a NaN
+    // goes through
+    __half2 mn = *reinterpret_cast<const __half2 *>(&x[0].x), mx = mn;
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const unsigned xs[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const __half2 h = *reinterpret_cast<const __half2 *>(&xs[e]);
+            mn = __hmin2_nan(mn, h);
+            mx = __hmax2_nan(mx, h);
         }
-        slot = blk * kBlock + pos % kBlock;
     }
-    const uint4 x = __ldg(reinterpret_cast<const uint4 *>((is_v ? a.v_new : a.k_new) + (size_t)rh * D) + c);
-    const unsigned xs[4] = {x.x, x.y, x.z, x.w};
-    float f[8];
-    bool finite = true;
+    mx = __hneg2(mx);
+    __half2 lh = __hmin2_nan(__lows2half2(mn, mx), __highs2half2(mn, mx));
 #pragma unroll
-    for (int e = 0; e < 4; e++) {
-        const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&xs[e]));
-        f[2 * e] = p.x;
-        f[2 * e + 1] = p.y;
-        finite = finite && (xs[e] & 0x7c00u) != 0x7c00u && (xs[e] & 0x7c000000u) != 0x7c000000u;
-    }
-    float lo = f[0], hi = f[0];
-#pragma unroll
-    for (int e = 1; e < 8; e++) {
-        lo = fminf(lo, f[e]);
-        hi = fmaxf(hi, f[e]);
-    }
-    if (!finite) hi = __int_as_float(0x7f800000);
-    const unsigned mask = kLanes == 32 ? 0xffffffffu
-                                       : ((1u << kLanes) - 1u) << ((threadIdx.x & 31) / kLanes * kLanes);
-#pragma unroll
-    for (int off = 1; off < kGroupLanes; off <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(mask, lo, off));
-        hi = fmaxf(hi, __shfl_xor_sync(mask, hi, off));
-    }
-    __half s16 = __float2half_rn(__fdiv_rn(hi - lo, 15.f)), z16 = __float2half_rn(lo);
+    for (int off = 1; off < kGroupLanes; off <<= 1) lh = __hmin2_nan(lh, __shfl_xor_sync(lanes, lh, off));
+    const float lo = __low2float(lh), range = -__high2float(lh) - lo;
+    __half s16 = __float2half_rn(__fdiv_rn(range, 15.f)), z16 = __low2half(lh);
     const float s = __half2float(s16);
-    unsigned word = 0;
-    if (hi == __int_as_float(0x7f800000)) {
+    uint4 codes = make_uint4(0u, 0u, 0u, 0u);
+    if (!(range < __int_as_float(0x7f800000))) {      // a NaN, or an infinity
         s16 = z16 = __ushort_as_half(0x7fff);
     } else if (s > 0.f) {
-#pragma unroll
-        for (int e = 0; e < 8; e++) {
-            const float code = fminf(rintf(__fdiv_rn(f[e] - lo, s)), 15.f);      // f[e] >= lo: not below 0
-            word |= (unsigned)(int)code << (4 * e);
-        }
+        float r;
+        asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(s));
+        // a scale that was rounded down by a large part of itself (a subnormal one)
+        const bool clamp = range * r > 15.4f;
+        codes.x = codes_of(x[0], lo, s, r, clamp);
+        codes.y = codes_of(x[1], lo, s, r, clamp);
+        codes.z = codes_of(x[2], lo, s, r, clamp);
+        codes.w = codes_of(x[3], lo, s, r, clamp);
     }
-    const size_t row = ((size_t)(slot / kBlock) * a.Hkv + hk) * kBlock + slot % kBlock;
-    *reinterpret_cast<unsigned *>((is_v ? a.v : a.k) + row * (D / 2) + 4 * c) = word;
-    if (c % kGroupLanes == 0)
-        (is_v ? a.vsz : a.ksz)[row * (D / GROUP) + c / kGroupLanes] = __halves2half2(s16, z16);
+    const size_t to = ((size_t)blk * a.Hkv + hk) * kBlock + at;
+    *reinterpret_cast<uint4 *>((is_v ? a.v : a.k) + to * (D / 2) + 16 * c) = codes;
+    if (c % kGroupLanes == 0) (is_v ? a.vsz : a.ksz)[to * (D / GROUP) + c / kGroupLanes] = __halves2half2(s16, z16);
 }
 
 // ----------------------------------------------------------------------------- attention: layout of a staged page

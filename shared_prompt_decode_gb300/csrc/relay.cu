@@ -29,6 +29,7 @@ constexpr int kMaxMqParts = 8;         // context splits of a multi-row request,
 static_assert(RELAY_MAX_SEGMENTS == kMaxSegments, "segment limit of the header and the kernels");
 static_assert(tc::kPageTC == kBlock, "page size of the tensor-core context path");
 static_assert(tc::kMaxBatchTC == kMaxB, "batch limit of the tensor-core kernel");
+constexpr int kRopeWarpsPerSm = 32;    // warps that relay_rope_axes spreads a batch of tokens over, per SM
 static_assert(RELAY_FLAG_POOL == FLAG_POOL, "flag of the header and the kernels");
 
 struct DevInfo {
@@ -1095,17 +1096,17 @@ relay_status_t relay_kv_append_q4(const relay_dims_t *dims, const void *k_new, c
     a.ksz = static_cast<__half2 *>(cache->k_sz);
     a.vsz = static_cast<__half2 *>(cache->v_sz);
     a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
-    const long long threads = (long long)a.B * a.Lq * a.Hkv * 2 * (dims->D / 8), grid = (threads + 255) / 256;
-    if (grid > INT_MAX) return RELAY_ERR_UNSUPPORTED;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dims->D == 128) {
-        if (cache->group == 128) q4::append_kernel<128, 128><<<(unsigned)grid, 256, 0, s>>>(a);
-        else if (cache->group == 64) q4::append_kernel<128, 64><<<(unsigned)grid, 256, 0, s>>>(a);
-        else q4::append_kernel<128, 32><<<(unsigned)grid, 256, 0, s>>>(a);
-    } else {
-        if (cache->group == 64) q4::append_kernel<64, 64><<<(unsigned)grid, 256, 0, s>>>(a);
-        else q4::append_kernel<64, 32><<<(unsigned)grid, 256, 0, s>>>(a);
-    }
+    a.magic = 0xffffffffu / (unsigned)a.Lq;
+    const long long threads = 2ll * a.Lq * a.Hkv * (dims->D / q4::kAppendDims);
+    if (threads > INT_MAX) return RELAY_ERR_UNSUPPORTED;
+    const long long grid = (threads + 255) / 256;
+    void (*fn)(const q4::Append);
+    if (dims->D == 128)
+        fn = cache->group == 128 ? q4::append_kernel<128, 128>
+                                 : cache->group == 64 ? q4::append_kernel<128, 64> : q4::append_kernel<128, 32>;
+    else
+        fn = cache->group == 64 ? q4::append_kernel<64, 64> : q4::append_kernel<64, 32>;
+    fn<<<dim3((unsigned)grid, (unsigned)a.B), 256, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
     return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
 }
 
@@ -1278,13 +1279,16 @@ relay_status_t relay_rope_axes(const relay_dims_t *dims, const void *q, const vo
     a.q_lens = q_lens;
     a.flags = static_cast<unsigned *>(ws) + CTRL_FLAGS;
     a.inverse = inverse != 0;
-    const int nh = a.H + a.Hkv, pass = 32 / (dims->D / 16);
-    a.hpw = pass;
-    const long long warps = (long long)a.B * a.Lq * ((nh + a.hpw - 1) / a.hpw), grid = (warps + 7) / 8;
-    if (grid > INT_MAX) return RELAY_ERR_UNSUPPORTED;
+    // all heads of a token on one warp where the tokens fill the GPU; with
+    // fewer tokens the heads are dealt out, a pass of a warp at least
+    const int nh = a.H + a.Hkv, pass = 32 / (dims->D / 16), tokens = a.B * a.Lq, passes = (nh + pass - 1) / pass;
+    const int parts = std::max(1, std::min(passes, kRopeWarpsPerSm * dev->sms / tokens));
+    a.hpw = (passes + parts - 1) / parts * pass;
+    const dim3 grid((tokens + kRopeWarps - 1) / kRopeWarps, (nh + a.hpw - 1) / a.hpw);
+    if (grid.y > 65535) return RELAY_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (dims->D == 128) rope_axes_kernel<128><<<(unsigned)grid, 256, 0, s>>>(a);
-    else rope_axes_kernel<64><<<(unsigned)grid, 256, 0, s>>>(a);
+    if (dims->D == 128) rope_axes_kernel<128><<<grid, kRopeWarps * 32, 0, s>>>(a);
+    else rope_axes_kernel<64><<<grid, kRopeWarps * 32, 0, s>>>(a);
     return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
 }
 

@@ -184,9 +184,10 @@ __global__ void __launch_bounds__(kStepThreads) block_release_kernel(const __gri
 // integers, so the wrap-around drops whole turns exactly).  A warp takes one
 // token and `hpw` of its heads: it forms the D / 2 sines and cosines once,
 // passes them through shared memory, and a lane then holds the eight pairs
-// that it turns in every head (D / 16 lanes a head, two 16-byte loads each).
+// that it turns in every head (D / 16 lanes a head, two 16-byte loads each,
+// kUnroll heads in flight).
 struct RopeAxes {
-    int B, Lq, H, Hkv, Ls, hpw;       // Hkv = 0 without k
+    int B, Lq, H, Hkv, Ls, hpw;       // Hkv = 0 without k; hpw: heads of a warp
     unsigned long long turn[kMaxRopePairs];
     unsigned char axis[kMaxRopePairs];
     const __half *q, *k;
@@ -196,19 +197,41 @@ struct RopeAxes {
     int inverse;
 };
 
+constexpr int kRopeWarps = 4;
+
+// two products and sums at a time (32-bit each, IEEE)
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    unsigned long long r, x = *reinterpret_cast<unsigned long long *>(&a), y = *reinterpret_cast<unsigned long long *>(&b),
+                          z = *reinterpret_cast<unsigned long long *>(&c);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    return *reinterpret_cast<float2 *>(&r);
+}
+
 template <int D>
-__global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ RopeAxes a)
+__global__ void __launch_bounds__(kRopeWarps * 32) rope_axes_kernel(const __grid_constant__ RopeAxes a)
 {
     constexpr int kLanes = D / 16, kHeads = 32 / kLanes;      // lanes of a head, heads of a warp's pass
-    __shared__ float2 cs[8][D / 2];
+    constexpr int kUnroll = 3;
+    __shared__ float2 cs[kRopeWarps][D / 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int nh = a.H + a.Hkv, parts = (nh + a.hpw - 1) / a.hpw;
-    const long long w = (long long)blockIdx.x * 8 + warp, tokens = (long long)a.B * a.Lq;
-    if (w >= tokens * parts) return;
-    const long long tok = w / parts;
-    const int h0 = (int)(w % parts) * a.hpw, h1 = min(h0 + a.hpw, nh);
-    const int b = (int)(tok / a.Lq), i = (int)(tok % a.Lq);
+    const int tokens = a.B * a.Lq, tok = blockIdx.x * kRopeWarps + warp;
+    if (tok >= tokens) return;
+    const int nh = a.H + a.Hkv, h0 = blockIdx.y * a.hpw, h1 = min(h0 + a.hpw, nh);
     if (a.q_lens) {
+        const int b = tok / a.Lq, i = tok - b * a.Lq;
         const int ql = a.q_lens[b];
         if (ql < 0 || ql > a.Lq) {
             if (lane == 0 && i == 0 && h0 == 0) atomicOr(a.flags, FLAG_BAD_Q_LEN);
@@ -218,7 +241,7 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
     }
 #pragma unroll
     for (int j = lane; j < D / 2; j += 32) {
-        const long long pos = (long long)a.Ls + a.pos[a.axis[j] * tokens + tok];
+        const long long pos = (long long)a.Ls + a.pos[(size_t)a.axis[j] * tokens + tok];
         const unsigned long long f = (unsigned long long)pos * a.turn[j];
         float s, c;
         sincospif((float)(int)(f >> 32) * 0x1p-31f, &s, &c);      // half turns in [-1, 1)
@@ -226,27 +249,45 @@ __global__ void __launch_bounds__(256) rope_axes_kernel(const __grid_constant__ 
     }
     __syncwarp();
     const int c = lane % kLanes;
-    float2 t[8];
+    float2 co[4], si[4], ni[4];      // cosines, sines and negative sines of the lane's pairs, two by two
 #pragma unroll
-    for (int e = 0; e < 8; e++) t[e] = cs[warp][8 * c + e];
-    for (int h = h0 + lane / kLanes; h < h1; h += kHeads) {
-        const bool isq = h < a.H;
-        const size_t off = (isq ? (size_t)tok * a.H + h : (size_t)tok * a.Hkv + (h - a.H)) * D + 8 * c;
-        const __half *src = (isq ? a.q : a.k) + off;
-        __half *dst = (isq ? a.q_out : a.k_out) + off;
-        const uint4 x = *reinterpret_cast<const uint4 *>(src), y = *reinterpret_cast<const uint4 *>(src + D / 2);
-        const unsigned xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-        unsigned xo[4], yo[4];
+    for (int e = 0; e < 4; e++) {
+        const float2 t0 = cs[warp][8 * c + 2 * e], t1 = cs[warp][8 * c + 2 * e + 1];
+        co[e] = make_float2(t0.x, t1.x);
+        si[e] = make_float2(t0.y, t1.y);
+        ni[e] = make_float2(-t0.y, -t1.y);
+    }
+    for (int hb = h0 + lane / kLanes; hb < h1; hb += kUnroll * kHeads) {
+        uint4 x[kUnroll], y[kUnroll];
+        size_t off[kUnroll];
 #pragma unroll
-        for (int e = 0; e < 4; e++) {
-            const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&xs[e]));
-            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&ys[e]));
-            const float2 p = t[2 * e], r = t[2 * e + 1];
-            xo[e] = pack_half2(u.x * p.x - v.x * p.y, u.y * r.x - v.y * r.y);
-            yo[e] = pack_half2(v.x * p.x + u.x * p.y, v.y * r.x + u.y * r.y);
+        for (int u = 0; u < kUnroll; u++) {
+            const int h = hb + u * kHeads;
+            if (h >= h1) continue;
+            const bool isq = h < a.H;
+            off[u] = (isq ? (size_t)tok * a.H + h : (size_t)tok * a.Hkv + (h - a.H)) * D + 8 * c;
+            const __half *src = (isq ? a.q : a.k) + off[u];
+            x[u] = *reinterpret_cast<const uint4 *>(src);
+            y[u] = *reinterpret_cast<const uint4 *>(src + D / 2);
         }
-        *reinterpret_cast<uint4 *>(dst) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
-        *reinterpret_cast<uint4 *>(dst + D / 2) = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+#pragma unroll
+        for (int u = 0; u < kUnroll; u++) {
+            const int h = hb + u * kHeads;
+            if (h >= h1) continue;
+            __half *dst = (h < a.H ? a.q_out : a.k_out) + off[u];
+            const unsigned xs[4] = {x[u].x, x[u].y, x[u].z, x[u].w}, ys[4] = {y[u].x, y[u].y, y[u].z, y[u].w};
+            unsigned xo[4], yo[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const float2 p = __half22float2(*reinterpret_cast<const __half2 *>(&xs[e]));
+                const float2 r = __half22float2(*reinterpret_cast<const __half2 *>(&ys[e]));
+                const float2 px = fma2(p, co[e], mul2(r, ni[e])), py = fma2(r, co[e], mul2(p, si[e]));
+                xo[e] = pack_half2(px.x, px.y);
+                yo[e] = pack_half2(py.x, py.y);
+            }
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(xo[0], xo[1], xo[2], xo[3]);
+            *reinterpret_cast<uint4 *>(dst + D / 2) = make_uint4(yo[0], yo[1], yo[2], yo[3]);
+        }
     }
 }
 
