@@ -204,9 +204,7 @@ struct PageQ {
     static constexpr int kCodes = kBlock * kRow;
     static constexpr int NG = D / GROUP;             // groups of a row
     static constexpr int kSz = kBlock * NG * 4;      // bytes of the (s, z) pairs of K or V
-    static constexpr int kStage = 2 * kCodes + 2 * kSz;
-    static constexpr int kRing = kRingBytes / kWarps;
-    static constexpr int kStages = kRing / kStage < 8 ? kRing / kStage : 8;
+    static constexpr int kPage = 2 * kCodes + 2 * kSz;
 };
 
 template <int D>
@@ -219,27 +217,189 @@ __device__ __forceinline__ int chunk_off(int row, int ch)
 template <int D>
 __device__ __forceinline__ int byte_off(int row, int byte) { return chunk_off<D>(row, byte >> 4) + (byte & 15); }
 
-// ----------------------------------------------------------------------------- attention: items
-// A warp's item: the keys of one KV head in a range of one request's pages
-// against up to 8 * NT columns.  Column v is query row v / G with head
-// hk * G + v % G (one row: the heads of the group).
-template <int D, int NT>
-struct Item {
-    int b, hk, v0, nv;      // first column and columns of the item
-    int ql, row0;           // query rows of the request; its first compact row
-    int split, p0, np;      // partial index; first page and pages
-    int n_ctx;
-    unsigned qb[NT][D / 16][2];
+// Shape of a CTA: warps, pages of a step (their keys share one round of the
+// softmax), steps in a warp's ring.  One CTA per SM.
+template <int D, int GROUP, int NT>
+struct Geo {
+    static constexpr int kPer = 2;
+    static constexpr int kW = NT > 1 ? 8 : D == 128 && GROUP == 32 ? 12 : 16;
+    static constexpr int kStep = kPer * PageQ<D, GROUP>::kPage;
+    static constexpr int kFit = 218 * 1024 / (kW * kStep);
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static_assert(kStages >= 3, "ring");
 };
 
-// Row state: O^T in units of (code * 2^-24 or 2^-20) * 2^e, softmax statistics
-// of the lane's columns 8 nt + 2t, + 1.
-template <int D, int GROUP, int NT>
+// ----------------------------------------------------------------------------- attention: work
+// The context work as one line of pages: for every request, KV head and tile
+// of columns (a sequence) the pages of the context, one after the other.  The
+// line is cut into chunks of Q pages, a chunk is one warp's work, and a
+// sequence inside a chunk leaves one partial result.  Chunk c and sequence s
+// have partial c + s: along the line either number grows at every cut, so no
+// two partials meet, and those of one sequence are neighbours.
+struct Args {
+    Params p;
+    Pool pool;
+    int nc;                   // columns kept per partial
+    int q_min;                // pages of a chunk, at least
+    long long part0;          // first partial row of the contexts
+};
+
+// Handed from the context kernel to the merge kernel.
+struct Sched {
+    int bad, Q;
+    long long *pre;           // [B + 1] pages of the line before request b
+    int *qo, *seq, *nctx;     // [B + 1] query rows and sequences before it, [B] tokens
+};
+__host__ __device__ inline size_t sched_bytes(int B) { return 16 + 8 * (size_t)(B + 1) + 4 * (size_t)(3 * B + 2); }
+__device__ __forceinline__ Sched sched_at(int *base, int B)
+{
+    Sched s;
+    s.pre = reinterpret_cast<long long *>(base + 4);
+    s.qo = reinterpret_cast<int *>(s.pre + B + 1);
+    s.seq = s.qo + B + 1;
+    s.nctx = s.seq + B + 1;
+    return s;
+}
+
+// Columns of a request: query row i and head c of the group are column i G +
+// c, in tiles of 8 * nt (two tensor-core tiles where one does not hold them).
+struct Cols {
+    int cols, nt, tiles;
+};
+__host__ __device__ inline Cols cols_of(int ql, int G)
+{
+    Cols c;
+    c.cols = ql * G;
+    c.nt = c.cols > 8 ? 2 : 1;
+    c.tiles = (c.cols + 8 * c.nt - 1) / (8 * c.nt);
+    return c;
+}
+
+struct Smem4 {
+    long long pre[kMaxB + 1];
+    long long warp_pre[16];
+    int qo[kMaxB + 1], seq[kMaxB + 1], nctx[kMaxB];
+    int warp_qo[16], warp_seq[16];
+    int bad;
+    alignas(128) unsigned char ring[16];      // (the launch gives it its size)
+};
+
+// One sequence at position f of the line.
+struct Seq {
+    int b, hk, tile, id;      // id: over the whole batch
+    int page, pages;          // page at f, pages of the sequence
+    int n, ql;
+    Cols c;
+};
+__device__ __forceinline__ Seq locate(const Params &p, const Smem4 &s, long long f)
+{
+    Seq q;
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s.pre[mid] <= f) lo = mid; else hi = mid - 1;
+    }
+    q.b = lo;
+    q.n = s.nctx[lo];
+    q.ql = s.qo[lo + 1] - s.qo[lo];
+    q.c = cols_of(q.ql, p.G);
+    q.pages = (q.n + kBlock - 1) / kBlock;
+    const unsigned rem = (unsigned)(f - s.pre[lo]);      // the host keeps a request below 2^31 pages
+    const int at = (int)(rem / (unsigned)q.pages);
+    q.page = (int)rem - at * q.pages;
+    q.hk = at / q.c.tiles;
+    q.tile = at - q.hk * q.c.tiles;
+    q.id = s.seq[lo] + at;
+    return q;
+}
+// Keys that row i of a request sees.
+__device__ __forceinline__ int keys_seen(int n, int ql, int i) { return max(0, min(n, n - ql + 1 + i)); }
+// Pages that any column of the sequence sees.
+__device__ __forceinline__ int pages_seen(const Params &p, const Seq &q)
+{
+    const int last = min(q.c.cols, (q.tile + 1) * 8 * q.c.nt) - 1;
+    return (keys_seen(q.n, q.ql, last / p.G) + kBlock - 1) / kBlock;
+}
+
+// The line of the batch, built by the whole CTA (W warps).
+template <int W>
+__device__ void build_line(const Params &p, Smem4 &s)
+{
+    constexpr int PER = (kMaxB + 32 * W - 1) / (32 * W);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int ql[PER], n[PER], sq[PER], sum_q = 0, sum_s = 0;
+    long long pg[PER], sum_p = 0;
+    unsigned flags = 0;
+    if (tid == 0) s.bad = 0;
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int b = tid * PER + k;
+        ql[k] = n[k] = 0;
+        if (b < p.B) {
+            ql[k] = p.q_lens ? p.q_lens[b] : p.Lq;
+            n[k] = p.ctx_lens[b];
+            if (ql[k] < 0 || ql[k] > p.Lq) { flags |= FLAG_BAD_Q_LEN; ql[k] = 0; }
+            if (n[k] < 0 || n[k] > p.max_blocks * kBlock) { flags |= FLAG_BAD_CTX_LEN; ql[k] = n[k] = 0; }
+        }
+        sq[k] = p.Hkv * cols_of(ql[k], p.G).tiles;
+        pg[k] = (long long)sq[k] * ((n[k] + kBlock - 1) / kBlock);
+        sum_q += ql[k];
+        sum_s += sq[k];
+        sum_p += pg[k];
+    }
+    int iq = sum_q, is = sum_s;
+    long long ip = sum_p;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int tq = __shfl_up_sync(0xffffffffu, iq, off), ts = __shfl_up_sync(0xffffffffu, is, off);
+        const long long tp = __shfl_up_sync(0xffffffffu, ip, off);
+        if (lane >= off) { iq += tq; is += ts; ip += tp; }
+    }
+    if (lane == 31) {
+        s.warp_qo[warp] = iq;
+        s.warp_seq[warp] = is;
+        s.warp_pre[warp] = ip;
+    }
+    __syncthreads();
+    if (flags) atomicOr(&s.bad, (int)flags);
+    int bq = iq - sum_q, bs = is - sum_s;
+    long long bp = ip - sum_p;
+    for (int j = 0; j < warp; j++) {
+        bq += s.warp_qo[j];
+        bs += s.warp_seq[j];
+        bp += s.warp_pre[j];
+    }
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int b = tid * PER + k;
+        if (b < p.B) {
+            s.qo[b] = bq;
+            s.seq[b] = bs;
+            s.pre[b] = bp;
+            s.nctx[b] = n[k];
+        }
+        bq += ql[k];
+        bs += sq[k];
+        bp += pg[k];
+    }
+    if (tid == 32 * W - 1) {
+        s.qo[p.B] = bq;
+        s.seq[p.B] = bs;
+        s.pre[p.B] = bp;
+    }
+    __syncthreads();
+}
+
+// ----------------------------------------------------------------------------- attention: one step
+// Softmax state of a warp's columns, E of them in a lane (8 nt + 2t, + 1; a
+// batch of single columns has E = 1: column 0, in the lanes of t = 0).  O^T in
+// units of (code * 2^-24 or 2^-20) * 2^-down.
+template <int D, int GROUP, int NT, int E>
 struct State {
     float o[NT][D / 16][4];
     float c[NT][D / GROUP][4];      // the same for a code of 8 in every dimension
-    float z[NT][D / GROUP][2];      // sum of p (z + 8 s) over the lane's keys
-    float m[NT][2], l[NT][2];
+    float z[NT][D / GROUP][E];      // sum of p (z + 8 s) over the lane's keys
+    float m[NT][E], l[NT][E];
     int e;                          // scale_exp of the largest V scale so far
 };
 
@@ -252,33 +412,33 @@ __device__ __forceinline__ int scale_exp(__half2 sz) { return ((__half_as_ushort
 __device__ __forceinline__ float scale_down(int e) { return __int_as_float((15 - e + 127) << 23); }
 
 template <int D, int GROUP, int NT>
-__device__ __forceinline__ void load_q(const Params &p, Item<D, NT> &it)
+__device__ __forceinline__ void load_q(const Params &p, const Seq &s, unsigned (&qb)[NT][D / 16][2])
 {
     constexpr int WPG = GROUP / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
-        const int v = it.v0 + 8 * nt + g;
-        const bool has = 8 * nt + g < it.nv;
-        const int i = has ? v / p.G : 0, c = has ? v % p.G : 0;
-        const __half *q = p.q + (((size_t)it.b * p.Lq + i) * p.H + it.hk * p.G + c) * D;
+        const int v = s.tile * 8 * NT + 8 * nt + g;
+        const bool has = v < s.c.cols;
+        const int i = has ? v / p.G : 0, c = has ? v - i * p.G : 0;
+        const __half *q = p.q + (((size_t)s.b * p.Lq + i) * p.H + s.hk * p.G + c) * D;
 #pragma unroll
         for (int w = 0; w < D / 32; w++) {
             // dimensions of word w of the lane: the K words are read the same way
             const int d0 = (w / WPG) * GROUP + t * (GROUP / 4) + 8 * (w % WPG);
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
             if (has) x = *reinterpret_cast<const uint4 *>(q + d0);
-            it.qb[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);          // dimensions 0, 4
-            it.qb[nt][2 * w][1] = __byte_perm(x.y, x.w, 0x5410);          // 2, 6
-            it.qb[nt][2 * w + 1][0] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
-            it.qb[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);      // 3, 7
+            qb[nt][2 * w][0] = __byte_perm(x.x, x.z, 0x5410);          // dimensions 0, 4
+            qb[nt][2 * w][1] = __byte_perm(x.y, x.w, 0x5410);          // 2, 6
+            qb[nt][2 * w + 1][0] = __byte_perm(x.x, x.z, 0x7632);      // 1, 5
+            qb[nt][2 * w + 1][1] = __byte_perm(x.y, x.w, 0x7632);      // 3, 7
         }
     }
 }
 
-// Sums of q over each group, for the lane's two columns of every tile.
-template <int D, int GROUP, int NT>
-__device__ __forceinline__ void q_sums(const Item<D, NT> &it, float (&qs)[NT][D / GROUP][2])
+// Sums of q over each group, for the lane's columns of every tile.
+template <int D, int GROUP, int NT, int E>
+__device__ __forceinline__ void q_sums(const unsigned (&qb)[NT][D / 16][2], float (&qs)[NT][D / GROUP][E])
 {
     constexpr int WPG = GROUP / 32;
     const int t = threadIdx.x & 3;
@@ -291,13 +451,13 @@ __device__ __forceinline__ void q_sums(const Item<D, NT> &it, float (&qs)[NT][D 
             for (int w = gi * 2 * WPG; w < (gi + 1) * 2 * WPG; w++)
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&it.qb[nt][w][r]));
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qb[nt][w][r]));
                     x += f.x + f.y;
                 }
             x += __shfl_xor_sync(0xffffffffu, x, 1);
             x += __shfl_xor_sync(0xffffffffu, x, 2);
-            qs[nt][gi][0] = __shfl_sync(0xffffffffu, x, 8 * t);
-            qs[nt][gi][1] = __shfl_sync(0xffffffffu, x, 8 * t + 4);
+#pragma unroll
+            for (int e = 0; e < E; e++) qs[nt][gi][e] = __shfl_sync(0xffffffffu, x, 8 * t + 4 * e);
         }
 }
 
@@ -336,23 +496,19 @@ __device__ __forceinline__ void load_page(const Params &p, const Pool &pool, uns
     }
 }
 
-// One warp, one page.  end[nt][e]: keys of this page that column e sees.
-template <int D, int GROUP, int NT, bool MASK>
-__device__ __forceinline__ void page_step(const unsigned char *st, const Item<D, NT> &it, const float (&qs)[NT][D / GROUP][2],
-                                          State<D, GROUP, NT> &s, const int (&end)[NT][2], float scale_log2)
+// S^T = K q of one staged page, a group at a time: keys g, g + 8.
+template <int D, int GROUP, int NT, int E>
+__device__ __forceinline__ void page_scores(const unsigned char *st, const unsigned (&qb)[NT][D / 16][2],
+                                            const float (&qs)[NT][D / GROUP][E], float (&sc)[NT][2 * E])
 {
     using P = PageQ<D, GROUP>;
     constexpr int NG = P::NG, WPG = GROUP / 32;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const float2 zero2 = make_float2(0.f, 0.f);
-
-    // S^T = K q, a group at a time
-    float sc[NT][4];
+    const __half2 *ksz = reinterpret_cast<const __half2 *>(st + 2 * P::kCodes);
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int e = 0; e < 4; e++) sc[nt][e] = 0.f;
-    const __half2 *ksz = reinterpret_cast<const __half2 *>(st + 2 * P::kCodes);
+        for (int e = 0; e < 2 * E; e++) sc[nt][e] = 0.f;
 #pragma unroll
     for (int gi = 0; gi < NG; gi++) {
         unsigned w0[WPG], w1[WPG];
@@ -384,120 +540,40 @@ __device__ __forceinline__ void page_step(const unsigned char *st, const Item<D,
             const int w = 2 * (gi * WPG + j);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                mma16816(lo[nt], a0, it.qb[nt][w][0], it.qb[nt][w][1]);
-                mma16816(hi[nt], a1, it.qb[nt][w + 1][0], it.qb[nt][w + 1][1]);
+                mma16816(lo[nt], a0, qb[nt][w][0], qb[nt][w][1]);
+                mma16816(hi[nt], a1, qb[nt][w + 1][0], qb[nt][w + 1][1]);
             }
         }
         const float2 k0 = __half22float2(ksz[g * NG + gi]), k1 = __half22float2(ksz[(g + 8) * NG + gi]);
+        const float f0 = k0.x * 0x1p20f, f1 = k1.x * 0x1p20f;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int e = 0; e < 4; e++) {
-                const float2 k = e < 2 ? k0 : k1;
-                sc[nt][e] += k.x * (lo[nt][e] * 0x1p24f + hi[nt][e] * 0x1p20f) + k.y * qs[nt][gi][e & 1];
+            for (int e = 0; e < E; e++) {
+                sc[nt][e] += f0 * fmaf(lo[nt][e], 16.f, hi[nt][e]) + k0.y * qs[nt][gi][e];
+                sc[nt][E + e] += f1 * fmaf(lo[nt][2 + e], 16.f, hi[nt][2 + e]) + k1.y * qs[nt][gi][e];
             }
     }
-    // online softmax per column (keys over the lanes' g)
-    bool moved = false;
-    float mu[NT][2], mn[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int e = 0; e < 2; e++) {
-            float x0 = sc[nt][e] * scale_log2, x1 = sc[nt][2 + e] * scale_log2;
-            if (MASK) {
-                x0 = g < end[nt][e] ? x0 : kNegInf;
-                x1 = g + 8 < end[nt][e] ? x1 : kNegInf;
-            }
-            sc[nt][e] = x0;
-            sc[nt][2 + e] = x1;
-            float mx = fmaxf(x0, x1);
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            mn[nt][e] = fmaxf(s.m[nt][e], mx);
-            mu[nt][e] = mn[nt][e] == kNegInf ? 0.f : mn[nt][e];
-            moved = moved || mn[nt][e] != s.m[nt][e];
-        }
-    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 2; e++) {
-                const float al = ex2(s.m[nt][e] - mu[nt][e]);
-                s.m[nt][e] = mn[nt][e];
-                s.l[nt][e] *= al;
-#pragma unroll
-                for (int gi = 0; gi < NG; gi++) {
-                    s.z[nt][gi][e] *= al;
-                    s.c[nt][gi][e] *= al;
-                    s.c[nt][gi][2 + e] *= al;
-                }
-#pragma unroll
-                for (int d = 0; d < D / 16; d++) {
-                    s.o[nt][d][e] *= al;
-                    s.o[nt][d][2 + e] *= al;
-                }
-            }
-    }
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            sc[nt][e] = ex2(sc[nt][e] - mu[nt][e & 1]);
-            s.l[nt][e & 1] += sc[nt][e];
-        }
-    // the V scales' common power of two: p s / 2^e fills fp16 from the top
-    const __half2 *vsz = ksz + kBlock * NG;
-    float2 v0[NG], v1[NG];
-    int em = 0;
-#pragma unroll
-    for (int gi = 0; gi < NG; gi++) {
-        const __half2 h0 = vsz[g * NG + gi], h1 = vsz[(g + 8) * NG + gi];
-        em = max(em, max(scale_exp(h0), scale_exp(h1)));
-        v0[gi] = __half22float2(h0);
-        v1[gi] = __half22float2(h1);
-    }
-    em = max(s.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)em));
-    if (em != s.e) {      // warp-uniform
-        const float al = __int_as_float((s.e - em + 127) << 23);
-        s.e = em;
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-#pragma unroll
-                for (int d = 0; d < D / 16; d++) s.o[nt][d][e] *= al;
-#pragma unroll
-                for (int gi = 0; gi < NG; gi++) s.c[nt][gi][e] *= al;
-            }
-    }
-    const float down = scale_down(em);
-    unsigned pb[NT][NG][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int gi = 0; gi < NG; gi++) {
-            float w[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) {
-                float2 v = e < 2 ? v0[gi] : v1[gi];
-                // a NaN behind the mask must not meet its zero weight
-                if (MASK) v = g + (e < 2 ? 0 : 8) < end[nt][e & 1] ? v : zero2;
-                w[e] = sc[nt][e] * (v.x * down);
-                s.z[nt][gi][e & 1] += sc[nt][e] * fmaf(8.f, v.x, v.y);
-            }
-            pb[nt][gi][0] = movmatrix_t(pack_half2(w[0], w[1]));
-            pb[nt][gi][1] = movmatrix_t(pack_half2(w[2], w[3]));
-            constexpr unsigned kEight = 0x00080008u;
-            const unsigned a[4] = {kEight, kEight, kEight, kEight};
-            mma16816(s.c[nt][gi], a, pb[nt][gi][0], pb[nt][gi][1]);
-        }
-    // O^T += V^T P.  A lane's operand rows are dimensions, its columns keys 2t,
-    // 2t + 1, 2t + 8, 2t + 9: two keys' words are interleaved by halves, and
-    // a tile is one code position of the words.  Rows of a tile share their
-    // group, so with GROUP = 32 (four words) the two halves of the rows take
-    // the same word at positions 8 bits apart.
+}
+
+// O^T += V^T P of one staged page.  A lane's operand rows are dimensions, its
+// columns keys 2t, 2t + 1, 2t + 8, 2t + 9: two keys' words are interleaved by
+// halves, and a tile is one code position of the words.  Rows of a tile share
+// their group, so with GROUP = 32 (four words) the two halves of the rows take
+// the same word at positions 8 bits apart.
+template <int D, int GROUP, int NT>
+__device__ __forceinline__ void page_values(const unsigned char *st, const unsigned (&pb)[NT][D / GROUP][2],
+                                            float (&o)[NT][D / 16][4], float (&c8)[NT][D / GROUP][4])
+{
+    using P = PageQ<D, GROUP>;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const unsigned char *vc = st + P::kCodes;
+    constexpr unsigned kEight = 0x00080008u;
+    const unsigned eights[4] = {kEight, kEight, kEight, kEight};
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int gi = 0; gi < P::NG; gi++) mma16816(c8[nt][gi], eights, pb[nt][gi][0], pb[nt][gi][1]);
     constexpr int kHalf = GROUP == 32 ? 32 : 64;      // dimensions of a set of tiles
 #pragma unroll
     for (int h = 0; h < D / kHalf; h++) {
@@ -516,8 +592,8 @@ __device__ __forceinline__ void page_step(const unsigned char *st, const Item<D,
             const unsigned a1[4] = {x0 & kHiCodes, y0 & kHiCodes, x1 & kHiCodes, y1 & kHiCodes};
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                mma16816(s.o[nt][2 * h], a0, pb[nt][gi][0], pb[nt][gi][1]);
-                mma16816(s.o[nt][2 * h + 1], a1, pb[nt][gi][0], pb[nt][gi][1]);
+                mma16816(o[nt][2 * h], a0, pb[nt][gi][0], pb[nt][gi][1]);
+                mma16816(o[nt][2 * h + 1], a1, pb[nt][gi][0], pb[nt][gi][1]);
             }
         } else {
 #pragma unroll
@@ -528,25 +604,146 @@ __device__ __forceinline__ void page_step(const unsigned char *st, const Item<D,
                 const unsigned a1[4] = {x & kHiCodes, xs & kHiCodes, y & kHiCodes, ys & kHiCodes};
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++) {
-                    mma16816(s.o[nt][4 * h + 2 * r], a0, pb[nt][gi][0], pb[nt][gi][1]);
-                    mma16816(s.o[nt][4 * h + 2 * r + 1], a1, pb[nt][gi][0], pb[nt][gi][1]);
+                    mma16816(o[nt][4 * h + 2 * r], a0, pb[nt][gi][0], pb[nt][gi][1]);
+                    mma16816(o[nt][4 * h + 2 * r + 1], a1, pb[nt][gi][0], pb[nt][gi][1]);
                 }
             }
         }
     }
 }
 
-// Writes the item's partials: normalised output and log2-sum-exp per column.
-template <int D, int GROUP, int NT>
-__device__ __forceinline__ void write_item(const Params &p, const Item<D, NT> &it, State<D, GROUP, NT> &s)
+// One warp, `np` staged pages of one sequence.  end[nt][e]: keys of the step
+// that the lane's column sees (MASK: not all of them by every column).
+template <int D, int GROUP, int NT, int E, int KP, bool MASK>
+__device__ __forceinline__ void step(const unsigned char *st, int np, const unsigned (&qb)[NT][D / 16][2],
+                                     const float (&qs)[NT][D / GROUP][E], State<D, GROUP, NT, E> &s,
+                                     const int (&end)[NT][E], float scale_log2)
+{
+    using P = PageQ<D, GROUP>;
+    constexpr int NG = P::NG;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    const float2 zero2 = make_float2(0.f, 0.f);
+
+    float sc[KP][NT][2 * E];
+#pragma unroll
+    for (int j = 0; j < KP; j++) {
+        if (j == 0 || j < np) {
+            page_scores<D, GROUP, NT, E>(st + j * P::kPage, qb, qs, sc[j]);
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 2 * E; e++) sc[j][nt][e] = kNegInf;
+        }
+    }
+    // online softmax per column (keys over the lanes' g)
+    bool moved = false;
+    float mu[NT][E], mn[NT][E];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < E; e++) {
+            float mx = kNegInf;
+#pragma unroll
+            for (int j = 0; j < KP; j++) {
+                float x0 = sc[j][nt][e] * scale_log2, x1 = sc[j][nt][E + e] * scale_log2;
+                if (MASK) {
+                    x0 = 16 * j + g < end[nt][e] ? x0 : kNegInf;
+                    x1 = 16 * j + g + 8 < end[nt][e] ? x1 : kNegInf;
+                }
+                sc[j][nt][e] = x0;
+                sc[j][nt][E + e] = x1;
+                mx = fmaxf(mx, fmaxf(x0, x1));
+            }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            mn[nt][e] = fmaxf(s.m[nt][e], mx);
+            mu[nt][e] = mn[nt][e] == kNegInf ? 0.f : mn[nt][e];
+            moved = moved || mn[nt][e] != s.m[nt][e];
+        }
+    // the V scales' common power of two: p s / 2^e fills fp16 from the top
+    float2 v0[KP][NG], v1[KP][NG];
+    int em = 0;
+#pragma unroll
+    for (int j = 0; j < KP; j++)
+#pragma unroll
+        for (int gi = 0; gi < NG; gi++) {
+            if (j == 0 || j < np) {
+                const __half2 *vsz = reinterpret_cast<const __half2 *>(st + j * P::kPage + 2 * P::kCodes + P::kSz);
+                const __half2 h0 = vsz[g * NG + gi], h1 = vsz[(g + 8) * NG + gi];
+                em = max(em, max(scale_exp(h0), scale_exp(h1)));
+                v0[j][gi] = __half22float2(h0);
+                v1[j][gi] = __half22float2(h1);
+            }
+        }
+    em = max(s.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)em));
+    if (__any_sync(0xffffffffu, moved) || em != s.e) {
+        const float ae = __int_as_float((s.e - em + 127) << 23);
+        s.e = em;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+                const float al = ex2(s.m[nt][e] - mu[nt][e]), ao = al * ae;
+                s.m[nt][e] = mn[nt][e];
+                s.l[nt][e] *= al;
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++) {
+                    s.z[nt][gi][e] *= al;
+                    s.c[nt][gi][e] *= ao;
+                    s.c[nt][gi][2 + e] *= ao;
+                }
+#pragma unroll
+                for (int d = 0; d < D / 16; d++) {
+                    s.o[nt][d][e] *= ao;
+                    s.o[nt][d][2 + e] *= ao;
+                }
+            }
+    }
+    const float down = scale_down(em);
+#pragma unroll
+    for (int j = 0; j < KP; j++) {
+        if (j > 0 && j >= np) break;
+        unsigned pb[NT][NG][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+            for (int e = 0; e < 2 * E; e++) {
+                sc[j][nt][e] = ex2(sc[j][nt][e] - mu[nt][e % E]);
+                s.l[nt][e % E] += sc[j][nt][e];
+            }
+#pragma unroll
+            for (int gi = 0; gi < NG; gi++) {
+                float w[2 * E];
+#pragma unroll
+                for (int e = 0; e < 2 * E; e++) {
+                    float2 v = e < E ? v0[j][gi] : v1[j][gi];
+                    // a NaN behind the mask must not meet its zero weight
+                    if (MASK) v = 16 * j + g + (e < E ? 0 : 8) < end[nt][e % E] ? v : zero2;
+                    w[e] = sc[j][nt][e] * (v.x * down);
+                    s.z[nt][gi][e % E] += sc[j][nt][e] * fmaf(8.f, v.x, v.y);
+                }
+                pb[nt][gi][0] = movmatrix_t(pack_half2(w[0], E > 1 ? w[E - 1] : 0.f));
+                pb[nt][gi][1] = movmatrix_t(pack_half2(w[E], E > 1 ? w[2 * E - 1] : 0.f));
+            }
+        }
+        page_values<D, GROUP, NT>(st + j * P::kPage, pb, s.o, s.c);
+    }
+}
+
+// Writes the partial of a sequence: normalised output and log2-sum-exp per
+// column, rows pr + column.
+template <int D, int GROUP, int NT, int E>
+__device__ __forceinline__ void write_partial(const Args &a, const Seq &q, State<D, GROUP, NT, E> &s, size_t pr0)
 {
     constexpr int NG = D / GROUP;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int nv = min(8 * NT, q.c.cols - q.tile * 8 * NT);
     const float up = __int_as_float((24 + s.e - 15 + 127) << 23);      // 2^24 / scale_down
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
+        for (int e = 0; e < E; e++) {
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
                 s.l[nt][e] += __shfl_xor_sync(0xffffffffu, s.l[nt][e], off);
@@ -554,12 +751,11 @@ __device__ __forceinline__ void write_item(const Params &p, const Item<D, NT> &i
                 for (int gi = 0; gi < NG; gi++) s.z[nt][gi][e] += __shfl_xor_sync(0xffffffffu, s.z[nt][gi][e], off);
             }
             const int c = 8 * nt + 2 * t + e;
-            if (c >= it.nv) continue;
-            const int v = it.v0 + c, i = v / p.G, h = it.hk * p.G + v % p.G;
-            const size_t pr = it.ql == 1 ? dec_slot(p, it.split, it.b, h) : mq_slot(p, it.split, it.row0 + i, h);
-            const float L = s.l[nt][e], inv = L > 0.f ? 1.f / L : 0.f;
+            if (c >= nv) continue;
+            const size_t pr = pr0 + c;
+            const float L = s.l[nt][e], inv = L == 0.f ? 0.f : 1.f / L;      // (a NaN goes on)
             const float f0 = up * inv, f1 = f0 * 0.0625f;
-            float *po = p.part_o + pr * D;
+            float *po = a.p.part_o + pr * D;
             if constexpr (GROUP == 32) {
 #pragma unroll
                 for (int gi = 0; gi < NG; gi++)
@@ -576,223 +772,332 @@ __device__ __forceinline__ void write_item(const Params &p, const Item<D, NT> &i
                     // tiles: code positions 0, 1, 4, 5 (rows g) and 2, 3, 6, 7 (rows g + 8)
 #pragma unroll
                     for (int r = 0; r < 2; r++) {
-                        const float(&a)[4] = s.o[nt][4 * hf + 2 * r], (&b)[4] = s.o[nt][4 * hf + 2 * r + 1];
+                        const float(&x)[4] = s.o[nt][4 * hf + 2 * r], (&y)[4] = s.o[nt][4 * hf + 2 * r + 1];
                         __stcg(reinterpret_cast<float4 *>(po + 64 * hf + 8 * g + 4 * r),
-                               make_float4(a[e] * f0 + z, b[e] * f1 + z, a[2 + e] * f0 + z, b[2 + e] * f1 + z));
+                               make_float4(x[e] * f0 + z, y[e] * f1 + z, x[2 + e] * f0 + z, y[2 + e] * f1 + z));
                     }
                 }
             }
-            if (g == 0) __stcg(p.part_lse + pr, L > 0.f ? s.m[nt][e] + lg2(L) : kNegInf);
+            if (g == 0) __stcg(a.p.part_lse + pr, L == 0.f ? kNegInf : s.m[nt][e] + lg2(L));
         }
 }
 
-// ----------------------------------------------------------------------------- attention: schedule
-// Shared memory: that of the row items, and the item prefix of this queue.
-template <int D>
-struct SmemQ {
-    Smem<D> row;
-    int it[kMaxB + 1];      // items before request b
-};
-
-// Context work of request b with ql rows and n tokens: columns, tiles of
-// columns, splits and keys per split.  One row: the pages of the context in
-// ns nearly equal runs of at most tps pages; several rows: ranges of ri.split
-// keys (the merge kernel reads both the same way).
-struct Work {
-    ReqInfo ri;
-    int cols, nt, tiles;
-};
-__device__ __forceinline__ Work work_of(const Params &p, int n, int ql, int tps, int max_nt)
-{
-    Work w;
-    w.ri = req_info(p, n, ql, tps);
-    w.cols = ql * p.G;
-    w.nt = w.cols > 8 && max_nt > 1 ? 2 : 1;
-    w.tiles = (w.cols + 8 * w.nt - 1) / (8 * w.nt);
-    return w;
-}
-
-template <int D>
-__device__ void build_schedule_q4(const Params &p, SmemQ<D> &sq, int max_nt, int items_per_warp)
-{
-    constexpr int PER = (kMaxB + kThreads - 1) / kThreads;
-    Smem<D> &s = sq.row;
-    const int tid = threadIdx.x;
-    int vq[PER], pages[PER], nn[PER], items[PER];
-    unsigned flags = 0;
-    if (tid == 0) s.bad = 0;
-#pragma unroll
-    for (int k = 0; k < PER; k++) {
-        const int b = tid * PER + k;
-        int ql = 0, n = 0;
-        if (b < p.B) {
-            ql = p.q_lens ? p.q_lens[b] : p.Lq;
-            n = p.ctx_lens[b];
-            s.segm[b] = ~0u;
-            if (ql < 0 || ql > p.Lq) { flags |= FLAG_BAD_Q_LEN; ql = 0; }
-            if (n < 0 || n > p.max_blocks * kBlock) { flags |= FLAG_BAD_CTX_LEN; ql = n = 0; }
-            s.nctx[b] = n;
-        }
-        vq[k] = ql;
-        nn[k] = n;
-        pages[k] = ql == 1 ? p.HQ * ((n + kBlock - 1) / kBlock) : 0;
-    }
-    __syncthreads();
-    if (flags) atomicOr(&s.bad, (int)flags);
-    block_scan<D, PER>(vq, s.qo, p.B, s);
-    block_scan<D, PER>(pages, s.dec, p.B, s);
-    if (tid == 0) {
-        const long long want = (long long)gridDim.x * kWarps * items_per_warp;
-        s.tps = max(p.tps_min, min(p.tps_max, (int)((s.dec[p.B] + want - 1) / want)));
-        if (s.qo[p.B] > p.max_q_total) s.bad |= FLAG_Q_TOTAL;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < PER; k++) {
-        items[k] = 0;
-        if (vq[k] > 0) {
-            const Work w = work_of(p, nn[k], vq[k], s.tps, max_nt);
-            items[k] = p.Hkv * w.tiles * w.ri.ns;
-        }
-    }
-    block_scan<D, PER>(items, sq.it, p.B, s);
-}
-
-// ----------------------------------------------------------------------------- attention: one item
-template <int D, int GROUP, int NT>
-__device__ void run_item(const Params &p, const Pool &pool, SmemQ<D> &sq, int b, int local, const Work &w)
-{
+// ----------------------------------------------------------------------------- attention: one chunk
+// The pages of a chunk in the order of the line, fetched a few steps ahead
+// of the arithmetic and across the sequences' ends.
+template <int D, int GROUP, int KP, int STAGES>
+struct Loader {
     using P = PageQ<D, GROUP>;
-    constexpr int S = P::kStages;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
-    unsigned char *ring = sq.row.ring + warp * P::kRing;
-    Item<D, NT> it;
-    it.b = b;
-    it.n_ctx = w.ri.n_ctx;
-    it.ql = w.ri.ql;
-    it.row0 = sq.row.qo[b];
-    it.split = local % w.ri.ns;
-    const int r = local / w.ri.ns, tile = r % w.tiles;
-    it.hk = r / w.tiles;
-    it.v0 = tile * 8 * NT;
-    it.nv = min(8 * NT, w.cols - it.v0);
-    // keys that column v sees: max(0, n - ql + 1 + i), and none past the split
-    auto sees = [&](int v) { return max(0, min(it.n_ctx, it.n_ctx - it.ql + 1 + v / p.G)); };
-    const int all = sees(it.v0), most = sees(it.v0 + it.nv - 1);      // first and last row of the item
-    if (it.ql == 1) {
-        it.p0 = (int)((long long)it.split * w.ri.pages / w.ri.ns);
-        it.np = (int)((long long)(it.split + 1) * w.ri.pages / w.ri.ns) - it.p0;
-    } else {
-        it.p0 = it.split * (w.ri.split / kBlock);
-        it.np = (min(most, (it.split + 1) * w.ri.split) + kBlock - 1) / kBlock - it.p0;
-    }
-    const int *table = p.block_tables + (size_t)b * p.max_blocks;
-    int blk = 0, window = -32;      // lane j: block of page `window` + j
-    int issued = 0;
-    auto issue = [&]() {
-        if (issued >= window + 32) {
-            window = issued;
-            blk = issued + lane < it.np ? table[it.p0 + issued + lane] : 0;
+    long long f;            // line position behind the current sequence's share
+    int left;               // pages of the chunk behind it
+    int hk, page, end, n;   // current sequence: next page, end of its share
+    const int *table;
+    int blk, window;        // lane j: block of page window + j
+    int slot;               // ring slot of the next step
+
+    // stages the next step of the chunk, if there is one, as one cp.async group
+    __device__ __forceinline__ void next(const Args &a, const Smem4 &s, unsigned char *ring)
+    {
+        const int lane = threadIdx.x & 31;
+        while (page >= end && left > 0) {
+            const Seq q = locate(a.p, s, f);
+            const int take = min(left, q.pages - q.page);
+            f += take;
+            left -= take;
+            hk = q.hk;
+            n = q.n;
+            page = q.page;
+            end = min(q.page + take, pages_seen(a.p, q));
+            table = a.p.block_tables + (size_t)q.b * a.p.max_blocks;
+            window = page;
+            blk = page + lane < end ? table[page + lane] : 0;
         }
-        load_page<D, GROUP>(p, pool, ring + (issued % S) * P::kStage, __shfl_sync(0xffffffffu, blk, issued - window), it.hk,
-                            min(kBlock, it.n_ctx - (it.p0 + issued) * kBlock), lane);
-        issued++;
-    };
-    for (int k = 0; k < S - 1; k++) {
-        if (issued < it.np) issue();
+        if (page < end) {
+            unsigned char *st = ring + slot * (KP * P::kPage);
+#pragma unroll
+            for (int j = 0; j < KP; j++) {
+                if (page + j < end) {
+                    if (page + j >= window + 32) {
+                        window = page + j;
+                        blk = window + lane < end ? table[window + lane] : 0;
+                    }
+                    load_page<D, GROUP>(a.p, a.pool, st + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window), hk,
+                                        min(kBlock, n - (page + j) * kBlock), lane);
+                }
+            }
+            page += KP;
+            slot = slot + 1 == STAGES ? 0 : slot + 1;
+        }
         cp_async_commit();
     }
-    load_q<D, GROUP, NT>(p, it);
-    float qs[NT][D / GROUP][2];
-    q_sums<D, GROUP, NT>(it, qs);
-    int see[NT][2];
-    State<D, GROUP, NT> s;
+};
+
+// One sequence's share of the chunk: `steps` of it are in the ring or come.
+template <int D, int GROUP, int NT, int E, int KP, int STAGES>
+__device__ __forceinline__ void run_share(const Args &a, const Smem4 &sm, unsigned char *ring, Loader<D, GROUP, KP, STAGES> &ld,
+                                          int &slot, const Seq &q, int take, size_t part)
+{
+    using P = PageQ<D, GROUP>;
+    const Params &p = a.p;
+    const int t = threadIdx.x & 3;
+    const int end_page = min(q.page + take, pages_seen(p, q));
+    unsigned qb[NT][D / 16][2];
+    float qs[NT][D / GROUP][E];
+    load_q<D, GROUP, NT>(p, q, qb);
+    q_sums<D, GROUP, NT, E>(qb, qs);
+    const int v0 = q.tile * 8 * NT, vlast = min(q.c.cols, v0 + 8 * NT) - 1;
+    const int all = keys_seen(q.n, q.ql, v0 / p.G);      // the first row sees least
+    int see[NT][E];
+    State<D, GROUP, NT, E> s;
     s.e = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; nt++)
+    for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
-        for (int e = 0; e < 2; e++) {
-            see[nt][e] = sees(min(it.v0 + 8 * nt + 2 * t + e, it.v0 + it.nv - 1));
+        for (int e = 0; e < E; e++) {
+            see[nt][e] = keys_seen(q.n, q.ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G);
             s.m[nt][e] = kNegInf;
             s.l[nt][e] = 0.f;
 #pragma unroll
-            for (int gi = 0; gi < P::NG; gi++) s.z[nt][gi][e] = s.c[nt][gi][e] = s.c[nt][gi][2 + e] = 0.f;
-#pragma unroll
-            for (int d = 0; d < D / 16; d++) s.o[nt][d][e] = s.o[nt][d][2 + e] = 0.f;
+            for (int gi = 0; gi < P::NG; gi++) s.z[nt][gi][e] = 0.f;
         }
-    for (int j = 0; j < it.np; j++) {
-        cp_async_wait<S - 2>();
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+#pragma unroll
+            for (int gi = 0; gi < P::NG; gi++) s.c[nt][gi][e] = 0.f;
+#pragma unroll
+            for (int d = 0; d < D / 16; d++) s.o[nt][d][e] = 0.f;
+        }
+    }
+    for (int page = q.page; page < end_page; page += KP) {
+        cp_async_wait<STAGES - 2>();
         __syncwarp();
-        const int key0 = (it.p0 + j) * kBlock;
-        int end[NT][2];
+        const int key0 = page * kBlock, np = min(KP, end_page - page);
+        int end[NT][E];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int e = 0; e < 2; e++) end[nt][e] = see[nt][e] - key0;
-        const unsigned char *st = ring + (j % S) * P::kStage;
-        if (key0 + kBlock <= all)
-            page_step<D, GROUP, NT, false>(st, it, qs, s, end, p.scale_log2);
+            for (int e = 0; e < E; e++) end[nt][e] = see[nt][e] - key0;
+        const unsigned char *st = ring + slot * (KP * P::kPage);
+        if (key0 + np * kBlock <= all)
+            step<D, GROUP, NT, E, KP, false>(st, np, qb, qs, s, end, p.scale_log2);
         else
-            page_step<D, GROUP, NT, true>(st, it, qs, s, end, p.scale_log2);
+            step<D, GROUP, NT, E, KP, true>(st, np, qb, qs, s, end, p.scale_log2);
         __syncwarp();
-        if (issued < it.np) issue();
-        cp_async_commit();
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
+        ld.next(a, sm, ring);
     }
-    cp_async_wait<0>();
-    __syncwarp();
-    write_item<D, GROUP, NT>(p, it, s);
+    write_partial<D, GROUP, NT, E>(a, q, s, a.part0 + part * a.nc);
 }
 
-// ----------------------------------------------------------------------------- attention: kernel
-// One CTA of 8 warps per SM, in the two phases of relay_kernel: row teams take
-// the system items (the fp16 prompt, read once per batch), then every warp on
-// its own takes items of the 4-bit contexts from one queue.  Partials and
-// schedule are handed to merge_kernel exactly as relay_kernel does.
-template <int D, int GROUP, int MAXNT>
-__global__ void __launch_bounds__(kThreads, 1) q4_kernel(const __grid_constant__ Params p, const __grid_constant__ Pool pool)
+// ----------------------------------------------------------------------------- attention: kernels
+// The context kernel: one CTA per SM, every warp on its own through chunks of
+// the line.  NT: tensor-core tiles of columns that a sequence may have; E as
+// in State.  It starts beside a grid in front of it that computes the prompt's
+// partials (whichever SMs that leaves) and ends only after it.
+template <int D, int GROUP, int NT, int E>
+__global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(const __grid_constant__ Args a)
 {
+    using G = Geo<D, GROUP, NT>;
     extern __shared__ __align__(128) unsigned char smem_raw[];
-    SmemQ<D> &sq = *reinterpret_cast<SmemQ<D> *>(smem_raw);
-    Smem<D> &s = sq.row;
-    build_schedule_q4<D>(p, sq, MAXNT, 2);
+    Smem4 &s = *reinterpret_cast<Smem4 *>(smem_raw);
+    const Params &p = a.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    build_line<G::kW>(p, s);
+    const long long total = s.pre[p.B], workers = (long long)gridDim.x * G::kW;
+    // pages of a chunk: one chunk a warp up to 24 pages, then up to four
+    // (finer ones balance better, and cost partials)
+    const long long per = (total + workers - 1) / workers;
+    const int parts = (int)min(4ll, (per + 23) / 24);
+    const int Q = (int)max((long long)a.q_min, parts > 1 ? (total + workers * parts - 1) / (workers * parts) : per);
+    const unsigned bad = (unsigned)s.bad | (s.qo[p.B] > p.max_q_total ? FLAG_Q_TOTAL : 0u);
     if (blockIdx.x == 0) {
-        for (int k = threadIdx.x; k <= p.B; k += kThreads) p.sched[1 + k] = s.qo[k];
-        for (int k = threadIdx.x; k < p.B; k += kThreads) p.sched[2 + p.B + k] = s.nctx[k];
-        if (threadIdx.x == 0) p.sched[0] = s.bad ? -1 : s.tps;
-    }
-    if (s.bad) {
-        if (threadIdx.x == 0) atomicOr(&p.ctrl[CTRL_FLAGS], (unsigned)s.bad);
-        return;
-    }
-    const int Mtot = s.qo[p.B];
-    const int T = (Mtot * p.G + kTileM - 1) / kTileM;
-    const int n_sys = has_sys(p.mode) && !p.skip_sys ? p.Hkv * T * p.seg_R[0] : 0;
-    {
-        const int team = team_of();
-        const bool leader = (threadIdx.x % kRowThreads) == 0;
-        for (int item = blockIdx.x + team * gridDim.x; item < n_sys;) {
-            sys_item<D, 0>(p, s, item, Mtot);
-            if (leader) s.item[team] = (int)(kTeams * gridDim.x + atomicAdd(&p.ctrl[CTRL_ROW_ITEMS], 1u));
-            team_sync();
-            item = s.item[team];
-            team_sync();
+        const Sched sc = sched_at(p.sched, p.B);
+        for (int k = threadIdx.x; k <= p.B; k += G::kW * 32) {
+            sc.pre[k] = s.pre[k];
+            sc.qo[k] = s.qo[k];
+            sc.seq[k] = s.seq[k];
+            if (k < p.B) sc.nctx[k] = s.nctx[k];
+        }
+        if (threadIdx.x == 0) {
+            p.sched[0] = bad ? -1 : 0;
+            p.sched[1] = Q;
+            if (bad) atomicOr(&p.ctrl[CTRL_FLAGS], bad);
         }
     }
-    const int n_items = sq.it[p.B];
-    const int lane = threadIdx.x & 31;
-    for (;;) {
-        int id = 0;
-        if (lane == 0) id = (int)atomicAdd(&p.ctrl[CTRL_DEC_ITEMS], 1u);
-        id = __shfl_sync(0xffffffffu, id, 0);
-        if (id >= n_items) break;
-        const int b = find_owner(sq.it, p.B, id);
-        const Work w = work_of(p, s.nctx[b], s.qo[b + 1] - s.qo[b], s.tps, MAXNT);
-        if (MAXNT > 1 && w.nt > 1) run_item<D, GROUP, MAXNT>(p, pool, sq, b, id - sq.it[b], w);
-        else run_item<D, GROUP, 1>(p, pool, sq, b, id - sq.it[b], w);
+    if (!bad) {
+        unsigned char *ring = s.ring + warp * (G::kStages * G::kStep);
+        const long long chunks = (total + Q - 1) / Q;
+        // first chunks are static, spread over the SMs; further ones come from
+        // a queue, asked for one chunk ahead
+        unsigned ticket = 0;
+        for (long long c = (long long)warp * gridDim.x + blockIdx.x; c < chunks;
+             c = workers + __shfl_sync(0xffffffffu, ticket, 0)) {
+            if (lane == 0) ticket = chunks > workers ? atomicAdd(&p.ctrl[CTRL_DEC_ITEMS], 1u) : 0x7fffffffu;
+            long long f = c * Q;
+            int left = (int)min((long long)Q, total - f);
+            Loader<D, GROUP, G::kPer, G::kStages> ld;
+            ld.f = f;
+            ld.left = left;
+            ld.page = ld.end = ld.slot = 0;
+            for (int k = 0; k < G::kStages - 1; k++) ld.next(a, s, ring);
+            int slot = 0;
+            while (left > 0) {
+                const Seq q = locate(p, s, f);
+                const int take = min(left, q.pages - q.page);
+                f += take;
+                left -= take;
+                const size_t part = (size_t)(c + q.id);
+                if (NT > 1 && q.c.nt > 1)
+                    run_share<D, GROUP, NT, E>(a, s, ring, ld, slot, q, take, part);
+                else
+                    run_share<D, GROUP, 1, E>(a, s, ring, ld, slot, q, take, part);
+            }
+            cp_async_wait<0>();
+            __syncwarp();
+        }
     }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
+// The prompt's partials beside it: the system items of the fp16 path (row
+// teams, the prompt read once per batch), in a grid of their own that lets the
+// context kernel start at once.
+template <int D, int KGF>
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ Params p)
+{
+    extern __shared__ __align__(128) unsigned char smem_raw[];
+    Smem<D> &s = *reinterpret_cast<Smem<D> *>(smem_raw);
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    constexpr int PER = (kMaxB + kThreads - 1) / kThreads;
+    int ql[PER];
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int b = threadIdx.x * PER + k;
+        ql[k] = 0;
+        if (b < p.B) {
+            ql[k] = p.q_lens ? p.q_lens[b] : p.Lq;
+            const int n = p.ctx_lens[b];
+            // a bad length fails the whole call (the context kernel reports it)
+            if (ql[k] < 0 || ql[k] > p.Lq || n < 0 || n > p.max_blocks * kBlock) ql[k] = 0;
+        }
+    }
+    block_scan<D, PER>(ql, s.qo, p.B, s);
+    const int Mtot = s.qo[p.B];
+    if (Mtot > p.max_q_total) return;
+    const int n_sys = p.Hkv * ((Mtot * p.G + kTileM - 1) / kTileM) * p.seg_R[0];
+    const int team = team_of();
+    const bool leader = (threadIdx.x % kRowThreads) == 0;
+    for (int item = blockIdx.x + team * gridDim.x; item < n_sys;) {
+        sys_item<D, KGF>(p, s, item, Mtot);
+        if (leader) s.item[team] = (int)(kTeams * gridDim.x + atomicAdd(&p.ctrl[CTRL_ROW_ITEMS], 1u));
+        team_sync();
+        item = s.item[team];
+        team_sync();
+    }
+}
+
+// The fusion: one warp per (row, head) combines the prompt's ranges and the
+// context's partials by their log-sum-exps, as merge_kernel does.
+template <int D>
+__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args a)
+{
+    constexpr int V = D / 32, CH = 8;
+    constexpr float kLn2 = 0.69314718055994531f;
+    __shared__ int qo[kMaxB + 1];
+    const Params &p = a.p;
+    const int lane = threadIdx.x & 31, d0 = lane * V;
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        p.ctrl[CTRL_ROW_ITEMS] = 0u;
+        p.ctrl[CTRL_DEC_ITEMS] = 0u;
+    }
+    const Sched sc = sched_at(p.sched, p.B);
+    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), r = w / p.H, h = w - r * p.H;
+    int b, i, ql;
+    if (p.q_lens) {
+        for (int k = threadIdx.x; k <= p.B; k += 256) qo[k] = sc.qo[k];
+        __syncthreads();
+        if (p.sched[0] < 0 || r >= qo[p.B]) return;
+        b = find_owner(qo, p.B, r);
+        i = r - qo[b];
+        ql = qo[b + 1] - qo[b];
+    } else {
+        b = r / p.Lq;
+        i = r - b * p.Lq;
+        ql = p.Lq;
+        if (b >= p.B) return;
+    }
+    const int bad = __ldcg(p.sched), Q = __ldcg(p.sched + 1), n = __ldcg(sc.nctx + b), seq = __ldcg(sc.seq + b);
+    const long long pre = __ldcg(sc.pre + b);
+    if (bad < 0) return;
+    const Cols c = cols_of(ql, p.G);
+    const int hk = h / p.G, v = i * p.G + h - hk * p.G, tile = v / (8 * c.nt), col = v - tile * 8 * c.nt;
+    const int pages = (n + kBlock - 1) / kBlock, at = hk * c.tiles + tile;
+    const long long f = pre + (long long)at * pages;
+    const long long c0 = f / Q, c1 = (f + pages - 1) / Q;
+    const int n_sys = has_sys(p.mode) ? p.R_sys : 0, n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
+    const size_t sys0 = sys_slot(p, 0, r, h), sys_st = (size_t)p.max_q_total * p.H;
+    const size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col;
+    auto slot = [&](int j) { return j < n_sys ? sys0 + j * sys_st : ctx0 + (size_t)(j - n_sys) * a.nc; };
+    float M = kNegInf, W = 0.f, acc[V];
+#pragma unroll
+    for (int k = 0; k < V; k++) acc[k] = 0.f;
+    for (int j0 = 0; j0 < n_parts; j0 += 32) {
+        const int cnt = min(32, n_parts - j0);
+        const float lk = lane < cnt ? __ldcg(p.part_lse + slot(j0 + lane)) : kNegInf;
+        float mk = lk;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+        const float Mn = fmaxf(M, mk), mu = Mn == kNegInf ? 0.f : Mn, al = ex2(M - mu), wk = ex2(lk - mu);
+        M = Mn;
+        W *= al;
+#pragma unroll
+        for (int k = 0; k < V; k++) acc[k] *= al;
+        for (int k0 = 0; k0 < cnt; k0 += CH) {
+            float x[CH][V];
+#pragma unroll
+            for (int k = 0; k < CH; k++) {
+                if (k0 + k < cnt) {
+                    const float *src = p.part_o + slot(j0 + k0 + k) * D + d0;
+                    if constexpr (V == 4) {
+                        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
+                        x[k][0] = t.x; x[k][1] = t.y; x[k][2] = t.z; x[k][3] = t.w;
+                    } else {
+                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
+                        x[k][0] = t.x; x[k][1] = t.y;
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < CH; k++) {
+                const float wt = __shfl_sync(0xffffffffu, wk, (k0 + k) & 31);
+                if (k0 + k < cnt) {
+                    W += wt;
+#pragma unroll
+                    for (int e = 0; e < V; e++) acc[e] += wt * x[k][e];
+                }
+            }
+        }
+    }
+    const float inv = W == 0.f ? 0.f : 1.f / W;
+    const float lse = W == 0.f ? kNegInf : (M + lg2(W)) * kLn2;
+    const size_t orow = ((size_t)b * p.Lq + i) * p.H + h;
+    if (p.mode == MODE_FUSED) {
+        __half *dst = p.out + orow * D + d0;
+        if constexpr (V == 4)
+            *reinterpret_cast<uint2 *>(dst) =
+                make_uint2(pack_half2(acc[0] * inv, acc[1] * inv), pack_half2(acc[2] * inv, acc[3] * inv));
+        else
+            *reinterpret_cast<unsigned *>(dst) = pack_half2(acc[0] * inv, acc[1] * inv);
+        if (p.lse_out && lane == 0) p.lse_out[orow] = lse;
+    } else {
+        float *dst = p.o_f32 + orow * D + d0;
+#pragma unroll
+        for (int k = 0; k < V; k++) dst[k] = acc[k] * inv;
+        if (lane == 0) p.lse_f32[orow] = lse;
+    }
 }
 
 }  // namespace q4

@@ -10,6 +10,7 @@
 #include <algorithm>
 #include <climits>
 #include <cmath>
+#include <cstddef>
 #include <cstdint>
 #include <mutex>
 
@@ -82,33 +83,58 @@ cudaError_t prepare_kernel(int *occ)
 }
 
 
-// The 4-bit streaming kernel of a shape, its shared memory, and the instances
-// for D, the group size and whether a request may bring more than 8 columns
-// (query rows times query heads of a KV head).
-using Q4Kernel = void (*)(const Params, const q4::Pool);
-Q4Kernel q4_kernel_for(int D, int group, bool wide)
+// The 4-bit context kernel of a shape: instances for D, the group size, and
+// the columns (query rows times query heads of a KV head) that a request may
+// bring: one, up to 8, more.
+struct Q4Kernel {
+    void (*fn)(const q4::Args);
+    int warps;
+    size_t smem;
+};
+template <int D, int GROUP, int NT, int E>
+Q4Kernel q4_instance()
 {
-    if (D == 128) {
-        if (group == 128) return wide ? q4::q4_kernel<128, 128, 2> : q4::q4_kernel<128, 128, 1>;
-        if (group == 64) return wide ? q4::q4_kernel<128, 64, 2> : q4::q4_kernel<128, 64, 1>;
-        return wide ? q4::q4_kernel<128, 32, 2> : q4::q4_kernel<128, 32, 1>;
-    }
-    if (group == 64) return wide ? q4::q4_kernel<64, 64, 2> : q4::q4_kernel<64, 64, 1>;
-    return wide ? q4::q4_kernel<64, 32, 2> : q4::q4_kernel<64, 32, 1>;
+    using G = q4::Geo<D, GROUP, NT>;
+    return {q4::ctx_kernel<D, GROUP, NT, E>, G::kW, offsetof(q4::Smem4, ring) + (size_t)G::kW * G::kStages * G::kStep};
 }
-size_t q4_smem(int D) { return D == 128 ? sizeof(q4::SmemQ<128>) : sizeof(q4::SmemQ<64>); }
+template <int D, int GROUP>
+Q4Kernel q4_instance(long long cols)
+{
+    return cols > 8 ? q4_instance<D, GROUP, 2, 2>() : cols > 1 ? q4_instance<D, GROUP, 1, 2>() : q4_instance<D, GROUP, 1, 1>();
+}
+Q4Kernel q4_kernel(int D, int group, long long cols)
+{
+    if (D == 128)
+        return group == 128 ? q4_instance<128, 128>(cols) : group == 64 ? q4_instance<128, 64>(cols) : q4_instance<128, 32>(cols);
+    return group == 64 ? q4_instance<64, 64>(cols) : q4_instance<64, 32>(cols);
+}
+
+// The kernel of the prompt's items beside it, for the key groups of a tile
+// (row_class; other values: any).
+using PromptKernel = void (*)(const Params);
+PromptKernel prompt_kernel(int D, int key_groups)
+{
+    if (D == 64) return q4::prompt_kernel<64, 0>;
+    return key_groups == 1 ? q4::prompt_kernel<128, 1> : key_groups == 2 ? q4::prompt_kernel<128, 2>
+         : key_groups == 4 ? q4::prompt_kernel<128, 4> : q4::prompt_kernel<128, 0>;
+}
 
 cudaError_t prepare_q4()
 {
-    for (int D : {64, 128})
+    cudaError_t e = cudaSuccess;
+    for (int D : {64, 128}) {
         for (int group : {32, 64, 128})
-            for (bool wide : {false, true}) {
-                if (group > D) continue;
-                const cudaError_t e = cudaFuncSetAttribute(q4_kernel_for(D, group, wide),
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, (int)q4_smem(D));
-                if (e != cudaSuccess) return e;
+            for (int cols : {1, 8, 9}) {
+                if (group > D || e != cudaSuccess) continue;
+                const Q4Kernel k = q4_kernel(D, group, cols);
+                e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
             }
-    return cudaSuccess;
+        for (int kg : {0, 1, 2, 4})
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(prompt_kernel(D, kg), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)(D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>)));
+    }
+    return e;
 }
 
 relay_status_t device_info(const DevInfo **out)
@@ -282,9 +308,8 @@ int round_up(int x, int m) { return (x + m - 1) / m * m; }
 // Work-item sizes and workspace layout for one mode, for a GPU of `sms` SMs
 // (one streaming CTA per SM; the number of system key ranges depends on it).
 // `seg`: several shared prefix segments (never on the tensor-core kernel);
-// null: the one system prompt of dims->Ls tokens.  `q4`: the contexts are in
-// a 4-bit pool.
-Plan make_plan(const relay_dims_t *d, int mode, int sms, const Segments *seg = nullptr, bool q4 = false)
+// null: the one system prompt of dims->Ls tokens.
+Plan make_plan(const relay_dims_t *d, int mode, int sms, const Segments *seg = nullptr)
 {
     Plan pl;
     pl.Mtot = d->max_q_total > 0 ? d->max_q_total : d->B * d->Lq;
@@ -371,27 +396,12 @@ Plan make_plan(const relay_dims_t *d, int mode, int sms, const Segments *seg = n
         pl.tps_min = d->ctx_split > 0 ? pl.tps_max
                                       : std::min(pl.tps_max, std::max(2, (max_pages + kMaxCtxParts - 1) / kMaxCtxParts));
         pl.c_dec = std::max(1, (max_pages + pl.tps_min - 1) / pl.tps_min);
-        int mq_parts = kMaxMqParts;
-        if (q4) {
-            // 4-bit pages are a quarter of the bytes, so items hold more of
-            // them (at least 8, where the context has them); a batch too
-            // small to give every warp an item that way is cut finer, into up
-            // to 256 parts a request
-            const long long warps = (long long)sms * kWarps;
-            const long long per_part = std::max<long long>(1, (long long)d->B * kv_heads(d));
-            const int parts = (int)std::max(64ll, std::min(256ll, 2 * warps / per_part));
-            pl.tps_max = d->ctx_split > 0 ? pl.ctx_split / kBlock : std::max(64, (max_pages + parts - 1) / parts);
-            pl.tps_min = d->ctx_split > 0 ? pl.tps_max : std::max(8, (max_pages + parts - 1) / parts);
-            pl.c_dec = std::max(1, (max_pages + pl.tps_min - 1) / pl.tps_min);
-            const long long tiles = ((long long)d->Lq * G + 15) / 16;
-            mq_parts = (int)std::max(8ll, std::min(64ll, 2 * warps / (per_part * tiles)));
-        }
         const long long max_keys = (long long)pl.n_prefix + (long long)d->max_blocks_per_seq * kBlock;
-        pl.mq_split_min = (int)((max_keys + mq_parts - 1) / mq_parts);
+        pl.mq_split_min = (int)((max_keys + kMaxMqParts - 1) / kMaxMqParts);
         // Requests of at least kTcCtxMinRows virtual rows per KV head take
         // their own context on the tensor cores, one split over all of it,
         // in the same grid as the system step (after its CTAs).
-        pl.ctx_tc = !q4 && d->D == 128 && pl.n_prefix == 0 && d->Lq > 1 && (long long)d->Lq * G >= kTcCtxMinRows &&
+        pl.ctx_tc = d->D == 128 && pl.n_prefix == 0 && d->Lq > 1 && (long long)d->Lq * G >= kTcCtxMinRows &&
                     d->num_blocks > 0 && d->max_blocks_per_seq > 0 && d->max_blocks_per_seq <= tc::kMaxPagesTC;
         if (pl.ctx_tc) {
             pl.mq_split_min = (int)max_keys;
@@ -480,27 +490,9 @@ relay_status_t make_segments(int n_seg, const void *const *k, const void *const 
     return RELAY_OK;
 }
 
-// `q4`: the contexts are in this 4-bit pool (groups of `group` dimensions).
-relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws, size_t ws_bytes,
-                            relay_stream_t stream, const Segments *seg = nullptr, const q4::Pool *q4 = nullptr,
-                            int group = 0)
+// The kernels' view of a shape, and of its prefix segments.
+void set_shape(Params &p, const relay_dims_t *d, const Plan &pl)
 {
-    if (!ws) return RELAY_ERR_WORKSPACE;
-    if (!aligned(ws, 256)) return RELAY_ERR_INVALID_ARG;
-    // host checks first: a workspace too small for any device, and (without
-    // q_lens every request has Lq rows, and the partial slots are laid out
-    // for max_q_total rows) a bound below B * Lq; with q_lens the kernel
-    // checks their sum on the device
-    const bool is_q4 = q4 != nullptr;
-    if (ws_bytes < make_plan(d, mode, 1, seg, is_q4).total) return RELAY_ERR_WORKSPACE;
-    if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1, seg, is_q4).Mtot) return RELAY_ERR_INVALID_ARG;
-    const DevInfo *dev = nullptr;
-    relay_status_t st = device_info(&dev);
-    if (st != RELAY_OK) return st;
-    Plan pl = make_plan(d, mode, dev->sms, seg, is_q4);
-    if (ws_bytes < pl.total) return RELAY_ERR_WORKSPACE;
-
-    unsigned char *base = static_cast<unsigned char *>(ws);
     p.B = d->B;
     p.Lq = d->Lq;
     p.H = d->H;
@@ -514,6 +506,90 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
     p.max_q_total = pl.Mtot;
     p.scale_log2 = scale_log2_of(d);
     p.n_prefix = pl.n_prefix;
+}
+
+void set_segments(Params &p, const Plan &pl, const Segments &sg)
+{
+    p.n_seg = sg.n;
+    for (int i = 0; i < sg.n; i++) {
+        p.seg_k[i] = static_cast<const __half *>(sg.k[i]);
+        p.seg_v[i] = static_cast<const __half *>(sg.v[i]);
+        p.seg_len[i] = sg.len[i];
+        p.seg_range[i] = pl.seg_range[i];
+        p.seg_R[i] = pl.seg_R[i];
+        p.seg_part0[i] = pl.seg_part0[i];
+    }
+}
+
+// The tensor-core grid of a decode step, at the front of `s`.
+relay_status_t launch_tc(const relay_dims_t *d, int mode, const Params &p, const Plan &pl, const DevInfo *dev,
+                         cudaStream_t s)
+{
+    // tensor cores: system partials, one CTA per (range, head, tile
+    // pair), then the multi-row requests' context partials, one CTA per
+    // (request, tile pair, head)
+    tc::TcParams t{};
+    t.B = d->B;
+    t.Lq = d->Lq;
+    t.H = d->H;
+    t.G = p.G;
+    t.Hkv = p.Hkv;
+    t.Ls = d->Ls;
+    t.max_q_total = pl.Mtot;
+    t.scale_log2 = p.scale_log2;
+    t.q = p.q;
+    t.q_lens = p.q_lens;
+    t.flags = p.ctrl;
+    t.part_o = p.part_o;
+    t.part_lse = p.part_lse;
+    t.R = pl.R_sys;
+    t.range = pl.sys_range;
+    t.pairs = tc_pairs(pl.Mtot * p.G);
+    t.n_sys = (int)pl.n_tc_sys;
+    t.ctx_pairs = pl.ctx_pairs;
+    t.ctx_lens = mode == MODE_SYS ? nullptr : p.ctx_lens;
+    t.block_tables = p.block_tables;
+    t.max_blocks = d->max_blocks_per_seq;
+    t.num_blocks = d->num_blocks;
+    t.mq_base = (long long)pl.mq_base;
+    t.queue = p.ctrl + CTRL_TC_QUEUE;
+    CUtensorMap tmK{}, tmV{}, tmKc{}, tmVc{};
+    if (pl.tc && (!encode_sys_map(&tmK, p.sys_k, p.Hkv, d->Ls) || !encode_sys_map(&tmV, p.sys_v, p.Hkv, d->Ls)))
+        return RELAY_ERR_CUDA;
+    if (pl.ctx_tc) {
+        if (!p.k_cache || !p.v_cache || !p.block_tables || !p.ctx_lens) return RELAY_ERR_INVALID_ARG;
+        if (!encode_pool_map(&tmKc, p.k_cache, p.Hkv, d->num_blocks) ||
+            !encode_pool_map(&tmVc, p.v_cache, p.Hkv, d->num_blocks))
+            return RELAY_ERR_CUDA;
+    }
+    // persistent: one CTA per SM at most
+    const long long tc_grid = std::min<long long>(pl.n_tc_sys + pl.n_tc_ctx, dev->sms);
+    t.n_yield = (dev->sms * kTcYieldPct + 50) / 100;
+    t.sms = dev->sms;
+    t.sys_stages = (float)pl.n_tc_sys * (float)((pl.sys_range + tc::kKeysTC - 1) / tc::kKeysTC);
+    tc::sys_tc_kernel<false><<<(unsigned)tc_grid, tc::kThreadsTC, tc::kSmemTC, s>>>(tmK, tmV, tmKc, tmVc, t);
+    return cudaGetLastError() == cudaSuccess ? RELAY_OK : RELAY_ERR_CUDA;
+}
+
+relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws, size_t ws_bytes,
+                            relay_stream_t stream, const Segments *seg = nullptr)
+{
+    if (!ws) return RELAY_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return RELAY_ERR_INVALID_ARG;
+    // host checks first: a workspace too small for any device, and (without
+    // q_lens every request has Lq rows, and the partial slots are laid out
+    // for max_q_total rows) a bound below B * Lq; with q_lens the kernel
+    // checks their sum on the device
+    if (ws_bytes < make_plan(d, mode, 1, seg).total) return RELAY_ERR_WORKSPACE;
+    if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1, seg).Mtot) return RELAY_ERR_INVALID_ARG;
+    const DevInfo *dev = nullptr;
+    relay_status_t st = device_info(&dev);
+    if (st != RELAY_OK) return st;
+    Plan pl = make_plan(d, mode, dev->sms, seg);
+    if (ws_bytes < pl.total) return RELAY_ERR_WORKSPACE;
+
+    unsigned char *base = static_cast<unsigned char *>(ws);
+    set_shape(p, d, pl);
     p.ctrl = reinterpret_cast<unsigned *>(base);
     p.sched = reinterpret_cast<int *>(base + pl.off_sched);
     p.part_o = reinterpret_cast<float *>(base + pl.off_part_o);
@@ -532,66 +608,12 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
     p.skip_mq = pl.ctx_tc ? 1 : 0;
     p.dec_static = (pl.n_tc_sys + pl.n_tc_ctx > 0 || d->B > 32) ? 0 : 3;
     p.mode = mode;
-    {
-        const Segments one = one_segment(d, p.sys_k, p.sys_v);
-        const Segments &sg = seg ? *seg : one;
-        p.n_seg = sg.n;
-        for (int i = 0; i < sg.n; i++) {
-            p.seg_k[i] = static_cast<const __half *>(sg.k[i]);
-            p.seg_v[i] = static_cast<const __half *>(sg.v[i]);
-            p.seg_len[i] = sg.len[i];
-            p.seg_range[i] = pl.seg_range[i];
-            p.seg_R[i] = pl.seg_R[i];
-            p.seg_part0[i] = pl.seg_part0[i];
-        }
-    }
+    set_segments(p, pl, seg ? *seg : one_segment(d, p.sys_k, p.sys_v));
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (pl.n_tc_sys + pl.n_tc_ctx > 0) {
-        // tensor cores: system partials, one CTA per (range, head, tile
-        // pair), then the multi-row requests' context partials, one CTA per
-        // (request, tile pair, head)
-        tc::TcParams t{};
-        t.B = d->B;
-        t.Lq = d->Lq;
-        t.H = d->H;
-        t.G = p.G;
-        t.Hkv = p.Hkv;
-        t.Ls = d->Ls;
-        t.max_q_total = pl.Mtot;
-        t.scale_log2 = p.scale_log2;
-        t.q = p.q;
-        t.q_lens = p.q_lens;
-        t.flags = p.ctrl;
-        t.part_o = p.part_o;
-        t.part_lse = p.part_lse;
-        t.R = pl.R_sys;
-        t.range = pl.sys_range;
-        t.pairs = tc_pairs(pl.Mtot * p.G);
-        t.n_sys = (int)pl.n_tc_sys;
-        t.ctx_pairs = pl.ctx_pairs;
-        t.ctx_lens = mode == MODE_SYS ? nullptr : p.ctx_lens;
-        t.block_tables = p.block_tables;
-        t.max_blocks = d->max_blocks_per_seq;
-        t.num_blocks = d->num_blocks;
-        t.mq_base = (long long)pl.mq_base;
-        t.queue = p.ctrl + CTRL_TC_QUEUE;
-        CUtensorMap tmK{}, tmV{}, tmKc{}, tmVc{};
-        if (pl.tc && (!encode_sys_map(&tmK, p.sys_k, p.Hkv, d->Ls) || !encode_sys_map(&tmV, p.sys_v, p.Hkv, d->Ls)))
-            return RELAY_ERR_CUDA;
-        if (pl.ctx_tc) {
-            if (!p.k_cache || !p.v_cache || !p.block_tables || !p.ctx_lens) return RELAY_ERR_INVALID_ARG;
-            if (!encode_pool_map(&tmKc, p.k_cache, p.Hkv, d->num_blocks) ||
-                !encode_pool_map(&tmVc, p.v_cache, p.Hkv, d->num_blocks))
-                return RELAY_ERR_CUDA;
-        }
-        // persistent: one CTA per SM at most
-        const long long tc_grid = std::min<long long>(pl.n_tc_sys + pl.n_tc_ctx, dev->sms);
-        t.n_yield = (dev->sms * kTcYieldPct + 50) / 100;
-        t.sms = dev->sms;
-        t.sys_stages = (float)pl.n_tc_sys * (float)((pl.sys_range + tc::kKeysTC - 1) / tc::kKeysTC);
-        tc::sys_tc_kernel<false><<<(unsigned)tc_grid, tc::kThreadsTC, tc::kSmemTC, s>>>(tmK, tmV, tmKc, tmVc, t);
-        if (cudaGetLastError() != cudaSuccess) return RELAY_ERR_CUDA;
+        st = launch_tc(d, mode, p, pl, dev, s);
+        if (st != RELAY_OK) return st;
     }
     {
         // the streaming kernel's instance for this shape
@@ -599,10 +621,7 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
         unsigned grid = 0;
         size_t smem = 0;
         const bool grp = p.G > 1;
-        if (q4) {
-            grid = dev->sms;
-            smem = q4_smem(d->D);
-        } else if (d->D == 128) {
+        if (d->D == 128) {
             grid = dev->sms * dev->occ128;
             smem = sizeof(Smem<128>);
             switch (row_class(d, pl, mode, p.G, p.q_lens != nullptr)) {
@@ -631,10 +650,7 @@ relay_status_t launch_relay(const relay_dims_t *d, int mode, Params p, void *ws,
             cfg.attrs = attr;
             cfg.numAttrs = 1;
         }
-        const cudaError_t e =
-            q4 ? cudaLaunchKernelEx(&cfg, q4_kernel_for(d->D, group, (long long)d->Lq * p.G > 8), p, *q4)
-               : cudaLaunchKernelEx(&cfg, fn, p);
-        if (e != cudaSuccess) {
+        if (cudaLaunchKernelEx(&cfg, fn, p) != cudaSuccess) {
             cudaGetLastError();
             return RELAY_ERR_CUDA;
         }
@@ -1044,10 +1060,108 @@ relay_status_t check_q4(const relay_dims_t *d, const relay_q4_cache_t *c)
     return RELAY_OK;
 }
 
-q4::Pool q4_pool(const relay_q4_cache_t *c)
+// Workspace of a call over a 4-bit pool: the prompt's partials as in the fp16
+// plan, then room for every chunk and every sequence of the line (q4::Args).
+struct PlanQ4 {
+    Plan sys;
+    int nc = 0, q_min = 0;
+    size_t off_part_o = 0, off_part_lse = 0, total = 0;
+};
+constexpr int kQ4MinPages = 4;        // pages of a chunk, at least
+constexpr int kQ4MaxWarps = 16;       // warps of a context CTA, at most
+
+PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
 {
-    return {static_cast<const unsigned char *>(c->k_codes), static_cast<const unsigned char *>(c->v_codes),
-            static_cast<const __half2 *>(c->k_sz), static_cast<const __half2 *>(c->v_sz)};
+    PlanQ4 pl;
+    pl.sys = make_plan(d, mode, sms);
+    pl.sys.ctx_tc = false;
+    pl.sys.ctx_pairs = 0;
+    pl.sys.n_tc_ctx = 0;
+    const int G = d->H / kv_heads(d);
+    const long long cols = (long long)d->Lq * G, tiles = cols <= 8 ? 1 : (cols + 15) / 16;
+    const long long seqs = kv_heads(d) * std::min((long long)d->B * tiles, (long long)pl.sys.Mtot * G / 16 + d->B);
+    pl.nc = (int)std::min(cols, cols <= 8 ? 8ll : 16ll);
+    pl.q_min = kQ4MinPages;
+    const double line = (double)d->B * kv_heads(d) * tiles * d->max_blocks_per_seq;
+    const long long chunks = (long long)std::min(line / kQ4MinPages + 1, 4.0 * kQ4MaxWarps * sms + 1);
+    const size_t rows = pl.sys.dec_base + (size_t)(chunks + seqs) * pl.nc;
+    pl.off_part_o = pl.sys.off_sched + (q4::sched_bytes(d->B) + 255) / 256 * 256;
+    pl.off_part_lse = pl.off_part_o + (rows * d->D * sizeof(float) + 255) / 256 * 256;
+    pl.total = pl.off_part_lse + (rows * sizeof(float) + 255) / 256 * 256;
+    return pl;
+}
+
+// The prompt's items and the contexts beside each other, then the fusion: two
+// grids and a third, chained as programmatic dependents.
+relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_q4_cache_t *cache, void *ws, size_t ws_bytes,
+                         relay_stream_t stream)
+{
+    if (!ws) return RELAY_ERR_WORKSPACE;
+    if (!aligned(ws, 256)) return RELAY_ERR_INVALID_ARG;
+    if (ws_bytes < make_plan_q4(d, mode, 1).total) return RELAY_ERR_WORKSPACE;
+    if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1).Mtot) return RELAY_ERR_INVALID_ARG;
+    const long long cols = (long long)d->Lq * (d->H / kv_heads(d));
+    if ((double)kv_heads(d) * ((cols + 7) / 8) * d->max_blocks_per_seq > INT_MAX) return RELAY_ERR_UNSUPPORTED;
+    const DevInfo *dev = nullptr;
+    relay_status_t st = device_info(&dev);
+    if (st != RELAY_OK) return st;
+    const PlanQ4 pl = make_plan_q4(d, mode, dev->sms);
+    if (ws_bytes < pl.total) return RELAY_ERR_WORKSPACE;
+
+    unsigned char *base = static_cast<unsigned char *>(ws);
+    set_shape(p, d, pl.sys);
+    set_segments(p, pl.sys, one_segment(d, p.sys_k, p.sys_v));
+    p.ctrl = reinterpret_cast<unsigned *>(base);
+    p.sched = reinterpret_cast<int *>(base + pl.sys.off_sched);
+    p.part_o = reinterpret_cast<float *>(base + pl.off_part_o);
+    p.part_lse = reinterpret_cast<float *>(base + pl.off_part_lse);
+    p.R_sys = pl.sys.R_sys;
+    p.sys_range = pl.sys.sys_range;
+    p.mode = mode;
+    q4::Args a{};
+    a.p = p;
+    a.pool = {static_cast<const unsigned char *>(cache->k_codes), static_cast<const unsigned char *>(cache->v_codes),
+              static_cast<const __half2 *>(cache->k_sz), static_cast<const __half2 *>(cache->v_sz)};
+    a.nc = pl.nc;
+    a.q_min = pl.q_min;
+    a.part0 = (long long)pl.sys.dec_base;
+
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    bool front = false;      // a grid of this call is in front of the context grid
+    if (pl.sys.n_tc_sys > 0) {
+        st = launch_tc(d, mode, p, pl.sys, dev, s);
+        if (st != RELAY_OK) return st;
+        front = true;
+    } else if (mode == MODE_FUSED && p.R_sys > 0) {
+        const int kg = p.q_lens || d->Lq != 1 ? 0 : row_class(d, pl.sys, MODE_SYS, p.G, false);
+        prompt_kernel(d->D, kg)<<<dev->sms, kThreads, d->D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>), s>>>(p);
+        if (cudaGetLastError() != cudaSuccess) return RELAY_ERR_CUDA;
+        front = true;
+    }
+    const Q4Kernel k = q4_kernel(d->D, cache->group, cols);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(dev->sms);
+    cfg.blockDim = dim3(32 * k.warps);
+    cfg.dynamicSmemBytes = k.smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = front ? 1 : 0;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, a);
+    if (e == cudaSuccess) {
+        cfg.gridDim = dim3((unsigned)(((long long)p.max_q_total * d->H + 7) / 8));
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        cfg.numAttrs = 1;
+        e = d->D == 128 ? cudaLaunchKernelEx(&cfg, q4::merge_kernel<128>, a) : cudaLaunchKernelEx(&cfg, q4::merge_kernel<64>, a);
+    }
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return RELAY_ERR_CUDA;
+    }
+    return RELAY_OK;
 }
 
 }  // namespace
@@ -1059,8 +1173,7 @@ size_t relay_workspace_size_q4(const relay_dims_t *dims)
     if (check_dims(dims) != RELAY_OK) return 0;
     const DevInfo *dev = nullptr;
     const int sms = device_info(&dev) == RELAY_OK ? dev->sms : INT_MAX / 4;
-    return std::max(make_plan(dims, MODE_FUSED, sms, nullptr, true).total,
-                    make_plan(dims, MODE_CTX, sms, nullptr, true).total);
+    return std::max(make_plan_q4(dims, MODE_FUSED, sms).total, make_plan_q4(dims, MODE_CTX, sms).total);
 }
 
 relay_status_t relay_kv_append_q4(const relay_dims_t *dims, const void *k_new, const void *v_new,
@@ -1130,8 +1243,7 @@ relay_status_t relay_ctx_attn_q4(const relay_dims_t *dims, const void *q, const 
     p.q_lens = q_lens;
     p.o_f32 = o_ctx;
     p.lse_f32 = lse_ctx;
-    const q4::Pool pool = q4_pool(cache);
-    return launch_relay(dims, MODE_CTX, p, ws, ws_bytes, stream, nullptr, &pool, cache->group);
+    return launch_q4(dims, MODE_CTX, p, cache, ws, ws_bytes, stream);
 }
 
 relay_status_t relay_attention_decode_q4(const relay_dims_t *dims, const void *q, const void *sys_k, const void *sys_v,
@@ -1158,8 +1270,7 @@ relay_status_t relay_attention_decode_q4(const relay_dims_t *dims, const void *q
     p.q_lens = q_lens;
     p.out = static_cast<__half *>(out);
     p.lse_out = lse_out;
-    const q4::Pool pool = q4_pool(cache);
-    return launch_relay(dims, MODE_FUSED, p, ws, ws_bytes, stream, nullptr, &pool, cache->group);
+    return launch_q4(dims, MODE_FUSED, p, cache, ws, ws_bytes, stream);
 }
 
 // ----------------------------------------------------------------------------- steps around the cache
