@@ -197,7 +197,8 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
 // A page of one KV head is staged as 16 rows of D / 2 bytes, K then V, in
 // 16-byte chunks permuted within 128-byte lines so that the operand reads
 // below (rows g or 2t, word or chunk of the other lane index) meet no bank
-// twice; then the (s, z) pairs of K and of V.
+// twice; then the (s, z) pairs of K and of V.  Pages start on a line, so a
+// chunk's place is an exclusive or away from its row's.
 template <int D, int GROUP>
 struct PageQ {
     static constexpr int kRow = D / 2;               // bytes of a row of codes
@@ -205,28 +206,69 @@ struct PageQ {
     static constexpr int NG = D / GROUP;             // groups of a row
     static constexpr int kSz = kBlock * NG * 4;      // bytes of the (s, z) pairs of K or V
     static constexpr int kPage = 2 * kCodes + 2 * kSz;
+    static_assert(kPage % 128 == 0 && kCodes % 512 == 0 && 2 * kSz <= 512, "a page starts on a line; copies of a warp");
 };
 
 template <int D>
-__device__ __forceinline__ int chunk_off(int row, int ch)
+__device__ __forceinline__ int row_off(int row)
 {
     constexpr int kPerLine = 256 / D;                // rows of a 128-byte line
-    const int line = row / kPerLine, pos = (row % kPerLine) * (D / 32) + ch;
+    const int line = row / kPerLine, pos = (row % kPerLine) * (D / 32);
     return line * 128 + ((pos ^ ((line & 3) << 1)) << 4);
 }
-template <int D>
-__device__ __forceinline__ int byte_off(int row, int byte) { return chunk_off<D>(row, byte >> 4) + (byte & 15); }
+// byte `byte` of a row (row_off)
+__device__ __forceinline__ int byte_off(int row, int byte) { return (row ^ (byte & 0x70)) + (byte & 15); }
+
+// What a lane reads and copies in every page: offsets in the staged page, and
+// where its share of block 0 lies.
+template <int D, int GROUP>
+struct Lane {
+    int k0, k1;                     // its K words: keys g, g + 8
+    int v[4];                       // its V words: keys 2t, 2t + 1, 2t + 8, 2t + 9
+    int sz;                         // the pairs of key g
+    int lane;
+    int to, sz_to, sz_at;           // copies: destinations, place among the pairs, sources
+    const unsigned char *kc, *vc, *szc;
+    bool copies_sz;
+
+    __device__ __forceinline__ void init(const Pool &pool)
+    {
+        using P = PageQ<D, GROUP>;
+        asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));      // (kept, not read again)
+        const int g = lane >> 2, t = lane & 3;
+        const int kb = t * (GROUP / 8), vb = 4 * (GROUP == 32 ? (g & 3) : g);
+        k0 = byte_off(row_off<D>(g), kb);
+        k1 = byte_off(row_off<D>(g + 8), kb);
+#pragma unroll
+        for (int k = 0; k < 4; k++) v[k] = P::kCodes + byte_off(row_off<D>(2 * t + (k & 1) + 8 * (k >> 1)), vb);
+        sz = 2 * P::kCodes + g * P::NG * 4;
+        constexpr int kPerRow = P::kRow / 16, kChunks = P::kSz / 16;
+        to = byte_off(row_off<D>(lane / kPerRow), 16 * (lane % kPerRow));
+        sz_to = 2 * P::kCodes + 16 * lane;
+        kc = pool.k + 16 * lane;
+        vc = pool.v + 16 * lane;
+        szc = reinterpret_cast<const unsigned char *>(lane < kChunks ? pool.ksz : pool.vsz) + 16 * (lane % kChunks);
+        sz_at = 16 * (lane % kChunks);
+        copies_sz = lane < 2 * kChunks;
+    }
+};
 
 // Shape of a CTA: warps, pages of a step (their keys share one round of the
 // softmax), steps in a warp's ring.  One CTA per SM.
 template <int D, int GROUP, int NT>
 struct Geo {
-    static constexpr int kPer = 2;
-    static constexpr int kW = NT > 1 ? 8 : D == 128 && GROUP == 32 ? 12 : 16;
+#ifndef KPER
+#define KPER 2
+#endif
+    static constexpr int kPer = NT > 1 || (D == 128 && GROUP == 32) ? 2 : KPER;
+#ifndef KW
+#define KW 12
+#endif
+    static constexpr int kW = NT > 1 ? 8 : D == 128 ? (GROUP == 32 && KW > 12 ? 12 : KW) : 16;
     static constexpr int kStep = kPer * PageQ<D, GROUP>::kPage;
     static constexpr int kFit = 218 * 1024 / (kW * kStep);
     static constexpr int kStages = kFit < 6 ? kFit : 6;
-    static_assert(kStages >= 3, "ring");
+    static_assert(kStages >= 2, "ring");
 };
 
 // ----------------------------------------------------------------------------- attention: work
@@ -241,6 +283,7 @@ struct Args {
     Pool pool;
     int nc;                   // columns kept per partial
     int q_min;                // pages of a chunk, at least
+    int queue;                // every chunk from the queue (a grid in front has some of the SMs), else the first static
     long long part0;          // first partial row of the contexts
 };
 
@@ -284,13 +327,22 @@ struct Smem4 {
     alignas(128) unsigned char ring[16];      // (the launch gives it its size)
 };
 
-// One sequence at position f of the line.
+// One sequence, and a page of it.
 struct Seq {
     int b, hk, tile, id;      // id: over the whole batch
-    int page, pages;          // page at f, pages of the sequence
+    int page, pages;
     int n, ql;
     Cols c;
 };
+__device__ __forceinline__ void set_request(const Params &p, const Smem4 &s, Seq &q, int b)
+{
+    q.b = b;
+    q.n = s.nctx[b];
+    q.ql = s.qo[b + 1] - s.qo[b];
+    q.c = cols_of(q.ql, p.G);
+    q.pages = (q.n + kBlock - 1) / kBlock;
+}
+// the sequence at position f of the line
 __device__ __forceinline__ Seq locate(const Params &p, const Smem4 &s, long long f)
 {
     Seq q;
@@ -299,11 +351,7 @@ __device__ __forceinline__ Seq locate(const Params &p, const Smem4 &s, long long
         const int mid = (lo + hi + 1) >> 1;
         if (s.pre[mid] <= f) lo = mid; else hi = mid - 1;
     }
-    q.b = lo;
-    q.n = s.nctx[lo];
-    q.ql = s.qo[lo + 1] - s.qo[lo];
-    q.c = cols_of(q.ql, p.G);
-    q.pages = (q.n + kBlock - 1) / kBlock;
+    set_request(p, s, q, lo);
     const unsigned rem = (unsigned)(f - s.pre[lo]);      // the host keeps a request below 2^31 pages
     const int at = (int)(rem / (unsigned)q.pages);
     q.page = (int)rem - at * q.pages;
@@ -311,6 +359,20 @@ __device__ __forceinline__ Seq locate(const Params &p, const Smem4 &s, long long
     q.tile = at - q.hk * q.c.tiles;
     q.id = s.seq[lo] + at;
     return q;
+}
+// the next one of the line (there is one)
+__device__ __forceinline__ void advance(const Params &p, const Smem4 &s, Seq &q)
+{
+    q.page = 0;
+    q.id++;
+    if (++q.tile < q.c.tiles) return;
+    q.tile = 0;
+    if (++q.hk < p.Hkv) return;
+    q.hk = 0;
+    int b = q.b + 1;
+    while (s.pre[b + 1] == s.pre[b]) b++;      // requests without pages
+    set_request(p, s, q, b);
+    q.id = s.seq[b];
 }
 // Keys that row i of a request sees.
 __device__ __forceinline__ int keys_seen(int n, int ql, int i) { return max(0, min(n, n - ql + 1 + i)); }
@@ -391,6 +453,72 @@ __device__ void build_line(const Params &p, Smem4 &s)
 }
 
 // ----------------------------------------------------------------------------- attention: one step
+// The lane's E columns of a tile, one or two.
+template <int E>
+struct Vec {
+    float x[E];
+    __device__ __forceinline__ float &operator[](int e) { return x[e]; }
+    __device__ __forceinline__ float operator[](int e) const { return x[e]; }
+    static __device__ __forceinline__ Vec all(float v)
+    {
+        Vec r;
+#pragma unroll
+        for (int e = 0; e < E; e++) r[e] = v;
+        return r;
+    }
+    // a row (0: keys g, 1: keys g + 8) of an accumulator tile
+    static __device__ __forceinline__ Vec row(const float (&c)[4], int i)
+    {
+        Vec r;
+#pragma unroll
+        for (int e = 0; e < E; e++) r[e] = c[2 * i + e];
+        return r;
+    }
+};
+template <int E>
+__device__ __forceinline__ Vec<E> vfma(Vec<E> a, float b, Vec<E> c)
+{
+    Vec<E> r;
+#pragma unroll
+    for (int e = 0; e < E; e++) r[e] = fmaf(a[e], b, c[e]);
+    return r;
+}
+template <int E>
+__device__ __forceinline__ Vec<E> vmul(Vec<E> a, float b)
+{
+    Vec<E> r;
+#pragma unroll
+    for (int e = 0; e < E; e++) r[e] = a[e] * b;
+    return r;
+}
+
+// the first product of a sum: no accumulator to clear
+__device__ __forceinline__ void mma16816_first(float c[4], const unsigned a[4], unsigned b0, unsigned b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+                 "{%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// the NG pairs of a token
+template <int NG>
+__device__ __forceinline__ void load_pairs(const unsigned char *at, __half2 (&h)[NG])
+{
+    unsigned w[NG];
+    if constexpr (NG == 1) {
+        w[0] = *reinterpret_cast<const unsigned *>(at);
+    } else if constexpr (NG == 2) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        w[0] = x.x; w[1] = x.y;
+    } else {
+        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+    }
+#pragma unroll
+    for (int i = 0; i < NG; i++) h[i] = *reinterpret_cast<const __half2 *>(&w[i]);
+}
+
 // Softmax state of a warp's columns, E of them in a lane (8 nt + 2t, + 1; a
 // batch of single columns has E = 1: column 0, in the lanes of t = 0).  O^T in
 // units of (code * 2^-24 or 2^-20) * 2^-down.
@@ -398,11 +526,12 @@ template <int D, int GROUP, int NT, int E>
 struct State {
     float o[NT][D / 16][4];
     float c[NT][D / GROUP][4];      // the same for a code of 8 in every dimension
-    float z[NT][D / GROUP][E];      // sum of p (z + 8 s) over the lane's keys
-    float m[NT][E], l[NT][E];
+    Vec<E> z[NT][D / GROUP];        // sum of p (z + 8 s) over the lane's keys
+    Vec<E> m[NT], l[NT];
     int e;                          // scale_exp of the largest V scale so far
 };
 
+constexpr float kSlack = 8.f;
 constexpr unsigned kLoCodes = 0x000f000fu, kHiCodes = 0x00f000f0u;
 
 // Biased exponent of a scale, plus one; 0 for an infinite or NaN scale, which
@@ -436,102 +565,79 @@ __device__ __forceinline__ void load_q(const Params &p, const Seq &s, unsigned (
     }
 }
 
-// Sums of q over each group, for the lane's columns of every tile.
+// Sums of q over each group, for the lane's columns of every tile: the product
+// with rows of ones.
 template <int D, int GROUP, int NT, int E>
-__device__ __forceinline__ void q_sums(const unsigned (&qb)[NT][D / 16][2], float (&qs)[NT][D / GROUP][E])
+__device__ __forceinline__ void q_sums(const unsigned (&qb)[NT][D / 16][2], Vec<E> (&qs)[NT][D / GROUP])
 {
     constexpr int WPG = GROUP / 32;
-    const int t = threadIdx.x & 3;
+    const unsigned ones[4] = {0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int gi = 0; gi < D / GROUP; gi++) {
-            float x = 0.f;
+            float x[4];
+            mma16816_first(x, ones, qb[nt][gi * 2 * WPG][0], qb[nt][gi * 2 * WPG][1]);
 #pragma unroll
-            for (int w = gi * 2 * WPG; w < (gi + 1) * 2 * WPG; w++)
-#pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&qb[nt][w][r]));
-                    x += f.x + f.y;
-                }
-            x += __shfl_xor_sync(0xffffffffu, x, 1);
-            x += __shfl_xor_sync(0xffffffffu, x, 2);
-#pragma unroll
-            for (int e = 0; e < E; e++) qs[nt][gi][e] = __shfl_sync(0xffffffffu, x, 8 * t + 4 * e);
+            for (int w = gi * 2 * WPG + 1; w < (gi + 1) * 2 * WPG; w++) mma16816(x, ones, qb[nt][w][0], qb[nt][w][1]);
+            qs[nt][gi] = Vec<E>::row(x, 0);
         }
 }
 
 // One lane's share of staging one page: `rows` valid tokens.  The codes are
 // copied whole (what lies behind the last token is a number either way); the
-// pairs of further tokens read as zero, so that nothing of them is left.
+// pairs of further tokens read as zero, so that nothing of them is left.  A
+// block id outside the pool is flagged and reads as zero.
 template <int D, int GROUP>
-__device__ __forceinline__ void load_page(const Params &p, const Pool &pool, unsigned char *st, int blk, int hk, int rows,
-                                          int lane)
+__device__ __forceinline__ void load_page(const Params &p, const Lane<D, GROUP> &ln, unsigned char *st, int blk, int hk,
+                                          int rows)
 {
     using P = PageQ<D, GROUP>;
-    const bool ok = blk >= 0 && blk < p.num_blocks;
-    if (!ok && lane == 0) atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
-    const size_t page = (size_t)(ok ? blk : 0) * p.Hkv + hk;
-    const unsigned char *kc = pool.k + page * P::kCodes, *vc = pool.v + page * P::kCodes;
+    const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
+    const unsigned page = (ok ? blk : 0) * p.Hkv + hk;      // the host keeps the pool below 2^31 of them
+    const unsigned char *kc = ln.kc + (size_t)page * P::kCodes, *vc = ln.vc + (size_t)page * P::kCodes;
+    const unsigned char *szc = ln.szc + (size_t)page * P::kSz;
+    if (!ok && ln.lane == 0) atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
 #pragma unroll
     for (int k = 0; k < P::kCodes / 512; k++) {
-        const int c = lane + 32 * k;
-        const int dst = chunk_off<D>(c / (D / 32), c % (D / 32));
-        cp_async16(st + dst, kc + 16 * c, ok);
-        cp_async16(st + P::kCodes + dst, vc + 16 * c, ok);
+        cp_async16(st + ln.to + 512 * k, kc + 512 * k, ok);
+        cp_async16(st + P::kCodes + ln.to + 512 * k, vc + 512 * k, ok);
     }
-    constexpr int kChunks = P::kSz / 16;      // of K, then of V
-#pragma unroll
-    for (int c0 = 0; c0 < 2 * kChunks; c0 += 32) {
-        const int c = c0 + lane;
-        if (c < 2 * kChunks) {
-            const int cc = c % kChunks;
-            const unsigned char *src =
-                reinterpret_cast<const unsigned char *>(c < kChunks ? pool.ksz : pool.vsz) + page * P::kSz + 16 * cc;
-            const int n = ok ? min(16, max(0, rows * P::NG * 4 - 16 * cc)) : 0;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;\n" ::"r"(
-                             smem_u32(st + 2 * P::kCodes + 16 * c)),
-                         "l"(src), "r"(n));
-        }
-    }
+    const int n = ok ? min(16, max(0, rows * P::NG * 4 - ln.sz_at)) : 0;
+    if (ln.copies_sz)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(st + ln.sz_to)), "l"(szc), "r"(n));
 }
 
 // S^T = K q of one staged page, a group at a time: keys g, g + 8.
 template <int D, int GROUP, int NT, int E>
-__device__ __forceinline__ void page_scores(const unsigned char *st, const unsigned (&qb)[NT][D / 16][2],
-                                            const float (&qs)[NT][D / GROUP][E], float (&sc)[NT][2 * E])
+__device__ __forceinline__ void page_scores(const unsigned char *st, const Lane<D, GROUP> &ln, const unsigned (&qb)[NT][D / 16][2],
+                                            const Vec<E> (&qs)[NT][D / GROUP], Vec<E> (&sc)[NT][2])
 {
     using P = PageQ<D, GROUP>;
     constexpr int NG = P::NG, WPG = GROUP / 32;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const __half2 *ksz = reinterpret_cast<const __half2 *>(st + 2 * P::kCodes);
-#pragma unroll
-    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-        for (int e = 0; e < 2 * E; e++) sc[nt][e] = 0.f;
+    __half2 h0[NG], h1[NG];
+    load_pairs<NG>(st + ln.sz, h0);
+    load_pairs<NG>(st + ln.sz + 8 * NG * 4, h1);
 #pragma unroll
     for (int gi = 0; gi < NG; gi++) {
         unsigned w0[WPG], w1[WPG];
-        const int byte = gi * (GROUP / 2) + t * (GROUP / 8);
+        const int x0 = gi * (GROUP / 2);      // group gi's bytes: an exclusive or away (a power of two below a line)
+        const unsigned char *r0 = st + (ln.k0 ^ x0), *r1 = st + (ln.k1 ^ x0);
         if constexpr (WPG == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(st + byte_off<D>(g, byte));
-            const uint4 y = *reinterpret_cast<const uint4 *>(st + byte_off<D>(g + 8, byte));
+            const uint4 x = *reinterpret_cast<const uint4 *>(r0);
+            const uint4 y = *reinterpret_cast<const uint4 *>(r1);
             w0[0] = x.x; w0[1] = x.y; w0[2] = x.z; w0[3] = x.w;
             w1[0] = y.x; w1[1] = y.y; w1[2] = y.z; w1[3] = y.w;
         } else if constexpr (WPG == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(st + byte_off<D>(g, byte));
-            const uint2 y = *reinterpret_cast<const uint2 *>(st + byte_off<D>(g + 8, byte));
+            const uint2 x = *reinterpret_cast<const uint2 *>(r0);
+            const uint2 y = *reinterpret_cast<const uint2 *>(r1);
             w0[0] = x.x; w0[1] = x.y;
             w1[0] = y.x; w1[1] = y.y;
         } else {
-            w0[0] = *reinterpret_cast<const unsigned *>(st + byte_off<D>(g, byte));
-            w1[0] = *reinterpret_cast<const unsigned *>(st + byte_off<D>(g + 8, byte));
+            w0[0] = *reinterpret_cast<const unsigned *>(r0);
+            w1[0] = *reinterpret_cast<const unsigned *>(r1);
         }
         float lo[NT][4], hi[NT][4];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) lo[nt][e] = hi[nt][e] = 0.f;
 #pragma unroll
         for (int j = 0; j < WPG; j++) {
             const unsigned x0 = w0[j] >> 8, x1 = w1[j] >> 8;
@@ -540,18 +646,24 @@ __device__ __forceinline__ void page_scores(const unsigned char *st, const unsig
             const int w = 2 * (gi * WPG + j);
 #pragma unroll
             for (int nt = 0; nt < NT; nt++) {
-                mma16816(lo[nt], a0, qb[nt][w][0], qb[nt][w][1]);
-                mma16816(hi[nt], a1, qb[nt][w + 1][0], qb[nt][w + 1][1]);
+                if (j == 0) {
+                    mma16816_first(lo[nt], a0, qb[nt][w][0], qb[nt][w][1]);
+                    mma16816_first(hi[nt], a1, qb[nt][w + 1][0], qb[nt][w + 1][1]);
+                } else {
+                    mma16816(lo[nt], a0, qb[nt][w][0], qb[nt][w][1]);
+                    mma16816(hi[nt], a1, qb[nt][w + 1][0], qb[nt][w + 1][1]);
+                }
             }
         }
-        const float2 k0 = __half22float2(ksz[g * NG + gi]), k1 = __half22float2(ksz[(g + 8) * NG + gi]);
-        const float f0 = k0.x * 0x1p20f, f1 = k1.x * 0x1p20f;
+        const float2 k0 = __half22float2(h0[gi]), k1 = __half22float2(h1[gi]);
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int e = 0; e < E; e++) {
-                sc[nt][e] += f0 * fmaf(lo[nt][e], 16.f, hi[nt][e]) + k0.y * qs[nt][gi][e];
-                sc[nt][E + e] += f1 * fmaf(lo[nt][2 + e], 16.f, hi[nt][2 + e]) + k1.y * qs[nt][gi][e];
+            for (int r = 0; r < 2; r++) {
+                const float2 k = r ? k1 : k0;
+                const Vec<E> dot = vfma(Vec<E>::row(lo[nt], r), 16.f, Vec<E>::row(hi[nt], r));
+                const Vec<E> z = gi ? vfma(qs[nt][gi], k.y, sc[nt][r]) : vmul(qs[nt][gi], k.y);
+                sc[nt][r] = vfma(dot, k.x * 0x1p20f, z);
             }
     }
 }
@@ -562,12 +674,10 @@ __device__ __forceinline__ void page_scores(const unsigned char *st, const unsig
 // their group, so with GROUP = 32 (four words) the two halves of the rows take
 // the same word at positions 8 bits apart.
 template <int D, int GROUP, int NT>
-__device__ __forceinline__ void page_values(const unsigned char *st, const unsigned (&pb)[NT][D / GROUP][2],
+__device__ __forceinline__ void page_values(const unsigned char *st, const Lane<D, GROUP> &ln, const unsigned (&pb)[NT][D / GROUP][2],
                                             float (&o)[NT][D / 16][4], float (&c8)[NT][D / GROUP][4])
 {
     using P = PageQ<D, GROUP>;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const unsigned char *vc = st + P::kCodes;
     constexpr unsigned kEight = 0x00080008u;
     const unsigned eights[4] = {kEight, kEight, kEight, kEight};
 #pragma unroll
@@ -577,16 +687,14 @@ __device__ __forceinline__ void page_values(const unsigned char *st, const unsig
     constexpr int kHalf = GROUP == 32 ? 32 : 64;      // dimensions of a set of tiles
 #pragma unroll
     for (int h = 0; h < D / kHalf; h++) {
-        const int byte = h * (kHalf / 2) + 4 * (GROUP == 32 ? (g & 3) : g);
         unsigned w[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            w[k] = *reinterpret_cast<const unsigned *>(vc + byte_off<D>(2 * t + (k & 1) + 8 * (k >> 1), byte));
+        for (int k = 0; k < 4; k++) w[k] = *reinterpret_cast<const unsigned *>(st + (ln.v[k] ^ (h * (kHalf / 2))));
         unsigned x0 = __byte_perm(w[0], w[1], 0x5410), y0 = __byte_perm(w[0], w[1], 0x7632);
         unsigned x1 = __byte_perm(w[2], w[3], 0x5410), y1 = __byte_perm(w[2], w[3], 0x7632);
         const int gi = h * kHalf / GROUP;
         if constexpr (GROUP == 32) {
-            const int sh = (g >> 2) * 8;
+            const int sh = (ln.lane >> 4) * 8;
             x0 >>= sh; y0 >>= sh; x1 >>= sh; y1 >>= sh;
             const unsigned a0[4] = {x0 & kLoCodes, y0 & kLoCodes, x1 & kLoCodes, y1 & kLoCodes};
             const unsigned a1[4] = {x0 & kHiCodes, y0 & kHiCodes, x1 & kHiCodes, y1 & kHiCodes};
@@ -612,33 +720,31 @@ __device__ __forceinline__ void page_values(const unsigned char *st, const unsig
     }
 }
 
-// One warp, `np` staged pages of one sequence.  end[nt][e]: keys of the step
-// that the lane's column sees (MASK: not all of them by every column).
-template <int D, int GROUP, int NT, int E, int KP, bool MASK>
-__device__ __forceinline__ void step(const unsigned char *st, int np, const unsigned (&qb)[NT][D / 16][2],
-                                     const float (&qs)[NT][D / GROUP][E], State<D, GROUP, NT, E> &s,
-                                     const int (&end)[NT][E], float scale_log2)
+// One warp, KP staged pages of one sequence that every column sees whole
+// (FULL), or np <= KP of which the lane's columns see end[nt][e] keys.
+template <int D, int GROUP, int NT, int E, int KP, bool FULL>
+__device__ __forceinline__ void step(const unsigned char *st, const Lane<D, GROUP> &ln, int np,
+                                     const unsigned (&qb)[NT][D / 16][2], const Vec<E> (&qs)[NT][D / GROUP],
+                                     State<D, GROUP, NT, E> &s, const int (&end)[NT][E], float scale_log2, float slack)
 {
     using P = PageQ<D, GROUP>;
     constexpr int NG = P::NG;
-    const int lane = threadIdx.x & 31, g = lane >> 2;
-    const float2 zero2 = make_float2(0.f, 0.f);
+    const int g = ln.lane >> 2;
 
-    float sc[KP][NT][2 * E];
+    Vec<E> sc[KP][NT][2];      // rows: keys g, g + 8
 #pragma unroll
     for (int j = 0; j < KP; j++) {
-        if (j == 0 || j < np) {
-            page_scores<D, GROUP, NT, E>(st + j * P::kPage, qb, qs, sc[j]);
+        if (FULL || j == 0 || j < np) {
+            page_scores<D, GROUP, NT, E>(st + j * P::kPage, ln, qb, qs, sc[j]);
         } else {
 #pragma unroll
-            for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                for (int e = 0; e < 2 * E; e++) sc[j][nt][e] = kNegInf;
+            for (int nt = 0; nt < NT; nt++) sc[j][nt][0] = sc[j][nt][1] = Vec<E>::all(kNegInf);
         }
     }
-    // online softmax per column (keys over the lanes' g)
+    // online softmax per column (keys over the lanes' g), the running maximum
+    // in units of q . k (the scale is positive)
     bool moved = false;
-    float mu[NT][E], mn[NT][E];
+    Vec<E> mn[NT], mu[NT];      // (mu: minus the maximum, in powers of two)
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -646,52 +752,57 @@ __device__ __forceinline__ void step(const unsigned char *st, int np, const unsi
             float mx = kNegInf;
 #pragma unroll
             for (int j = 0; j < KP; j++) {
-                float x0 = sc[j][nt][e] * scale_log2, x1 = sc[j][nt][E + e] * scale_log2;
-                if (MASK) {
-                    x0 = 16 * j + g < end[nt][e] ? x0 : kNegInf;
-                    x1 = 16 * j + g + 8 < end[nt][e] ? x1 : kNegInf;
+                if (!FULL) {
+                    if (16 * j + g >= end[nt][e]) sc[j][nt][0][e] = kNegInf;
+                    if (16 * j + g + 8 >= end[nt][e]) sc[j][nt][1][e] = kNegInf;
                 }
-                sc[j][nt][e] = x0;
-                sc[j][nt][E + e] = x1;
-                mx = fmaxf(mx, fmaxf(x0, x1));
+                mx = fmaxf(mx, fmaxf(sc[j][nt][0][e], sc[j][nt][1][e]));
             }
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            mn[nt][e] = fmaxf(s.m[nt][e], mx);
-            mu[nt][e] = mn[nt][e] == kNegInf ? 0.f : mn[nt][e];
-            moved = moved || mn[nt][e] != s.m[nt][e];
+            // a reference that the maximum has left by less than 2^kSlack is
+            // kept: weights up to that are as exact, and most steps rescale nothing
+            const float m = s.m[nt][e];
+            const bool move = mx > m + slack;      // (always, from minus infinity to a number)
+            mn[nt][e] = move ? mx : m;
+            mu[nt][e] = mn[nt][e] == kNegInf ? 0.f : -mn[nt][e] * scale_log2;
+            moved = moved || move;
         }
     // the V scales' common power of two: p s / 2^e fills fp16 from the top
-    float2 v0[KP][NG], v1[KP][NG];
+    __half2 h[KP][2][NG];
     int em = 0;
 #pragma unroll
     for (int j = 0; j < KP; j++)
+        if (FULL || j == 0 || j < np) {
 #pragma unroll
-        for (int gi = 0; gi < NG; gi++) {
-            if (j == 0 || j < np) {
-                const __half2 *vsz = reinterpret_cast<const __half2 *>(st + j * P::kPage + 2 * P::kCodes + P::kSz);
-                const __half2 h0 = vsz[g * NG + gi], h1 = vsz[(g + 8) * NG + gi];
-                em = max(em, max(scale_exp(h0), scale_exp(h1)));
-                v0[j][gi] = __half22float2(h0);
-                v1[j][gi] = __half22float2(h1);
+            for (int r = 0; r < 2; r++) {
+                load_pairs<NG>(st + j * P::kPage + P::kSz + ln.sz + r * 8 * NG * 4, h[j][r]);
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++)
+                    if (!FULL) em = max(em, scale_exp(h[j][r][gi]));
             }
         }
+    if (FULL) {      // the keys are all seen: their largest scale as it is
+        __half2 top = __habs2(h[0][0][0]);
+#pragma unroll
+        for (int i = 1; i < KP * 2 * NG; i++) top = __hmax2(top, __habs2(h[i / (2 * NG)][i / NG % 2][i % NG]));
+        em = scale_exp(top);
+    }
     em = max(s.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)em));
-    if (__any_sync(0xffffffffu, moved) || em != s.e) {
+    if (__any_sync(0xffffffffu, moved || em != s.e)) {
         const float ae = __int_as_float((s.e - em + 127) << 23);
         s.e = em;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                const float al = ex2(s.m[nt][e] - mu[nt][e]), ao = al * ae;
+                const float al = ex2(fmaf(s.m[nt][e], scale_log2, mu[nt][e])), ao = al * ae;
                 s.m[nt][e] = mn[nt][e];
                 s.l[nt][e] *= al;
 #pragma unroll
                 for (int gi = 0; gi < NG; gi++) {
                     s.z[nt][gi][e] *= al;
                     s.c[nt][gi][e] *= ao;
-                    s.c[nt][gi][2 + e] *= ao;
                 }
 #pragma unroll
                 for (int d = 0; d < D / 16; d++) {
@@ -703,31 +814,44 @@ __device__ __forceinline__ void step(const unsigned char *st, int np, const unsi
     const float down = scale_down(em);
 #pragma unroll
     for (int j = 0; j < KP; j++) {
-        if (j > 0 && j >= np) break;
+        if (!FULL && j > 0 && j >= np) break;
         unsigned pb[NT][NG][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) {
+        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-            for (int e = 0; e < 2 * E; e++) {
-                sc[j][nt][e] = ex2(sc[j][nt][e] - mu[nt][e % E]);
-                s.l[nt][e % E] += sc[j][nt][e];
-            }
+            for (int r = 0; r < 2; r++) {
+                sc[j][nt][r] = vfma(sc[j][nt][r], scale_log2, mu[nt]);
 #pragma unroll
-            for (int gi = 0; gi < NG; gi++) {
-                float w[2 * E];
-#pragma unroll
-                for (int e = 0; e < 2 * E; e++) {
-                    float2 v = e < E ? v0[j][gi] : v1[j][gi];
-                    // a NaN behind the mask must not meet its zero weight
-                    if (MASK) v = 16 * j + g + (e < E ? 0 : 8) < end[nt][e % E] ? v : zero2;
-                    w[e] = sc[j][nt][e] * (v.x * down);
-                    s.z[nt][gi][e % E] += sc[j][nt][e] * fmaf(8.f, v.x, v.y);
+                for (int e = 0; e < E; e++) {
+                    sc[j][nt][r][e] = ex2(sc[j][nt][r][e]);
+                    s.l[nt][e] += sc[j][nt][r][e];
                 }
-                pb[nt][gi][0] = movmatrix_t(pack_half2(w[0], E > 1 ? w[E - 1] : 0.f));
-                pb[nt][gi][1] = movmatrix_t(pack_half2(w[E], E > 1 ? w[2 * E - 1] : 0.f));
             }
-        }
-        page_values<D, GROUP, NT>(st + j * P::kPage, pb, s.o, s.c);
+#pragma unroll
+        for (int gi = 0; gi < NG; gi++)
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const float2 v = __half22float2(h[j][r][gi]);
+                const float vs = v.x * down, vz = fmaf(8.f, v.x, v.y);
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    Vec<E> w;
+                    if (FULL) {
+                        w = vmul(sc[j][nt][r], vs);
+                        s.z[nt][gi] = vfma(sc[j][nt][r], vz, s.z[nt][gi]);
+                    } else {
+                        // a NaN behind the mask must not meet its zero weight
+#pragma unroll
+                        for (int e = 0; e < E; e++) {
+                            const bool seen = 16 * j + g + 8 * r < end[nt][e];
+                            w[e] = seen ? sc[j][nt][r][e] * vs : 0.f;
+                            s.z[nt][gi][e] += seen ? sc[j][nt][r][e] * vz : 0.f;
+                        }
+                    }
+                    pb[nt][gi][r] = movmatrix_t(pack_half2(w[0], E > 1 ? w[E - 1] : 0.f));
+                }
+            }
+        page_values<D, GROUP, NT>(st + j * P::kPage, ln, pb, s.o, s.c);
     }
 }
 
@@ -778,88 +902,127 @@ __device__ __forceinline__ void write_partial(const Args &a, const Seq &q, State
                     }
                 }
             }
-            if (g == 0) __stcg(a.p.part_lse + pr, L == 0.f ? kNegInf : s.m[nt][e] + lg2(L));
+            if (g == 0) __stcg(a.p.part_lse + pr, L == 0.f ? kNegInf : fmaf(s.m[nt][e], a.p.scale_log2, lg2(L)));
         }
 }
 
 // ----------------------------------------------------------------------------- attention: one chunk
-// The pages of a chunk in the order of the line, fetched a few steps ahead
-// of the arithmetic and across the sequences' ends.
+// The chunks of a warp: the first one is static (spread over the SMs) where
+// all CTAs start together, the others come from a queue and are asked for one
+// ahead.
+struct Chunks {
+    long long total, count, queue0;      // queue0: the queue's first chunk
+    int Q;
+    unsigned ticket;
+
+    __device__ __forceinline__ void ask(const Params &p)
+    {
+        ticket = 0x7fffffffu;
+        if (count > queue0 && (threadIdx.x & 31) == 0) ticket = atomicAdd(&p.ctrl[CTRL_DEC_ITEMS], 1u);
+    }
+    __device__ __forceinline__ long long take() const { return queue0 + __shfl_sync(0xffffffffu, ticket, 0); }
+};
+
+// Position in a chunk: the current sequence and the pages behind its share.
+struct Walk {
+    Seq q;
+    int left;               // pages of the chunk from the sequence's page on
+
+    __device__ __forceinline__ void start(const Params &p, const Smem4 &s, const Chunks &ch, long long c)
+    {
+        q = locate(p, s, c * ch.Q);
+        left = (int)min((long long)ch.Q, ch.total - c * ch.Q);
+    }
+    __device__ __forceinline__ int take() const { return min(left, q.pages - q.page); }
+    __device__ __forceinline__ void next(const Params &p, const Smem4 &s)
+    {
+        left -= take();
+        if (left > 0) advance(p, s, q);
+    }
+};
+
+// The pages in the order of the line, fetched a few steps ahead of the
+// arithmetic, across the ends of sequences and chunks.
 template <int D, int GROUP, int KP, int STAGES>
 struct Loader {
     using P = PageQ<D, GROUP>;
-    long long f;            // line position behind the current sequence's share
-    int left;               // pages of the chunk behind it
-    int hk, page, end, n;   // current sequence: next page, end of its share
-    const int *table;
-    int blk, window;        // lane j: block of page window + j
-    int slot;               // ring slot of the next step
+    Walk w;
+    long long ahead;            // the warp's next chunk, once taken from the queue (else -1)
+    int page, end;              // next page, end of the sequence's share
+    int blk, window;            // lane j: block of page window + j
+    int slot;                   // ring slot of the next step
+    int issued;                 // steps staged so far
 
-    // stages the next step of the chunk, if there is one, as one cp.async group
-    __device__ __forceinline__ void next(const Args &a, const Smem4 &s, unsigned char *ring)
+    __device__ __forceinline__ const int *table(const Params &p) const { return p.block_tables + (size_t)w.q.b * p.max_blocks; }
+    __device__ __forceinline__ void enter(const Params &p, int lane)
     {
-        const int lane = threadIdx.x & 31;
-        while (page >= end && left > 0) {
-            const Seq q = locate(a.p, s, f);
-            const int take = min(left, q.pages - q.page);
-            f += take;
-            left -= take;
-            hk = q.hk;
-            n = q.n;
-            page = q.page;
-            end = min(q.page + take, pages_seen(a.p, q));
-            table = a.p.block_tables + (size_t)q.b * a.p.max_blocks;
-            window = page;
-            blk = page + lane < end ? table[page + lane] : 0;
-        }
-        if (page < end) {
+        page = w.q.page;
+        end = min(page + w.take(), pages_seen(p, w.q));
+        window = page;
+        blk = page + lane < end ? table(p)[page + lane] : 0;
+    }
+    // Stages the warp's next steps, a cp.async group each, until the ring is
+    // full (`done` steps have left it) or nothing is left to stage.
+    __device__ __forceinline__ void fill(const Args &a, const Smem4 &s, const Lane<D, GROUP> &ln, const Chunks &ch,
+                                         unsigned char *ring, int done)
+    {
+        const int lane = ln.lane;
+        while (issued - done < STAGES - 1) {
+            while (page >= end) {
+                if (w.left > 0) w.next(a.p, s);
+                if (w.left <= 0) {
+                    if (ahead >= 0) return;            // one chunk ahead at most
+                    ahead = ch.take();
+                    if (ahead >= ch.count) return;
+                    w.start(a.p, s, ch, ahead);
+                }
+                enter(a.p, lane);
+            }
             unsigned char *st = ring + slot * (KP * P::kPage);
 #pragma unroll
             for (int j = 0; j < KP; j++) {
                 if (page + j < end) {
                     if (page + j >= window + 32) {
                         window = page + j;
-                        blk = window + lane < end ? table[window + lane] : 0;
+                        blk = window + lane < end ? table(a.p)[window + lane] : 0;
                     }
-                    load_page<D, GROUP>(a.p, a.pool, st + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window), hk,
-                                        min(kBlock, n - (page + j) * kBlock), lane);
+                    load_page<D, GROUP>(a.p, ln, st + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window), w.q.hk,
+                                        w.q.n - (page + j) * kBlock);
                 }
             }
             page += KP;
             slot = slot + 1 == STAGES ? 0 : slot + 1;
+            issued++;
+            cp_async_commit();
         }
-        cp_async_commit();
     }
 };
 
-// One sequence's share of the chunk: `steps` of it are in the ring or come.
+// One sequence's share of the chunk: its steps are in the ring or come.
 template <int D, int GROUP, int NT, int E, int KP, int STAGES>
-__device__ __forceinline__ void run_share(const Args &a, const Smem4 &sm, unsigned char *ring, Loader<D, GROUP, KP, STAGES> &ld,
-                                          int &slot, const Seq &q, int take, size_t part)
+__device__ __forceinline__ void run_share(const Args &a, const Smem4 &sm, const Lane<D, GROUP> &ln, const Chunks &ch,
+                                          unsigned char *ring, Loader<D, GROUP, KP, STAGES> &ld, int &slot, int &done,
+                                          const Seq &q, int take, size_t part)
 {
     using P = PageQ<D, GROUP>;
     const Params &p = a.p;
-    const int t = threadIdx.x & 3;
+    const int t = ln.lane & 3;
     const int end_page = min(q.page + take, pages_seen(p, q));
     unsigned qb[NT][D / 16][2];
-    float qs[NT][D / GROUP][E];
+    Vec<E> qs[NT][D / GROUP];
     load_q<D, GROUP, NT>(p, q, qb);
     q_sums<D, GROUP, NT, E>(qb, qs);
     const int v0 = q.tile * 8 * NT, vlast = min(q.c.cols, v0 + 8 * NT) - 1;
     const int all = keys_seen(q.n, q.ql, v0 / p.G);      // the first row sees least
-    int see[NT][E];
+    const float slack = kSlack / p.scale_log2;
     State<D, GROUP, NT, E> s;
     s.e = 0;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
+        s.m[nt] = Vec<E>::all(kNegInf);
+        s.l[nt] = Vec<E>::all(0.f);
 #pragma unroll
-        for (int e = 0; e < E; e++) {
-            see[nt][e] = keys_seen(q.n, q.ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G);
-            s.m[nt][e] = kNegInf;
-            s.l[nt][e] = 0.f;
-#pragma unroll
-            for (int gi = 0; gi < P::NG; gi++) s.z[nt][gi][e] = 0.f;
-        }
+        for (int gi = 0; gi < P::NG; gi++) s.z[nt][gi] = Vec<E>::all(0.f);
 #pragma unroll
         for (int e = 0; e < 4; e++) {
 #pragma unroll
@@ -869,22 +1032,26 @@ __device__ __forceinline__ void run_share(const Args &a, const Smem4 &sm, unsign
         }
     }
     for (int page = q.page; page < end_page; page += KP) {
-        cp_async_wait<STAGES - 2>();
+        // the ring is full but at the end of the warp's work
+        if (ld.issued - done == STAGES - 1) cp_async_wait<STAGES - 2>();
+        else cp_async_wait<0>();
         __syncwarp();
-        const int key0 = page * kBlock, np = min(KP, end_page - page);
-        int end[NT][E];
-#pragma unroll
-        for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-            for (int e = 0; e < E; e++) end[nt][e] = see[nt][e] - key0;
+        const int key0 = page * kBlock;
         const unsigned char *st = ring + slot * (KP * P::kPage);
-        if (key0 + np * kBlock <= all)
-            step<D, GROUP, NT, E, KP, false>(st, np, qb, qs, s, end, p.scale_log2);
-        else
-            step<D, GROUP, NT, E, KP, true>(st, np, qb, qs, s, end, p.scale_log2);
+        int end[NT][E];
+        if (page + KP <= end_page && key0 + KP * kBlock <= all) {
+            step<D, GROUP, NT, E, KP, true>(st, ln, KP, qb, qs, s, end, p.scale_log2, slack);
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < E; e++)
+                    end[nt][e] = keys_seen(q.n, q.ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G) - key0;
+            step<D, GROUP, NT, E, KP, false>(st, ln, end_page - page, qb, qs, s, end, p.scale_log2, slack);
+        }
         __syncwarp();
         slot = slot + 1 == STAGES ? 0 : slot + 1;
-        ld.next(a, sm, ring);
+        ld.fill(a, sm, ln, ch, ring, ++done);
     }
     write_partial<D, GROUP, NT, E>(a, q, s, a.part0 + part * a.nc);
 }
@@ -901,14 +1068,19 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     extern __shared__ __align__(128) unsigned char smem_raw[];
     Smem4 &s = *reinterpret_cast<Smem4 *>(smem_raw);
     const Params &p = a.p;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int warp = threadIdx.x >> 5;
+    Chunks ch;
+    ch.count = 1;      // (asked for before the number of chunks is known)
+    ch.queue0 = 0;
+    if (a.queue) ch.ask(p);
     build_line<G::kW>(p, s);
     const long long total = s.pre[p.B], workers = (long long)gridDim.x * G::kW;
-    // pages of a chunk: one chunk a warp up to 24 pages, then up to four
-    // (finer ones balance better, and cost partials)
+    // pages of a chunk: one chunk a warp up to 24 pages (two where the warps
+    // do not start together), then two or three: finer ones balance better,
+    // and cost partials
     const long long per = (total + workers - 1) / workers;
-    const int parts = (int)min(4ll, (per + 23) / 24);
-    const int Q = (int)max((long long)a.q_min, parts > 1 ? (total + workers * parts - 1) / (workers * parts) : per);
+    const int parts = per <= 24 ? 1 + a.queue : 2 + a.queue;
+    const int Q = (int)max((long long)a.q_min, (total + workers * parts - 1) / (workers * parts));
     const unsigned bad = (unsigned)s.bad | (s.qo[p.B] > p.max_q_total ? FLAG_Q_TOTAL : 0u);
     if (blockIdx.x == 0) {
         const Sched sc = sched_at(p.sched, p.B);
@@ -924,37 +1096,49 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
             if (bad) atomicOr(&p.ctrl[CTRL_FLAGS], bad);
         }
     }
-    if (!bad) {
+    ch.total = total;
+    ch.count = (total + Q - 1) / Q;
+    const long long first = a.queue ? ch.take() : (long long)warp * gridDim.x + blockIdx.x;
+    ch.queue0 = a.queue ? 0 : workers;
+    ch.Q = Q;
+    if (!bad && first < ch.count) {
         unsigned char *ring = s.ring + warp * (G::kStages * G::kStep);
-        const long long chunks = (total + Q - 1) / Q;
-        // first chunks are static, spread over the SMs; further ones come from
-        // a queue, asked for one chunk ahead
-        unsigned ticket = 0;
-        for (long long c = (long long)warp * gridDim.x + blockIdx.x; c < chunks;
-             c = workers + __shfl_sync(0xffffffffu, ticket, 0)) {
-            if (lane == 0) ticket = chunks > workers ? atomicAdd(&p.ctrl[CTRL_DEC_ITEMS], 1u) : 0x7fffffffu;
-            long long f = c * Q;
-            int left = (int)min((long long)Q, total - f);
-            Loader<D, GROUP, G::kPer, G::kStages> ld;
-            ld.f = f;
-            ld.left = left;
-            ld.page = ld.end = ld.slot = 0;
-            for (int k = 0; k < G::kStages - 1; k++) ld.next(a, s, ring);
-            int slot = 0;
-            while (left > 0) {
-                const Seq q = locate(p, s, f);
-                const int take = min(left, q.pages - q.page);
-                f += take;
-                left -= take;
-                const size_t part = (size_t)(c + q.id);
-                if (NT > 1 && q.c.nt > 1)
-                    run_share<D, GROUP, NT, E>(a, s, ring, ld, slot, q, take, part);
+        Lane<D, GROUP> ln;
+        ln.init(a.pool);
+        ch.ask(p);
+        Walk w;
+        w.start(p, s, ch, first);
+        Loader<D, GROUP, G::kPer, G::kStages> ld;
+        ld.w = w;
+        ld.ahead = -1;
+        ld.slot = ld.issued = 0;
+        ld.enter(p, ln.lane);
+        int slot = 0, done = 0;
+        for (long long c = first;;) {
+            ld.fill(a, s, ln, ch, ring, done);
+            for (;;) {
+                const size_t part = (size_t)(c + w.q.id);
+                if (NT > 1 && w.q.c.nt > 1)
+                    run_share<D, GROUP, NT, E>(a, s, ln, ch, ring, ld, slot, done, w.q, w.take(), part);
                 else
-                    run_share<D, GROUP, 1, E>(a, s, ring, ld, slot, q, take, part);
+                    run_share<D, GROUP, 1, E>(a, s, ln, ch, ring, ld, slot, done, w.q, w.take(), part);
+                w.next(p, s);
+                if (w.left <= 0) break;
             }
-            cp_async_wait<0>();
-            __syncwarp();
+            // the next chunk: the one the loader is ahead in, or (it never
+            // came to this one's end, which has no page to read) a new one
+            const bool in = ld.ahead >= 0;
+            c = in ? ld.ahead : ch.take();
+            if (c >= ch.count) break;
+            w.start(p, s, ch, c);
+            ch.ask(p);
+            ld.ahead = -1;
+            if (!in) {
+                ld.w = w;
+                ld.enter(p, ln.lane);
+            }
         }
+        cp_async_wait<0>();
     }
     __syncthreads();
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -998,89 +1182,130 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     }
 }
 
-// The fusion: one warp per (row, head) combines the prompt's ranges and the
-// context's partials by their log-sum-exps, as merge_kernel does.
-template <int D>
+// The fusion: WPR warps per (row, head) combine the prompt's ranges and the
+// context's partials by their log-sum-exps, as merge_kernel of the fp16 path
+// does.  With few rows it is one memory round trip after another, so four
+// warps share a row's parts; with many rows one warp a row moves the bytes.
+template <int D, int WPR>
 __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args a)
 {
-    constexpr int V = D / 32, CH = 8;
+    constexpr int V = D / 32, CH = 8, kRows = 8 / WPR;
     constexpr float kLn2 = 0.69314718055994531f;
     __shared__ int qo[kMaxB + 1];
+    __shared__ float sm_m[8], sm_w[8];
+    __shared__ float sm_acc[WPR > 1 ? 8 : 1][D];
     const Params &p = a.p;
-    const int lane = threadIdx.x & 31, d0 = lane * V;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR, d0 = lane * V;
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.ctrl[CTRL_ROW_ITEMS] = 0u;
         p.ctrl[CTRL_DEC_ITEMS] = 0u;
     }
     const Sched sc = sched_at(p.sched, p.B);
-    const int w = blockIdx.x * 8 + (threadIdx.x >> 5), r = w / p.H, h = w - r * p.H;
-    int b, i, ql;
+    const int w = blockIdx.x * kRows + warp / WPR, r = w / p.H, h = w - r * p.H;
+    int b = 0, i = 0, ql = p.Lq;
+    bool live = true;
     if (p.q_lens) {
         for (int k = threadIdx.x; k <= p.B; k += 256) qo[k] = sc.qo[k];
         __syncthreads();
-        if (p.sched[0] < 0 || r >= qo[p.B]) return;
-        b = find_owner(qo, p.B, r);
-        i = r - qo[b];
-        ql = qo[b + 1] - qo[b];
+        live = p.sched[0] >= 0 && r < qo[p.B];
+        if (live) {
+            b = find_owner(qo, p.B, r);
+            i = r - qo[b];
+            ql = qo[b + 1] - qo[b];
+        }
     } else {
         b = r / p.Lq;
         i = r - b * p.Lq;
-        ql = p.Lq;
-        if (b >= p.B) return;
+        live = b < p.B;
+        if (!live) b = 0;
     }
     const int bad = __ldcg(p.sched), Q = __ldcg(p.sched + 1), n = __ldcg(sc.nctx + b), seq = __ldcg(sc.seq + b);
     const long long pre = __ldcg(sc.pre + b);
-    if (bad < 0) return;
-    const Cols c = cols_of(ql, p.G);
-    const int hk = h / p.G, v = i * p.G + h - hk * p.G, tile = v / (8 * c.nt), col = v - tile * 8 * c.nt;
-    const int pages = (n + kBlock - 1) / kBlock, at = hk * c.tiles + tile;
-    const long long f = pre + (long long)at * pages;
-    const long long c0 = f / Q, c1 = (f + pages - 1) / Q;
-    const int n_sys = has_sys(p.mode) ? p.R_sys : 0, n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
-    const size_t sys0 = sys_slot(p, 0, r, h), sys_st = (size_t)p.max_q_total * p.H;
-    const size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col;
-    auto slot = [&](int j) { return j < n_sys ? sys0 + j * sys_st : ctx0 + (size_t)(j - n_sys) * a.nc; };
+    live = live && bad >= 0;
     float M = kNegInf, W = 0.f, acc[V];
 #pragma unroll
     for (int k = 0; k < V; k++) acc[k] = 0.f;
-    for (int j0 = 0; j0 < n_parts; j0 += 32) {
-        const int cnt = min(32, n_parts - j0);
-        const float lk = lane < cnt ? __ldcg(p.part_lse + slot(j0 + lane)) : kNegInf;
-        float mk = lk;
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
-        const float Mn = fmaxf(M, mk), mu = Mn == kNegInf ? 0.f : Mn, al = ex2(M - mu), wk = ex2(lk - mu);
-        M = Mn;
-        W *= al;
-#pragma unroll
-        for (int k = 0; k < V; k++) acc[k] *= al;
-        for (int k0 = 0; k0 < cnt; k0 += CH) {
+    if (live) {
+        const Cols c = cols_of(ql, p.G);
+        const int hk = h / p.G, v = i * p.G + h - hk * p.G, tile = v / (8 * c.nt), col = v - tile * 8 * c.nt;
+        const int pages = (n + kBlock - 1) / kBlock, at = hk * c.tiles + tile;
+        const long long f = pre + (long long)at * pages;
+        const long long c0 = f / Q, c1 = (f + pages - 1) / Q;
+        const int n_sys = has_sys(p.mode) ? p.R_sys : 0, n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
+        const size_t sys0 = sys_slot(p, 0, r, h), sys_st = (size_t)p.max_q_total * p.H;
+        const size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col;
+        auto slot = [&](int j) { return j < n_sys ? sys0 + j * sys_st : ctx0 + (size_t)(j - n_sys) * a.nc; };
+        // this warp's parts: part, part + WPR, ...
+        const int mine = (n_parts - part + WPR - 1) / WPR;
+        for (int j0 = 0; j0 < mine; j0 += 32) {
+            const int cnt = min(32, mine - j0);
+            const float lk = lane < cnt ? __ldcg(p.part_lse + slot((j0 + lane) * WPR + part)) : kNegInf;
             float x[CH][V];
+            auto load = [&](int k0) {
 #pragma unroll
-            for (int k = 0; k < CH; k++) {
-                if (k0 + k < cnt) {
-                    const float *src = p.part_o + slot(j0 + k0 + k) * D + d0;
-                    if constexpr (V == 4) {
-                        const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
-                        x[k][0] = t.x; x[k][1] = t.y; x[k][2] = t.z; x[k][3] = t.w;
-                    } else {
-                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
-                        x[k][0] = t.x; x[k][1] = t.y;
+                for (int k = 0; k < CH; k++) {
+                    if (k0 + k < cnt) {
+                        const float *src = p.part_o + slot((j0 + k0 + k) * WPR + part) * D + d0;
+                        if constexpr (V == 4) {
+                            const float4 t = __ldcg(reinterpret_cast<const float4 *>(src));
+                            x[k][0] = t.x; x[k][1] = t.y; x[k][2] = t.z; x[k][3] = t.w;
+                        } else {
+                            const float2 t = __ldcg(reinterpret_cast<const float2 *>(src));
+                            x[k][0] = t.x; x[k][1] = t.y;
+                        }
                     }
                 }
-            }
+            };
+            load(0);      // with the log-sum-exps: one round trip
+            float mk = lk;
 #pragma unroll
-            for (int k = 0; k < CH; k++) {
-                const float wt = __shfl_sync(0xffffffffu, wk, (k0 + k) & 31);
-                if (k0 + k < cnt) {
-                    W += wt;
+            for (int off = 16; off > 0; off >>= 1) mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, off));
+            const float Mn = fmaxf(M, mk), mu = Mn == kNegInf ? 0.f : Mn, al = ex2(M - mu), wk = ex2(lk - mu);
+            M = Mn;
+            W *= al;
 #pragma unroll
-                    for (int e = 0; e < V; e++) acc[e] += wt * x[k][e];
+            for (int k = 0; k < V; k++) acc[k] *= al;
+            for (int k0 = 0; k0 < cnt; k0 += CH) {
+                if (k0 > 0) load(k0);
+#pragma unroll
+                for (int k = 0; k < CH; k++) {
+                    const float wt = __shfl_sync(0xffffffffu, wk, (k0 + k) & 31);
+                    if (k0 + k < cnt) {
+                        W += wt;
+#pragma unroll
+                        for (int e = 0; e < V; e++) acc[e] += wt * x[k][e];
+                    }
                 }
             }
         }
     }
+    if constexpr (WPR > 1) {
+        if (lane == 0) {
+            sm_m[warp] = M;
+            sm_w[warp] = W;
+        }
+#pragma unroll
+        for (int k = 0; k < V; k++) sm_acc[warp][d0 + k] = acc[k];
+        __syncthreads();
+        if (part > 0) return;
+        float top = M;
+#pragma unroll
+        for (int k = 1; k < WPR; k++) top = fmaxf(top, sm_m[warp + k]);
+        const float mu = top == kNegInf ? 0.f : top, al = ex2(M - mu);
+        W *= al;
+#pragma unroll
+        for (int e = 0; e < V; e++) acc[e] *= al;
+#pragma unroll
+        for (int k = 1; k < WPR; k++) {
+            const float ak = ex2(sm_m[warp + k] - mu);
+            W += sm_w[warp + k] * ak;
+#pragma unroll
+            for (int e = 0; e < V; e++) acc[e] += sm_acc[warp + k][d0 + e] * ak;
+        }
+        M = top;
+    }
+    if (!live) return;
     const float inv = W == 0.f ? 0.f : 1.f / W;
     const float lse = W == 0.f ? kNegInf : (M + lg2(W)) * kLn2;
     const size_t orow = ((size_t)b * p.Lq + i) * p.H + h;

@@ -1073,11 +1073,21 @@ constexpr int kQ4MaxWarps = 16;       // warps of a context CTA, at most
 PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
 {
     PlanQ4 pl;
-    pl.sys = make_plan(d, mode, sms);
+    const int G = d->H / kv_heads(d);
+    relay_dims_t ds = *d;
+    const long long rows_v = (long long)(d->max_q_total > 0 ? d->max_q_total : d->B * d->Lq) * G;
+    if (mode == MODE_FUSED && d->Ls > 0 && d->sys_range == 0 && !(d->D == 128 && rows_v > kTcMinRows)) {
+        // the prompt's items beside the contexts: a team each on half the SMs
+        // (there is no other work for the teams of such a CTA), but ranges of
+        // at least 128 keys
+        const long long tiles = (rows_v + kTileM - 1) / kTileM;
+        const long long want = std::max(1ll, (long long)sms / (kv_heads(d) * tiles));
+        ds.sys_range = std::max(128, round_up((int)((d->Ls + want - 1) / want), kTileK));
+    }
+    pl.sys = make_plan(&ds, mode, sms);
     pl.sys.ctx_tc = false;
     pl.sys.ctx_pairs = 0;
     pl.sys.n_tc_ctx = 0;
-    const int G = d->H / kv_heads(d);
     const long long cols = (long long)d->Lq * G, tiles = cols <= 8 ? 1 : (cols + 15) / 16;
     const long long seqs = kv_heads(d) * std::min((long long)d->B * tiles, (long long)pl.sys.Mtot * G / 16 + d->B);
     pl.nc = (int)std::min(cols, cols <= 8 ? 8ll : 16ll);
@@ -1101,7 +1111,9 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     if (ws_bytes < make_plan_q4(d, mode, 1).total) return RELAY_ERR_WORKSPACE;
     if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1).Mtot) return RELAY_ERR_INVALID_ARG;
     const long long cols = (long long)d->Lq * (d->H / kv_heads(d));
-    if ((double)kv_heads(d) * ((cols + 7) / 8) * d->max_blocks_per_seq > INT_MAX) return RELAY_ERR_UNSUPPORTED;
+    if ((double)kv_heads(d) * ((cols + 7) / 8) * d->max_blocks_per_seq > INT_MAX ||
+        (double)d->num_blocks * kv_heads(d) > INT_MAX)
+        return RELAY_ERR_UNSUPPORTED;
     const DevInfo *dev = nullptr;
     relay_status_t st = device_info(&dev);
     if (st != RELAY_OK) return st;
@@ -1132,9 +1144,13 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
         st = launch_tc(d, mode, p, pl.sys, dev, s);
         if (st != RELAY_OK) return st;
         front = true;
+        a.queue = 1;
     } else if (mode == MODE_FUSED && p.R_sys > 0) {
         const int kg = p.q_lens || d->Lq != 1 ? 0 : row_class(d, pl.sys, MODE_SYS, p.G, false);
-        prompt_kernel(d->D, kg)<<<dev->sms, kThreads, d->D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>), s>>>(p);
+        const long long items = (long long)p.Hkv * (((long long)p.max_q_total * p.G + kTileM - 1) / kTileM) * p.R_sys;
+        const int grid = (int)std::min<long long>((items + kTeams - 1) / kTeams, dev->sms);
+        a.queue = grid < dev->sms;
+        prompt_kernel(d->D, kg)<<<grid, kThreads, d->D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>), s>>>(p);
         if (cudaGetLastError() != cudaSuccess) return RELAY_ERR_CUDA;
         front = true;
     }
@@ -1151,11 +1167,15 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     cfg.numAttrs = front ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, a);
     if (e == cudaSuccess) {
-        cfg.gridDim = dim3((unsigned)(((long long)p.max_q_total * d->H + 7) / 8));
+        const long long rows = (long long)p.max_q_total * d->H;
+        const bool shared = rows <= 32ll * dev->sms;      // (row, head) pairs: fewer than the GPU holds warps
+        cfg.gridDim = dim3((unsigned)(shared ? (rows + 1) / 2 : (rows + 7) / 8));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
-        e = d->D == 128 ? cudaLaunchKernelEx(&cfg, q4::merge_kernel<128>, a) : cudaLaunchKernelEx(&cfg, q4::merge_kernel<64>, a);
+        void (*fn)(const q4::Args) = d->D == 128 ? (shared ? q4::merge_kernel<128, 4> : q4::merge_kernel<128, 1>)
+                                                 : (shared ? q4::merge_kernel<64, 4> : q4::merge_kernel<64, 1>);
+        e = cudaLaunchKernelEx(&cfg, fn, a);
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
