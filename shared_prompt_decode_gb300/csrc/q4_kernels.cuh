@@ -22,6 +22,7 @@
 #pragma once
 
 #include <cuda_fp16.h>
+#include <stddef.h>
 #include <stdint.h>
 
 #include "relay_kernels.cuh"
@@ -216,60 +217,73 @@ __device__ __forceinline__ int row_off(int row)
     const int line = row / kPerLine, pos = (row % kPerLine) * (D / 32);
     return line * 128 + ((pos ^ ((line & 3) << 1)) << 4);
 }
-// byte `byte` of a row (row_off)
+// byte `byte` of the row at row_off `row`
 __device__ __forceinline__ int byte_off(int row, int byte) { return (row ^ (byte & 0x70)) + (byte & 15); }
 
-// What a lane reads and copies in every page: offsets in the staged page, and
-// where its share of block 0 lies.
+// What a lane reads and copies in every page.  Its further rows are fixed
+// steps away: 8 rows are an exclusive or and a sum, the next row is an
+// exclusive or (D = 128: row 2t + 1 is the other half of row 2t's line).
 template <int D, int GROUP>
 struct Lane {
-    int k0, k1;                     // its K words: keys g, g + 8
-    int v[4];                       // its V words: keys 2t, 2t + 1, 2t + 8, 2t + 9
-    int sz;                         // the pairs of key g
+    using P = PageQ<D, GROUP>;
+    static constexpr int kXor8 = D == 128 ? 0 : 64, kAdd8 = D == 128 ? 512 : 256, kXor1 = D == 128 ? 64 : 32;
     int lane;
-    int to, sz_to, sz_at;           // copies: destinations, place among the pairs, sources
-    const unsigned char *kc, *vc, *szc;
-    bool copies_sz;
+    unsigned k0;                    // its K words of key g
+    unsigned v0;                    // its V words of key 2t
+    unsigned sz;                    // the pairs of key g
+    unsigned to;                    // its first copied chunk
+    unsigned long long at;          // that chunk's place among the block's codes
+    const unsigned char *szc;       // its chunk of the pairs of block 0
 
     __device__ __forceinline__ void init(const Pool &pool)
     {
-        using P = PageQ<D, GROUP>;
         asm volatile("mov.u32 %0, %%laneid;" : "=r"(lane));      // (kept, not read again)
         const int g = lane >> 2, t = lane & 3;
-        const int kb = t * (GROUP / 8), vb = 4 * (GROUP == 32 ? (g & 3) : g);
-        k0 = byte_off(row_off<D>(g), kb);
-        k1 = byte_off(row_off<D>(g + 8), kb);
-#pragma unroll
-        for (int k = 0; k < 4; k++) v[k] = P::kCodes + byte_off(row_off<D>(2 * t + (k & 1) + 8 * (k >> 1)), vb);
+        k0 = byte_off(row_off<D>(g), t * (GROUP / 8));
+        v0 = P::kCodes + byte_off(row_off<D>(2 * t), 4 * (GROUP == 32 ? (g & 3) : g));
         sz = 2 * P::kCodes + g * P::NG * 4;
         constexpr int kPerRow = P::kRow / 16, kChunks = P::kSz / 16;
         to = byte_off(row_off<D>(lane / kPerRow), 16 * (lane % kPerRow));
-        sz_to = 2 * P::kCodes + 16 * lane;
-        kc = pool.k + 16 * lane;
-        vc = pool.v + 16 * lane;
+        at = 16 * lane;
         szc = reinterpret_cast<const unsigned char *>(lane < kChunks ? pool.ksz : pool.vsz) + 16 * (lane % kChunks);
-        sz_at = 16 * (lane % kChunks);
-        copies_sz = lane < 2 * kChunks;
+    }
+    // address of its K words of key g + 8 r, of its V words of key 2t + (k & 1) + 8 (k >> 1), x bytes into the row
+    __device__ __forceinline__ unsigned k(unsigned st, int r, int x) const
+    {
+        return ((st + k0) ^ (unsigned)(r * kXor8 ^ x)) + r * kAdd8;
+    }
+    __device__ __forceinline__ unsigned v(unsigned st, int k, int x) const
+    {
+        return ((st + v0) ^ (unsigned)((k & 1) * kXor1 ^ (k >> 1) * kXor8 ^ x)) + (k >> 1) * kAdd8;
     }
 };
 
-// Shape of a CTA: warps, pages of a step (their keys share one round of the
-// softmax), steps in a warp's ring.  One CTA per SM.
-template <int D, int GROUP, int NT>
-struct Geo {
-#ifndef KPER
-#define KPER 2
-#endif
-    static constexpr int kPer = NT > 1 || (D == 128 && GROUP == 32) ? 2 : KPER;
-#ifndef KW
-#define KW 12
-#endif
-    static constexpr int kW = NT > 1 ? 8 : D == 128 ? (GROUP == 32 && KW > 12 ? 12 : KW) : 16;
-    static constexpr int kStep = kPer * PageQ<D, GROUP>::kPage;
-    static constexpr int kFit = 218 * 1024 / (kW * kStep);
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
-    static_assert(kStages >= 2, "ring");
-};
+__device__ __forceinline__ unsigned lds32(unsigned a)
+{
+    unsigned x;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(x) : "r"(a));
+    return x;
+}
+__device__ __forceinline__ uint2 lds64(unsigned a)
+{
+    uint2 x;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(x.x), "=r"(x.y) : "r"(a));
+    return x;
+}
+__device__ __forceinline__ uint4 lds128(unsigned a)
+{
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(a));
+    return x;
+}
+// 16 bytes from global to shared memory, the first n of them (the others
+// zero), where `go` is set: no branch
+__device__ __forceinline__ void copy16(unsigned to, const void *from, int n, bool go)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %3, 0;\n @p cp.async.cg.shared.global [%0], [%1], 16, %2; }" ::"r"(to),
+                 "l"(from), "r"(n), "r"((unsigned)go)
+                 : "memory");
+}
 
 // ----------------------------------------------------------------------------- attention: work
 // The context work as one line of pages: for every request, KV head and tile
@@ -285,22 +299,22 @@ struct Args {
     int q_min;                // pages of a chunk, at least
     int queue;                // every chunk from the queue (a grid in front has some of the SMs), else the first static
     long long part0;          // first partial row of the contexts
+    float slack;              // kSlack in units of q . k
 };
 
 // Handed from the context kernel to the merge kernel.
 struct Sched {
     int bad, Q;
     long long *pre;           // [B + 1] pages of the line before request b
-    int *qo, *seq, *nctx;     // [B + 1] query rows and sequences before it, [B] tokens
+    int *qo, *seq;            // [B + 1] query rows and sequences before it
 };
-__host__ __device__ inline size_t sched_bytes(int B) { return 16 + 8 * (size_t)(B + 1) + 4 * (size_t)(3 * B + 2); }
+__host__ __device__ inline size_t sched_bytes(int B) { return 16 + 8 * (size_t)(B + 1) + 4 * (size_t)(2 * B + 2); }
 __device__ __forceinline__ Sched sched_at(int *base, int B)
 {
     Sched s;
     s.pre = reinterpret_cast<long long *>(base + 4);
     s.qo = reinterpret_cast<int *>(s.pre + B + 1);
     s.seq = s.qo + B + 1;
-    s.nctx = s.seq + B + 1;
     return s;
 }
 
@@ -314,32 +328,66 @@ __host__ __device__ inline Cols cols_of(int ql, int G)
     Cols c;
     c.cols = ql * G;
     c.nt = c.cols > 8 ? 2 : 1;
-    c.tiles = (c.cols + 8 * c.nt - 1) / (8 * c.nt);
+    c.tiles = (c.cols + 8 * c.nt - 1) >> (2 + c.nt);
     return c;
 }
-
-struct Smem4 {
-    long long pre[kMaxB + 1];
-    long long warp_pre[16];
-    int qo[kMaxB + 1], seq[kMaxB + 1], nctx[kMaxB];
-    int warp_qo[16], warp_seq[16];
-    int bad;
-    alignas(128) unsigned char ring[16];      // (the launch gives it its size)
-};
 
 // One sequence, and a page of it.
 struct Seq {
     int b, hk, tile, id;      // id: over the whole batch
     int page, pages;
-    int n, ql;
-    Cols c;
+    int n, ql, tiles;
 };
+// A place in a chunk: the sequence, and the pages of the chunk from its page on.
+struct alignas(16) Walk {
+    Seq q;
+    int left;
+    __device__ __forceinline__ int take() const { return min(left, q.pages - q.page); }
+};
+// A sequence's share of a chunk, as its loads were opened.
+struct alignas(16) Share {
+    int b, hk, tile, part;
+    int page, end;            // pages to read
+    int n, ql;
+};
+constexpr int kMaxWarps = 16, kShares = 3;
+
+struct Smem4 {
+    long long pre[kMaxB + 1];
+    long long warp_pre[16];
+    int qo[kMaxB + 1], seq[kMaxB + 1];
+    int warp_qo[16], warp_seq[16];
+    int bad;
+    Walk walk[kMaxWarps];                     // where a warp's loads are
+    Share share[kMaxWarps][kShares];          // its shares that are open, oldest first
+    alignas(128) unsigned char ring[16];      // (the launch gives it its size)
+};
+
+// Shape of a CTA: warps, pages of a step (their keys share one round of the
+// softmax), steps in a warp's ring.  One CTA per SM.
+constexpr size_t kMaxSmem = 227 * 1024;
+template <int D, int GROUP, int NT>
+struct Geo {
+#ifndef KPER
+#define KPER 2
+#endif
+    static constexpr int kPer = NT > 1 || (D == 128 && GROUP == 32) ? 2 : KPER;
+#ifndef KW
+#define KW 12
+#endif
+    static constexpr int kW = NT > 1 ? 8 : D == 128 ? (GROUP == 32 && KW > 12 ? 12 : KW) : 16;
+    static constexpr int kStep = kPer * PageQ<D, GROUP>::kPage;
+    static constexpr int kFit = (int)((kMaxSmem - offsetof(Smem4, ring)) / (kW * kStep));
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static_assert(kStages >= 2, "ring");
+};
+
 __device__ __forceinline__ void set_request(const Params &p, const Smem4 &s, Seq &q, int b)
 {
     q.b = b;
-    q.n = s.nctx[b];
+    q.n = p.ctx_lens[b];      // (in range, or the call has ended)
     q.ql = s.qo[b + 1] - s.qo[b];
-    q.c = cols_of(q.ql, p.G);
+    q.tiles = cols_of(q.ql, p.G).tiles;
     q.pages = (q.n + kBlock - 1) / kBlock;
 }
 // the sequence at position f of the line
@@ -355,8 +403,8 @@ __device__ __forceinline__ Seq locate(const Params &p, const Smem4 &s, long long
     const unsigned rem = (unsigned)(f - s.pre[lo]);      // the host keeps a request below 2^31 pages
     const int at = (int)(rem / (unsigned)q.pages);
     q.page = (int)rem - at * q.pages;
-    q.hk = at / q.c.tiles;
-    q.tile = at - q.hk * q.c.tiles;
+    q.hk = q.tiles == 1 ? at : at / q.tiles;
+    q.tile = at - q.hk * q.tiles;
     q.id = s.seq[lo] + at;
     return q;
 }
@@ -365,7 +413,7 @@ __device__ __forceinline__ void advance(const Params &p, const Smem4 &s, Seq &q)
 {
     q.page = 0;
     q.id++;
-    if (++q.tile < q.c.tiles) return;
+    if (++q.tile < q.tiles) return;
     q.tile = 0;
     if (++q.hk < p.Hkv) return;
     q.hk = 0;
@@ -379,7 +427,9 @@ __device__ __forceinline__ int keys_seen(int n, int ql, int i) { return max(0, m
 // Pages that any column of the sequence sees.
 __device__ __forceinline__ int pages_seen(const Params &p, const Seq &q)
 {
-    const int last = min(q.c.cols, (q.tile + 1) * 8 * q.c.nt) - 1;
+    if (q.ql == 1) return q.pages;
+    const Cols c = cols_of(q.ql, p.G);
+    const int last = min(c.cols, (q.tile + 1) * 8 * c.nt) - 1;
     return (keys_seen(q.n, q.ql, last / p.G) + kBlock - 1) / kBlock;
 }
 
@@ -438,7 +488,6 @@ __device__ void build_line(const Params &p, Smem4 &s)
             s.qo[b] = bq;
             s.seq[b] = bs;
             s.pre[b] = bp;
-            s.nctx[b] = n[k];
         }
         bq += ql[k];
         bs += sq[k];
@@ -503,16 +552,16 @@ __device__ __forceinline__ void mma16816_first(float c[4], const unsigned a[4], 
 
 // the NG pairs of a token
 template <int NG>
-__device__ __forceinline__ void load_pairs(const unsigned char *at, __half2 (&h)[NG])
+__device__ __forceinline__ void load_pairs(unsigned at, __half2 (&h)[NG])
 {
     unsigned w[NG];
     if constexpr (NG == 1) {
-        w[0] = *reinterpret_cast<const unsigned *>(at);
+        w[0] = lds32(at);
     } else if constexpr (NG == 2) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(at);
+        const uint2 x = lds64(at);
         w[0] = x.x; w[1] = x.y;
     } else {
-        const uint4 x = *reinterpret_cast<const uint4 *>(at);
+        const uint4 x = lds128(at);
         w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
     }
 #pragma unroll
@@ -541,15 +590,15 @@ __device__ __forceinline__ int scale_exp(__half2 sz) { return ((__half_as_ushort
 __device__ __forceinline__ float scale_down(int e) { return __int_as_float((15 - e + 127) << 23); }
 
 template <int D, int GROUP, int NT>
-__device__ __forceinline__ void load_q(const Params &p, const Seq &s, unsigned (&qb)[NT][D / 16][2])
+__device__ __forceinline__ void load_q(const Params &p, int lane, const Share &s, int cols, unsigned (&qb)[NT][D / 16][2])
 {
     constexpr int WPG = GROUP / 32;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int nt = 0; nt < NT; nt++) {
         const int v = s.tile * 8 * NT + 8 * nt + g;
-        const bool has = v < s.c.cols;
-        const int i = has ? v / p.G : 0, c = has ? v - i * p.G : 0;
+        const bool has = v < cols;
+        const int i = s.ql == 1 || !has ? 0 : v / p.G, c = has ? v - i * p.G : 0;
         const __half *q = p.q + (((size_t)s.b * p.Lq + i) * p.H + s.hk * p.G + c) * D;
 #pragma unroll
         for (int w = 0; w < D / 32; w++) {
@@ -584,33 +633,46 @@ __device__ __forceinline__ void q_sums(const unsigned (&qb)[NT][D / 16][2], Vec<
         }
 }
 
-// One lane's share of staging one page: `rows` valid tokens.  The codes are
-// copied whole (what lies behind the last token is a number either way); the
-// pairs of further tokens read as zero, so that nothing of them is left.  A
-// block id outside the pool is flagged and reads as zero.
+// One lane's share of staging one page (where `go` is set): `rows` valid
+// tokens.  The codes are copied whole (what lies behind the last token is a
+// number either way); the pairs of further tokens read as zero, so that
+// nothing of them is left.  A block id of -1 (block_ids) reads as zero.
 template <int D, int GROUP>
-__device__ __forceinline__ void load_page(const Params &p, const Lane<D, GROUP> &ln, unsigned char *st, int blk, int hk,
-                                          int rows)
+__device__ __forceinline__ void load_page(const Params &p, const Pool &pool, const Lane<D, GROUP> &ln, unsigned st, int blk,
+                                          int hk, int rows, bool go)
 {
     using P = PageQ<D, GROUP>;
-    const bool ok = (unsigned)blk < (unsigned)p.num_blocks;
-    const unsigned page = (ok ? blk : 0) * p.Hkv + hk;      // the host keeps the pool below 2^31 of them
-    const unsigned char *kc = ln.kc + (size_t)page * P::kCodes, *vc = ln.vc + (size_t)page * P::kCodes;
-    const unsigned char *szc = ln.szc + (size_t)page * P::kSz;
-    if (!ok && ln.lane == 0) atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
+    const int all = blk >= 0 ? 16 : 0;
+    const unsigned page = max(blk, 0) * p.Hkv + hk;      // the host keeps the pool below 2^31 of them
+    const unsigned long long off = (unsigned long long)page * P::kCodes + ln.at;
+    const unsigned char *kc = pool.k + off, *vc = pool.v + off;
+    const unsigned to = st + ln.to;
 #pragma unroll
     for (int k = 0; k < P::kCodes / 512; k++) {
-        cp_async16(st + ln.to + 512 * k, kc + 512 * k, ok);
-        cp_async16(st + P::kCodes + ln.to + 512 * k, vc + 512 * k, ok);
+        copy16(to + 512 * k, kc + 512 * k, all, go);
+        copy16(to + P::kCodes + 512 * k, vc + 512 * k, all, go);
     }
-    const int n = ok ? min(16, max(0, rows * P::NG * 4 - ln.sz_at)) : 0;
-    if (ln.copies_sz)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(st + ln.sz_to)), "l"(szc), "r"(n));
+    constexpr int kChunks = P::kSz / 16;      // of K, then of V
+    const int n = min(all, max(0, rows * P::NG * 4 - 16 * (ln.lane % kChunks)));
+    copy16(st + 2 * P::kCodes + 16 * ln.lane, ln.szc + (unsigned long long)page * P::kSz, n, go && ln.lane < 2 * kChunks);
+}
+// Lane j's entry of a table, one outside the pool flagged and -1.
+__device__ __forceinline__ int block_id(const Params &p, const int *table, int at, int end)
+{
+    int blk = 0;
+    if (at < end) {
+        blk = table[at];
+        if ((unsigned)blk >= (unsigned)p.num_blocks) {
+            atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
+            blk = -1;
+        }
+    }
+    return blk;
 }
 
 // S^T = K q of one staged page, a group at a time: keys g, g + 8.
 template <int D, int GROUP, int NT, int E>
-__device__ __forceinline__ void page_scores(const unsigned char *st, const Lane<D, GROUP> &ln, const unsigned (&qb)[NT][D / 16][2],
+__device__ __forceinline__ void page_scores(unsigned st, const Lane<D, GROUP> &ln, const unsigned (&qb)[NT][D / 16][2],
                                             const Vec<E> (&qs)[NT][D / GROUP], Vec<E> (&sc)[NT][2])
 {
     using P = PageQ<D, GROUP>;
@@ -621,21 +683,18 @@ __device__ __forceinline__ void page_scores(const unsigned char *st, const Lane<
 #pragma unroll
     for (int gi = 0; gi < NG; gi++) {
         unsigned w0[WPG], w1[WPG];
-        const int x0 = gi * (GROUP / 2);      // group gi's bytes: an exclusive or away (a power of two below a line)
-        const unsigned char *r0 = st + (ln.k0 ^ x0), *r1 = st + (ln.k1 ^ x0);
+        const unsigned r0 = ln.k(st, 0, gi * (GROUP / 2)), r1 = ln.k(st, 1, gi * (GROUP / 2));
         if constexpr (WPG == 4) {
-            const uint4 x = *reinterpret_cast<const uint4 *>(r0);
-            const uint4 y = *reinterpret_cast<const uint4 *>(r1);
+            const uint4 x = lds128(r0), y = lds128(r1);
             w0[0] = x.x; w0[1] = x.y; w0[2] = x.z; w0[3] = x.w;
             w1[0] = y.x; w1[1] = y.y; w1[2] = y.z; w1[3] = y.w;
         } else if constexpr (WPG == 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(r0);
-            const uint2 y = *reinterpret_cast<const uint2 *>(r1);
+            const uint2 x = lds64(r0), y = lds64(r1);
             w0[0] = x.x; w0[1] = x.y;
             w1[0] = y.x; w1[1] = y.y;
         } else {
-            w0[0] = *reinterpret_cast<const unsigned *>(r0);
-            w1[0] = *reinterpret_cast<const unsigned *>(r1);
+            w0[0] = lds32(r0);
+            w1[0] = lds32(r1);
         }
         float lo[NT][4], hi[NT][4];
 #pragma unroll
@@ -674,7 +733,7 @@ __device__ __forceinline__ void page_scores(const unsigned char *st, const Lane<
 // their group, so with GROUP = 32 (four words) the two halves of the rows take
 // the same word at positions 8 bits apart.
 template <int D, int GROUP, int NT>
-__device__ __forceinline__ void page_values(const unsigned char *st, const Lane<D, GROUP> &ln, const unsigned (&pb)[NT][D / GROUP][2],
+__device__ __forceinline__ void page_values(unsigned st, const Lane<D, GROUP> &ln, const unsigned (&pb)[NT][D / GROUP][2],
                                             float (&o)[NT][D / 16][4], float (&c8)[NT][D / GROUP][4])
 {
     using P = PageQ<D, GROUP>;
@@ -689,7 +748,7 @@ __device__ __forceinline__ void page_values(const unsigned char *st, const Lane<
     for (int h = 0; h < D / kHalf; h++) {
         unsigned w[4];
 #pragma unroll
-        for (int k = 0; k < 4; k++) w[k] = *reinterpret_cast<const unsigned *>(st + (ln.v[k] ^ (h * (kHalf / 2))));
+        for (int k = 0; k < 4; k++) w[k] = lds32(ln.v(st, k, h * (kHalf / 2)));
         unsigned x0 = __byte_perm(w[0], w[1], 0x5410), y0 = __byte_perm(w[0], w[1], 0x7632);
         unsigned x1 = __byte_perm(w[2], w[3], 0x5410), y1 = __byte_perm(w[2], w[3], 0x7632);
         const int gi = h * kHalf / GROUP;
@@ -723,7 +782,7 @@ __device__ __forceinline__ void page_values(const unsigned char *st, const Lane<
 // One warp, KP staged pages of one sequence that every column sees whole
 // (FULL), or np <= KP of which the lane's columns see end[nt][e] keys.
 template <int D, int GROUP, int NT, int E, int KP, bool FULL>
-__device__ __forceinline__ void step(const unsigned char *st, const Lane<D, GROUP> &ln, int np,
+__device__ __forceinline__ void step(unsigned st, const Lane<D, GROUP> &ln, int np,
                                      const unsigned (&qb)[NT][D / 16][2], const Vec<E> (&qs)[NT][D / GROUP],
                                      State<D, GROUP, NT, E> &s, const int (&end)[NT][E], float scale_log2, float slack)
 {
@@ -858,11 +917,10 @@ __device__ __forceinline__ void step(const unsigned char *st, const Lane<D, GROU
 // Writes the partial of a sequence: normalised output and log2-sum-exp per
 // column, rows pr + column.
 template <int D, int GROUP, int NT, int E>
-__device__ __forceinline__ void write_partial(const Args &a, const Seq &q, State<D, GROUP, NT, E> &s, size_t pr0)
+__device__ __forceinline__ void write_partial(const Args &a, int lane, int nv, State<D, GROUP, NT, E> &s, size_t pr0)
 {
     constexpr int NG = D / GROUP;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int nv = min(8 * NT, q.c.cols - q.tile * 8 * NT);
+    const int g = lane >> 2, t = lane & 3;
     const float up = __int_as_float((24 + s.e - 15 + 127) << 23);      // 2^24 / scale_down
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
@@ -877,7 +935,7 @@ __device__ __forceinline__ void write_partial(const Args &a, const Seq &q, State
             const int c = 8 * nt + 2 * t + e;
             if (c >= nv) continue;
             const size_t pr = pr0 + c;
-            const float L = s.l[nt][e], inv = L == 0.f ? 0.f : 1.f / L;      // (a NaN goes on)
+            const float L = s.l[nt][e], inv = L == 0.f ? 0.f : __fdividef(1.f, L);      // (a NaN goes on)
             const float f0 = up * inv, f1 = f0 * 0.0625f;
             float *po = a.p.part_o + pr * D;
             if constexpr (GROUP == 32) {
@@ -923,98 +981,102 @@ struct Chunks {
     __device__ __forceinline__ long long take() const { return queue0 + __shfl_sync(0xffffffffu, ticket, 0); }
 };
 
-// Position in a chunk: the current sequence and the pages behind its share.
-struct Walk {
-    Seq q;
-    int left;               // pages of the chunk from the sequence's page on
-
-    __device__ __forceinline__ void start(const Params &p, const Smem4 &s, const Chunks &ch, long long c)
-    {
-        q = locate(p, s, c * ch.Q);
-        left = (int)min((long long)ch.Q, ch.total - c * ch.Q);
-    }
-    __device__ __forceinline__ int take() const { return min(left, q.pages - q.page); }
-    __device__ __forceinline__ void next(const Params &p, const Smem4 &s)
-    {
-        left -= take();
-        if (left > 0) advance(p, s, q);
-    }
-};
-
 // The pages in the order of the line, fetched a few steps ahead of the
-// arithmetic, across the ends of sequences and chunks.
+// arithmetic, across the ends of sequences and chunks.  What only the end of a
+// share needs is kept in shared memory.
 template <int D, int GROUP, int KP, int STAGES>
 struct Loader {
     using P = PageQ<D, GROUP>;
-    Walk w;
-    long long ahead;            // the warp's next chunk, once taken from the queue (else -1)
-    int page, end;              // next page, end of the sequence's share
+    int page, end, hk, n;       // the open share: next page, its end, KV head, tokens
     int blk, window;            // lane j: block of page window + j
-    int slot;                   // ring slot of the next step
+    const int *table;
+    unsigned at;                // ring place of the next step
     int issued;                 // steps staged so far
+    int opened;                 // shares opened so far
+    long long chunk;            // (its number, for the partials)
 
-    __device__ __forceinline__ const int *table(const Params &p) const { return p.block_tables + (size_t)w.q.b * p.max_blocks; }
-    __device__ __forceinline__ void enter(const Params &p, int lane)
+    // Opens the warp's next share, if there is one and room for it.
+    __device__ __forceinline__ bool open(const Args &a, Smem4 &s, int lane, int warp, Chunks &ch, int closed)
     {
-        page = w.q.page;
-        end = min(page + w.take(), pages_seen(p, w.q));
+        if (opened - closed >= kShares) return false;
+        Walk w = s.walk[warp];
+        if (w.left <= 0) {
+            chunk = ch.take();
+            if (chunk >= ch.count) return false;
+            ch.ask(a.p);
+            w.q = locate(a.p, s, chunk * ch.Q);
+            w.left = (int)min((long long)ch.Q, ch.total - chunk * ch.Q);
+        }
+        Share sh;
+        sh.b = w.q.b;
+        sh.hk = w.q.hk;
+        sh.tile = w.q.tile;
+        sh.part = (int)(chunk + w.q.id);
+        sh.n = w.q.n;
+        sh.ql = w.q.ql;
+        const int take = w.take();
+        sh.page = w.q.page;
+        sh.end = min(sh.page + take, pages_seen(a.p, w.q));
+        page = sh.page;
+        end = sh.end;
+        hk = sh.hk;
+        n = w.q.n;
+        table = a.p.block_tables + (size_t)sh.b * a.p.max_blocks;
         window = page;
-        blk = page + lane < end ? table(p)[page + lane] : 0;
+        blk = block_id(a.p, table, page + lane, end);
+        w.left -= take;
+        if (w.left > 0) advance(a.p, s, w.q);
+        __syncwarp();
+        if (lane == 0) {
+            s.walk[warp] = w;
+            s.share[warp][opened % kShares] = sh;
+        }
+        __syncwarp();
+        opened++;
+        return true;
     }
     // Stages the warp's next steps, a cp.async group each, until the ring is
-    // full (`done` steps have left it) or nothing is left to stage.
-    __device__ __forceinline__ void fill(const Args &a, const Smem4 &s, const Lane<D, GROUP> &ln, const Chunks &ch,
-                                         unsigned char *ring, int done)
+    // full (`done` steps have left it) or nothing is left to stage (`closed`
+    // shares are done).
+    __device__ __forceinline__ void fill(const Args &a, Smem4 &s, const Lane<D, GROUP> &ln, int warp, Chunks &ch, unsigned ring,
+                                         int done, int closed)
     {
-        const int lane = ln.lane;
         while (issued - done < STAGES - 1) {
-            while (page >= end) {
-                if (w.left > 0) w.next(a.p, s);
-                if (w.left <= 0) {
-                    if (ahead >= 0) return;            // one chunk ahead at most
-                    ahead = ch.take();
-                    if (ahead >= ch.count) return;
-                    w.start(a.p, s, ch, ahead);
-                }
-                enter(a.p, lane);
+            if (page >= end) {
+                if (!open(a, s, ln.lane, warp, ch, closed)) return;
+                continue;      // (it may have no page to read)
             }
-            unsigned char *st = ring + slot * (KP * P::kPage);
+            static_assert(32 % KP == 0, "a step's blocks are in one window");
+            if (page >= window + 32) {
+                window = page;
+                blk = block_id(a.p, table, window + ln.lane, end);
+            }
 #pragma unroll
-            for (int j = 0; j < KP; j++) {
-                if (page + j < end) {
-                    if (page + j >= window + 32) {
-                        window = page + j;
-                        blk = window + lane < end ? table(a.p)[window + lane] : 0;
-                    }
-                    load_page<D, GROUP>(a.p, ln, st + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window), w.q.hk,
-                                        w.q.n - (page + j) * kBlock);
-                }
-            }
+            for (int j = 0; j < KP; j++)
+                load_page<D, GROUP>(a.p, a.pool, ln, at + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window), hk,
+                                    n - (page + j) * kBlock, j == 0 || page + j < end);
             page += KP;
-            slot = slot + 1 == STAGES ? 0 : slot + 1;
+            at = at + KP * P::kPage == ring + STAGES * KP * P::kPage ? ring : at + KP * P::kPage;
             issued++;
             cp_async_commit();
         }
     }
 };
 
-// One sequence's share of the chunk: its steps are in the ring or come.
+// One share: its steps are in the ring or come.
 template <int D, int GROUP, int NT, int E, int KP, int STAGES>
-__device__ __forceinline__ void run_share(const Args &a, const Smem4 &sm, const Lane<D, GROUP> &ln, const Chunks &ch,
-                                          unsigned char *ring, Loader<D, GROUP, KP, STAGES> &ld, int &slot, int &done,
-                                          const Seq &q, int take, size_t part)
+__device__ __forceinline__ void run_share(const Args &a, Smem4 &sm, const Lane<D, GROUP> &ln, int warp, Chunks &ch, unsigned ring,
+                                          Loader<D, GROUP, KP, STAGES> &ld, unsigned &at, int &done, int closed, const Share sh)
 {
     using P = PageQ<D, GROUP>;
     const Params &p = a.p;
-    const int t = ln.lane & 3;
-    const int end_page = min(q.page + take, pages_seen(p, q));
+    const int n = sh.n, ql = sh.ql, cols = ql * p.G;
     unsigned qb[NT][D / 16][2];
     Vec<E> qs[NT][D / GROUP];
-    load_q<D, GROUP, NT>(p, q, qb);
+    load_q<D, GROUP, NT>(p, ln.lane, sh, cols, qb);
     q_sums<D, GROUP, NT, E>(qb, qs);
-    const int v0 = q.tile * 8 * NT, vlast = min(q.c.cols, v0 + 8 * NT) - 1;
-    const int all = keys_seen(q.n, q.ql, v0 / p.G);      // the first row sees least
-    const float slack = kSlack / p.scale_log2;
+    const int v0 = sh.tile * 8 * NT;
+    const int all = ql == 1 ? n : keys_seen(n, ql, v0 / p.G);      // the first row sees least
     State<D, GROUP, NT, E> s;
     s.e = 0;
 #pragma unroll
@@ -1031,29 +1093,30 @@ __device__ __forceinline__ void run_share(const Args &a, const Smem4 &sm, const 
             for (int d = 0; d < D / 16; d++) s.o[nt][d][e] = 0.f;
         }
     }
-    for (int page = q.page; page < end_page; page += KP) {
+    // pages that end below this are seen whole by every column
+    const int full_end = min(sh.end, all / kBlock);
+    for (int page = sh.page; page < sh.end; page += KP) {
         // the ring is full but at the end of the warp's work
         if (ld.issued - done == STAGES - 1) cp_async_wait<STAGES - 2>();
         else cp_async_wait<0>();
         __syncwarp();
-        const int key0 = page * kBlock;
-        const unsigned char *st = ring + slot * (KP * P::kPage);
         int end[NT][E];
-        if (page + KP <= end_page && key0 + KP * kBlock <= all) {
-            step<D, GROUP, NT, E, KP, true>(st, ln, KP, qb, qs, s, end, p.scale_log2, slack);
+        if (page + KP <= full_end) {
+            step<D, GROUP, NT, E, KP, true>(at, ln, KP, qb, qs, s, end, p.scale_log2, a.slack);
         } else {
+            const int t = ln.lane & 3, vlast = min(cols, v0 + 8 * NT) - 1;
 #pragma unroll
             for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                 for (int e = 0; e < E; e++)
-                    end[nt][e] = keys_seen(q.n, q.ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G) - key0;
-            step<D, GROUP, NT, E, KP, false>(st, ln, end_page - page, qb, qs, s, end, p.scale_log2, slack);
+                    end[nt][e] = (ql == 1 ? n : keys_seen(n, ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G)) - page * kBlock;
+            step<D, GROUP, NT, E, KP, false>(at, ln, sh.end - page, qb, qs, s, end, p.scale_log2, a.slack);
         }
         __syncwarp();
-        slot = slot + 1 == STAGES ? 0 : slot + 1;
-        ld.fill(a, sm, ln, ch, ring, ++done);
+        at = at + KP * P::kPage == ring + STAGES * KP * P::kPage ? ring : at + KP * P::kPage;
+        ld.fill(a, sm, ln, warp, ch, ring, ++done, closed);
     }
-    write_partial<D, GROUP, NT, E>(a, q, s, a.part0 + part * a.nc);
+    write_partial<D, GROUP, NT, E>(a, ln.lane, min(8 * NT, cols - v0), s, a.part0 + (long long)sh.part * a.nc);
 }
 
 // ----------------------------------------------------------------------------- attention: kernels
@@ -1079,7 +1142,10 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     // do not start together), then two or three: finer ones balance better,
     // and cost partials
     const long long per = (total + workers - 1) / workers;
-    const int parts = per <= 24 ? 1 + a.queue : 2 + a.queue;
+#ifndef PARTS
+#define PARTS (per <= 24 ? 1 + a.queue : 2 + a.queue)
+#endif
+    const int parts = PARTS;
     const int Q = (int)max((long long)a.q_min, (total + workers * parts - 1) / (workers * parts));
     const unsigned bad = (unsigned)s.bad | (s.qo[p.B] > p.max_q_total ? FLAG_Q_TOTAL : 0u);
     if (blockIdx.x == 0) {
@@ -1088,7 +1154,6 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
             sc.pre[k] = s.pre[k];
             sc.qo[k] = s.qo[k];
             sc.seq[k] = s.seq[k];
-            if (k < p.B) sc.nctx[k] = s.nctx[k];
         }
         if (threadIdx.x == 0) {
             p.sched[0] = bad ? -1 : 0;
@@ -1102,41 +1167,30 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     ch.queue0 = a.queue ? 0 : workers;
     ch.Q = Q;
     if (!bad && first < ch.count) {
-        unsigned char *ring = s.ring + warp * (G::kStages * G::kStep);
+        const unsigned ring = smem_u32(s.ring) + warp * (G::kStages * G::kStep);
         Lane<D, GROUP> ln;
         ln.init(a.pool);
         ch.ask(p);
-        Walk w;
-        w.start(p, s, ch, first);
+        if (ln.lane == 0) {
+            Walk w;
+            w.q = locate(p, s, first * Q);
+            w.left = (int)min((long long)Q, total - first * Q);
+            s.walk[warp] = w;
+        }
+        __syncwarp();
         Loader<D, GROUP, G::kPer, G::kStages> ld;
-        ld.w = w;
-        ld.ahead = -1;
-        ld.slot = ld.issued = 0;
-        ld.enter(p, ln.lane);
-        int slot = 0, done = 0;
-        for (long long c = first;;) {
-            ld.fill(a, s, ln, ch, ring, done);
-            for (;;) {
-                const size_t part = (size_t)(c + w.q.id);
-                if (NT > 1 && w.q.c.nt > 1)
-                    run_share<D, GROUP, NT, E>(a, s, ln, ch, ring, ld, slot, done, w.q, w.take(), part);
-                else
-                    run_share<D, GROUP, 1, E>(a, s, ln, ch, ring, ld, slot, done, w.q, w.take(), part);
-                w.next(p, s);
-                if (w.left <= 0) break;
-            }
-            // the next chunk: the one the loader is ahead in, or (it never
-            // came to this one's end, which has no page to read) a new one
-            const bool in = ld.ahead >= 0;
-            c = in ? ld.ahead : ch.take();
-            if (c >= ch.count) break;
-            w.start(p, s, ch, c);
-            ch.ask(p);
-            ld.ahead = -1;
-            if (!in) {
-                ld.w = w;
-                ld.enter(p, ln.lane);
-            }
+        ld.chunk = first;
+        ld.page = ld.end = ld.issued = ld.opened = 0;
+        ld.at = ring;
+        unsigned at = ring;
+        for (int done = 0, closed = 0;; closed++) {
+            ld.fill(a, s, ln, warp, ch, ring, done, closed);
+            if (ld.opened == closed) break;      // no share is left
+            const Share sh = s.share[warp][closed % kShares];
+            if (NT > 1 && sh.ql * p.G > 8)
+                run_share<D, GROUP, NT, E>(a, s, ln, warp, ch, ring, ld, at, done, closed, sh);
+            else
+                run_share<D, GROUP, 1, E>(a, s, ln, warp, ch, ring, ld, at, done, closed, sh);
         }
         cp_async_wait<0>();
     }
@@ -1220,7 +1274,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
         live = b < p.B;
         if (!live) b = 0;
     }
-    const int bad = __ldcg(p.sched), Q = __ldcg(p.sched + 1), n = __ldcg(sc.nctx + b), seq = __ldcg(sc.seq + b);
+    const int bad = __ldcg(p.sched), Q = __ldcg(p.sched + 1), n = __ldg(p.ctx_lens + b), seq = __ldcg(sc.seq + b);
     const long long pre = __ldcg(sc.pre + b);
     live = live && bad >= 0;
     float M = kNegInf, W = 0.f, acc[V];
@@ -1231,7 +1285,14 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
         const int hk = h / p.G, v = i * p.G + h - hk * p.G, tile = v / (8 * c.nt), col = v - tile * 8 * c.nt;
         const int pages = (n + kBlock - 1) / kBlock, at = hk * c.tiles + tile;
         const long long f = pre + (long long)at * pages;
-        const long long c0 = f / Q, c1 = (f + pages - 1) / Q;
+        long long c0, c1;      // its chunks
+        if (f + pages <= 0xffffffffll) {
+            c0 = (unsigned)f / (unsigned)Q;
+            c1 = (unsigned)(f + pages - 1) / (unsigned)Q;
+        } else {
+            c0 = f / Q;
+            c1 = (f + pages - 1) / Q;
+        }
         const int n_sys = has_sys(p.mode) ? p.R_sys : 0, n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
         const size_t sys0 = sys_slot(p, 0, r, h), sys_st = (size_t)p.max_q_total * p.H;
         const size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col;

@@ -1081,7 +1081,10 @@ PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
         // (there is no other work for the teams of such a CTA), but ranges of
         // at least 128 keys
         const long long tiles = (rows_v + kTileM - 1) / kTileM;
-        const long long want = std::max(1ll, (long long)sms / (kv_heads(d) * tiles));
+        #ifndef WANTMUL
+#define WANTMUL 2
+#endif
+        const long long want = std::max(1ll, WANTMUL * (long long)sms / (kv_heads(d) * tiles));
         ds.sys_range = std::max(128, round_up((int)((d->Ls + want - 1) / want), kTileK));
     }
     pl.sys = make_plan(&ds, mode, sms);
@@ -1137,6 +1140,7 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     a.nc = pl.nc;
     a.q_min = pl.q_min;
     a.part0 = (long long)pl.sys.dec_base;
+    a.slack = q4::kSlack / p.scale_log2;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     bool front = false;      // a grid of this call is in front of the context grid
@@ -1148,7 +1152,11 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     } else if (mode == MODE_FUSED && p.R_sys > 0) {
         const int kg = p.q_lens || d->Lq != 1 ? 0 : row_class(d, pl.sys, MODE_SYS, p.G, false);
         const long long items = (long long)p.Hkv * (((long long)p.max_q_total * p.G + kTileM - 1) / kTileM) * p.R_sys;
+#ifndef HALFGRID
+        const int grid = dev->sms;
+#else
         const int grid = (int)std::min<long long>((items + kTeams - 1) / kTeams, dev->sms);
+#endif
         a.queue = grid < dev->sms;
         prompt_kernel(d->D, kg)<<<grid, kThreads, d->D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>), s>>>(p);
         if (cudaGetLastError() != cudaSuccess) return RELAY_ERR_CUDA;
