@@ -29,6 +29,7 @@ Entry points (same names as the C ABI in include/relay.h):
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 from dataclasses import dataclass
@@ -551,10 +552,46 @@ def relay_rope(q, ctx_lens, Ls, k_new=None, q_lens=None, base=10000.0, workspace
 
 
 # ----------------------------------------------------------------------------- steps around the cache
-def _current(dev):
-    """The library launches on the current device: tensors of another one are refused, not reached from here."""
+# These calls are short on the device, so their checks are one pass over the
+# arguments (_at: the address of a tensor that is as it has to be); where
+# something is not, the checks are made again one by one for the message.
+_F16, _F32, _I32, _U8 = torch.float16, torch.float32, torch.int32, torch.uint8
+
+
+class _Mismatch(Exception):
+    pass
+
+
+def _at(t, dtype, shape, dev):
+    if t is None:
+        return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise _Mismatch
+
+
+def _explain(what, first, *args):
+    """Raises for the first of (name, tensor, dtype, shape) that is not as it has to be: shapes, then devices and
+    types; `first` names the tensor whose device the others have to be on."""
+    dev = None
+    for name, t, _, shape in args:
+        if t is not None:
+            _shape(t, name, shape)
+        if name == first:
+            dev = t.device
+    for name, t, dtype, _ in args:
+        if t is not None:
+            _need(t, name, dtype, None if name == first else dev)
     if dev.index != torch.cuda.current_device():
         raise ValueError(f"the tensors are on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    raise ValueError(f"{what}: arguments")
+
+
+def _raw_stream(stream, dev):
+    """The stream of a call: the library launches on the current device, which has to be the tensors'."""
+    if dev != torch.cuda.current_device():
+        raise _Mismatch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def _on_stream(stream, make, *args, **kw):
@@ -565,10 +602,18 @@ def _on_stream(stream, make, *args, **kw):
         return make(*args, **kw)
 
 
-def _small_workspace(workspace, dev, stream):
+def _workspace(workspace, dev, stream, make=torch.zeros, *args, **kw):
+    """The caller's workspace, or a new one (256 bytes, or what `make` makes)."""
     if workspace is None:
-        workspace = _on_stream(stream, torch.zeros, 256, dtype=torch.uint8, device=dev)
+        return _on_stream(stream, make, *args, **kw) if args else _on_stream(stream, make, 256, dtype=_U8, device=dev)
+    if workspace.dtype is not _U8 or workspace.get_device() != dev.index:
+        raise ValueError(f"workspace must be torch.uint8 on {dev}, got {workspace.dtype} on {workspace.device}")
     return workspace
+
+
+@functools.lru_cache(maxsize=1024)
+def _dims(B, Lq, H, D, Ls=0, num_blocks=0, max_blocks=0, Hkv=0):
+    return Dims(B, Lq, H, D, Ls, 16, num_blocks, max_blocks, 0, 0, 0, 0.0, Hkv)
 
 
 MAX_ROPE_AXES = 4
@@ -578,7 +623,11 @@ def rope_axis_map(sections, D, interleaved=False) -> bytes:
     """The axis of each of the D / 2 pairs of relay_rope_axes.  sections: pairs per axis, together D / 2; in runs
     (axis 0's pairs first), or interleaved: pair a + n k belongs to axis a (of n) for k < sections[a], a > 0, and
     every other pair to axis 0."""
-    sections = [int(x) for x in sections]
+    return _axis_map(tuple(int(x) for x in sections), D, bool(interleaved))
+
+
+@functools.lru_cache(maxsize=64)
+def _axis_map(sections, D, interleaved):
     half, n = D // 2, len(sections)
     if not 1 <= n <= MAX_ROPE_AXES or min(sections) < 0 or sum(sections) != half:
         raise ValueError(f"sections {sections} must be 1..{MAX_ROPE_AXES} counts that add up to {half}")
@@ -598,45 +647,35 @@ def relay_rope_axes(q, positions, Ls, sections, k_new=None, q_lens=None, base=10
     """Rotary embedding with one position per axis: q [B, Lq, H, D] (and k_new [B, Lq, Hkv, D]) at positions Ls +
     positions[a][b][i] ([n_axes, B, Lq] int32) for the pairs that `sections` (rope_axis_map) gives to axis a;
     `inverse` turns back.  In place, or into q_out / k_out.  Returns q_out, k_out."""
-    dev = q.device
     B, Lq, H, D = q.shape
-    q_out = q if q_out is None else q_out
-    k_out = k_new if k_out is None else k_out
-    if k_new is None and k_out is not None:
+    if q_out is None:
+        q_out = q
+    if k_out is None:
+        k_out = k_new
+    elif k_new is None:
         raise ValueError("k_out without k_new")
-    Hkv = H
-    if k_new is not None:
-        Hkv = k_new.shape[2] if k_new.dim() == 4 else 0
-        _shape(k_new, "k_new", (B, Lq, Hkv, D))
-        _same(k_out, k_new, ("k_out", "k_new"))
-    _shape(positions, "positions", (len(sections), B, Lq))
-    _shape(q_lens, "q_lens", (B,))
-    _same(q_out, q, ("q_out", "q"))
+    Hkv = H if k_new is None else k_new.shape[2] if k_new.dim() == 4 else 0
+    n = len(sections)
     axis = rope_axis_map(sections, D, interleaved)
-    _need(q, "q", torch.float16)
-    _current(dev)
-    _need(q_out, "q_out", torch.float16, dev)
-    _need(positions, "positions", torch.int32, dev)
-    _opt(k_new, "k_new", torch.float16, dev)
-    _opt(k_out, "k_out", torch.float16, dev)
-    _opt(q_lens, "q_lens", torch.int32, dev)
-    dims = Dims(B, Lq, H, D, int(Ls), 16, 0, 0, 0, 0, 0, 0.0, Hkv)
-    workspace = _small_workspace(workspace, dev, stream)
-    rc = lib().relay_rope_axes(ctypes.byref(dims), _ptr(q), _ptr(k_new), _ptr(positions), len(sections), axis,
-                               _ptr(q_lens), float(base), int(inverse), _ptr(q_out), _ptr(k_out), _ptr(workspace),
-                               workspace.numel(), _stream(stream))
-    _check(rc, "relay_rope_axes")
+    dev = q.get_device()
+    try:
+        s = _raw_stream(stream, dev)
+        pq, pk = _at(q, _F16, (B, Lq, H, D), dev), _at(k_new, _F16, (B, Lq, Hkv, D), dev)
+        pqo = pq if q_out is q else _at(q_out, _F16, (B, Lq, H, D), dev)
+        pko = pk if k_out is k_new else _at(k_out, _F16, (B, Lq, Hkv, D), dev)
+        pp, pl = _at(positions, _I32, (n, B, Lq), dev), _at(q_lens, _I32, (B,), dev)
+        if pp is None:
+            raise _Mismatch
+    except (_Mismatch, RuntimeError, AssertionError):
+        _explain("relay_rope_axes", "q", ("q", q, _F16, (B, Lq, H, D)), ("k_new", k_new, _F16, (B, Lq, Hkv, D)),
+                 ("q_out", q_out, _F16, (B, Lq, H, D)), ("k_out", k_out, _F16, (B, Lq, Hkv, D)),
+                 ("positions", positions, _I32, (n, B, Lq)), ("q_lens", q_lens, _I32, (B,)))
+    workspace = _workspace(workspace, q.device, stream)
+    rc = lib().relay_rope_axes(_dims(B, Lq, H, D, int(Ls), 0, 0, Hkv), pq, pk, pp, n, axis, pl, base, bool(inverse), pqo,
+                               pko, workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _check(rc, "relay_rope_axes")
     return q_out, k_out
-
-
-def _free_list(free_blocks, n_free, n_free_out, dev):
-    if free_blocks.dim() != 1:
-        raise ValueError(f"free_blocks {tuple(free_blocks.shape)} must be [num_blocks]")
-    _shape(n_free, "n_free", (1,))
-    _shape(n_free_out, "n_free_out", (1,))
-    _need(free_blocks, "free_blocks", torch.int32, dev)
-    _need(n_free, "n_free", torch.int32, dev)
-    _need(n_free_out, "n_free_out", torch.int32, dev)
 
 
 def relay_block_plan(ctx_lens, block_tables, free_blocks, n_free, q_lens=None, Lq=1, slot_map=None, n_free_out=None,
@@ -644,49 +683,54 @@ def relay_block_plan(ctx_lens, block_tables, free_blocks, n_free, q_lens=None, L
     """Block tables (in place) and slot map ([B, Lq] int32, returned) of a step in which request b grows by q_lens[b]
     (or Lq) tokens to ctx_lens[b], the new blocks taken from the end of free_blocks ([num_blocks], the first n_free[0]
     in use).  n_free_out: where the new count goes (None: into n_free)."""
-    dev = ctx_lens.device
-    if ctx_lens.dim() != 1:
-        raise ValueError(f"ctx_lens {tuple(ctx_lens.shape)} must be [B]")
-    B = ctx_lens.shape[0]
-    n_free_out = n_free if n_free_out is None else n_free_out
-    _table_shapes(B, block_tables, ctx_lens, q_lens)
-    _shape(slot_map, "slot_map", (B, Lq))
-    _need(ctx_lens, "ctx_lens", torch.int32)
-    _current(dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _opt(q_lens, "q_lens", torch.int32, dev)
-    _free_list(free_blocks, n_free, n_free_out, dev)
-    if slot_map is None:
-        slot_map = _on_stream(stream, torch.empty, (B, Lq), dtype=torch.int32, device=dev)
-    _need(slot_map, "slot_map", torch.int32, dev)
-    dims = Dims(B, Lq, 1, 64, 0, 16, free_blocks.shape[0], block_tables.shape[1], 0, 0, 0, 0.0, 0)
-    workspace = _small_workspace(workspace, dev, stream)
-    rc = lib().relay_block_plan(ctypes.byref(dims), _ptr(ctx_lens), _ptr(q_lens), _ptr(free_blocks), _ptr(n_free),
-                                _ptr(block_tables), _ptr(slot_map), _ptr(n_free_out), _ptr(workspace),
-                                workspace.numel(), _stream(stream))
-    _check(rc, "relay_block_plan")
+    if n_free_out is None:
+        n_free_out = n_free
+    B, dev = ctx_lens.numel(), ctx_lens.get_device()
+    mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
+    num = free_blocks.numel()
+    try:
+        s = _raw_stream(stream, dev)
+        pc, pl, pt = _at(ctx_lens, _I32, (B,), dev), _at(q_lens, _I32, (B,), dev), _at(block_tables, _I32, (B, mb), dev)
+        pf, pn = _at(free_blocks, _I32, (num,), dev), _at(n_free, _I32, (1,), dev)
+        po = pn if n_free_out is n_free else _at(n_free_out, _I32, (1,), dev)
+        if slot_map is None:
+            slot_map = _on_stream(stream, torch.empty, (B, Lq), dtype=_I32, device=ctx_lens.device)
+        ps = _at(slot_map, _I32, (B, Lq), dev)
+    except (_Mismatch, RuntimeError, AssertionError):
+        _explain("relay_block_plan", "ctx_lens", ("ctx_lens", ctx_lens, _I32, (B,)), ("q_lens", q_lens, _I32, (B,)),
+                 ("block_tables", block_tables, _I32, (B, mb)), ("free_blocks", free_blocks, _I32, (num,)),
+                 ("n_free", n_free, _I32, (1,)), ("n_free_out", n_free_out, _I32, (1,)),
+                 ("slot_map", slot_map, _I32, (B, Lq)))
+    workspace = _workspace(workspace, ctx_lens.device, stream)
+    rc = lib().relay_block_plan(_dims(B, Lq, 1, 64, 0, num, mb), pc, pl, pf, pn, pt, ps, po, workspace.data_ptr(),
+                                workspace.numel(), s)
+    if rc:
+        _check(rc, "relay_block_plan")
     return slot_map
 
 
 def relay_block_release(done, ctx_lens, block_tables, free_blocks, n_free, n_free_out=None, workspace=None, stream=None):
     """Append the blocks of the requests with done[b] != 0 ([B] int32) to free_blocks (in place); the new count goes
     to n_free_out (None: into n_free).  Returns n_free_out."""
-    dev = done.device
-    if done.dim() != 1:
-        raise ValueError(f"done {tuple(done.shape)} must be [B]")
-    B = done.shape[0]
-    n_free_out = n_free if n_free_out is None else n_free_out
-    _table_shapes(B, block_tables, ctx_lens, None)
-    _need(done, "done", torch.int32)
-    _current(dev)
-    _need(ctx_lens, "ctx_lens", torch.int32, dev)
-    _need(block_tables, "block_tables", torch.int32, dev)
-    _free_list(free_blocks, n_free, n_free_out, dev)
-    dims = Dims(B, 1, 1, 64, 0, 16, free_blocks.shape[0], block_tables.shape[1], 0, 0, 0, 0.0, 0)
-    workspace = _small_workspace(workspace, dev, stream)
-    rc = lib().relay_block_release(ctypes.byref(dims), _ptr(done), _ptr(ctx_lens), _ptr(block_tables), _ptr(free_blocks),
-                                   _ptr(n_free), _ptr(n_free_out), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(rc, "relay_block_release")
+    if n_free_out is None:
+        n_free_out = n_free
+    B, dev = done.numel(), done.get_device()
+    mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
+    num = free_blocks.numel()
+    try:
+        s = _raw_stream(stream, dev)
+        pd, pc, pt = _at(done, _I32, (B,), dev), _at(ctx_lens, _I32, (B,), dev), _at(block_tables, _I32, (B, mb), dev)
+        pf, pn = _at(free_blocks, _I32, (num,), dev), _at(n_free, _I32, (1,), dev)
+        po = pn if n_free_out is n_free else _at(n_free_out, _I32, (1,), dev)
+    except (_Mismatch, RuntimeError, AssertionError):
+        _explain("relay_block_release", "done", ("done", done, _I32, (B,)), ("ctx_lens", ctx_lens, _I32, (B,)),
+                 ("block_tables", block_tables, _I32, (B, mb)), ("free_blocks", free_blocks, _I32, (num,)),
+                 ("n_free", n_free, _I32, (1,)), ("n_free_out", n_free_out, _I32, (1,)))
+    workspace = _workspace(workspace, done.device, stream)
+    rc = lib().relay_block_release(_dims(B, 1, 1, 64, 0, num, mb), pd, pc, pt, pf, pn, po, workspace.data_ptr(),
+                                   workspace.numel(), s)
+    if rc:
+        _check(rc, "relay_block_release")
     return n_free_out
 
 
@@ -703,11 +747,12 @@ class Q4Cache:
         self.num_blocks, self.Hkv, _, half = k_codes.shape
         self.D = 2 * half
         groups = k_sz.shape[3] if k_sz.dim() == 5 else 0
-        if groups < 1 or self.D % groups or                 tuple(k_sz.shape) != (self.num_blocks, self.Hkv, 16, groups, 2):
+        if groups < 1 or self.D % groups or \
+                tuple(k_sz.shape) != (self.num_blocks, self.Hkv, 16, groups, 2):
             raise ValueError(f"k_sz {tuple(k_sz.shape)} must be [{self.num_blocks}, {self.Hkv}, 16, D / group, 2]")
         self.group = self.D // groups
-        for name, t, dtype in (("k_codes", k_codes, torch.uint8), ("k_sz", k_sz, torch.float16),
-                               ("v_codes", v_codes, torch.uint8), ("v_sz", v_sz, torch.float16)):
+        for name, t, dtype in (("k_codes", k_codes, _U8), ("k_sz", k_sz, _F16), ("v_codes", v_codes, _U8),
+                               ("v_sz", v_sz, _F16)):
             _need(t, name, dtype, k_codes.device)
         self.k_codes, self.k_sz, self.v_codes, self.v_sz = k_codes, k_sz, v_codes, v_sz
         self.device = k_codes.device
@@ -719,8 +764,7 @@ def make_q4_cache(num_blocks, Hkv, D, group=128, device=None) -> Q4Cache:
     if group not in (32, 64, 128) or D % group:
         raise ValueError(f"group {group} must be 32, 64 or 128 and divide D = {D}")
     z = lambda *shape, dtype: torch.zeros(num_blocks, Hkv, 16, *shape, dtype=dtype, device=device or "cuda")
-    return Q4Cache(z(D // 2, dtype=torch.uint8), z(D // group, 2, dtype=torch.float16),
-                   z(D // 2, dtype=torch.uint8), z(D // group, 2, dtype=torch.float16))
+    return Q4Cache(z(D // 2, dtype=_U8), z(D // group, 2, dtype=_F16), z(D // 2, dtype=_U8), z(D // group, 2, dtype=_F16))
 
 
 def workspace_size_q4(dims: Dims) -> int:
@@ -732,14 +776,16 @@ def make_workspace_q4(dims: Dims, device=None) -> torch.Tensor:
     n = workspace_size_q4(dims)
     if n == 0:
         raise ValueError(f"invalid dims {dims}")
-    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+    return torch.zeros(n, dtype=_U8, device=device or "cuda")
 
 
-def _check_cache(cache: Q4Cache, D, dev):
+def _check_cache(cache: Q4Cache, D, Hkv, H, dev):
     if cache.D != D:
         raise ValueError(f"the 4-bit pool has D = {cache.D}, expected {D}")
-    if cache.device != dev:
-        raise ValueError(f"the 4-bit pool is on {cache.device}, expected {dev}")
+    if cache.Hkv != Hkv:
+        raise ValueError(f"{Hkv} KV heads, but the 4-bit pool has {cache.Hkv}")
+    if H % cache.Hkv:
+        raise ValueError(f"{H} query heads over the 4-bit pool's {cache.Hkv} KV heads")
 
 
 def relay_kv_append_q4(k_new, v_new, block_tables, ctx_lens, cache: Q4Cache, q_lens=None, slot_map=None, workspace=None,
@@ -747,104 +793,97 @@ def relay_kv_append_q4(k_new, v_new, block_tables, ctx_lens, cache: Q4Cache, q_l
     """Quantise the step's new K/V rows ([B, Lq, Hkv, D] fp16) into the 4-bit pool in place, at each request's last
     q_lens[b] context positions, or at slot_map ([B, Lq] int32, from relay_block_plan; block_tables and ctx_lens may
     then be None).  Device-side problems are flagged in `workspace` (device_status), which is returned."""
-    dev = k_new.device
     B, Lq, Hkv, D = k_new.shape
-    _same(k_new, v_new, ("k_new", "v_new"))
-    if cache.Hkv != Hkv:
-        raise ValueError(f"k_new has {Hkv} KV heads, the 4-bit pool {cache.Hkv}")
-    max_blocks = 0
-    if slot_map is None:
-        _table_shapes(B, block_tables, ctx_lens, q_lens)
-        max_blocks = block_tables.shape[1]
-    _shape(q_lens, "q_lens", (B,))
-    _shape(slot_map, "slot_map", (B, Lq))
-    _need(k_new, "k_new", torch.float16)
-    _current(dev)
-    _need(v_new, "v_new", torch.float16, dev)
-    _check_cache(cache, D, dev)
-    if slot_map is None:
-        _need(block_tables, "block_tables", torch.int32, dev)
-        _need(ctx_lens, "ctx_lens", torch.int32, dev)
-    else:
+    mb = 0
+    if slot_map is not None:
         block_tables = ctx_lens = None
-        _need(slot_map, "slot_map", torch.int32, dev)
-    _opt(q_lens, "q_lens", torch.int32, dev)
-    dims = Dims(B, Lq, Hkv, D, 0, 16, cache.num_blocks, max_blocks, 0, 0, 0, 0.0, Hkv)
-    workspace = _small_workspace(workspace, dev, stream)
-    rc = lib().relay_kv_append_q4(ctypes.byref(dims), _ptr(k_new), _ptr(v_new), _ptr(block_tables), _ptr(ctx_lens),
-                                  _ptr(q_lens), _ptr(slot_map), ctypes.byref(cache._struct), _ptr(workspace),
-                                  workspace.numel(), _stream(stream))
-    _check(rc, "relay_kv_append_q4")
+    elif block_tables.dim() == 2:
+        mb = block_tables.shape[1]
+    dev = k_new.get_device()
+    try:
+        s = _raw_stream(stream, dev)
+        pk, pv = _at(k_new, _F16, (B, Lq, Hkv, D), dev), _at(v_new, _F16, (B, Lq, Hkv, D), dev)
+        pt, pc = _at(block_tables, _I32, (B, mb), dev), _at(ctx_lens, _I32, (B,), dev)
+        pl, ps = _at(q_lens, _I32, (B,), dev), _at(slot_map, _I32, (B, Lq), dev)
+        if cache.D != D or cache.Hkv != Hkv or cache.device.index != dev:
+            raise _Mismatch
+    except (_Mismatch, RuntimeError, AssertionError):
+        _check_cache(cache, D, Hkv, Hkv, k_new.device)
+        _explain("relay_kv_append_q4", "k_new", ("k_new", k_new, _F16, (B, Lq, Hkv, D)),
+                 ("v_new", v_new, _F16, (B, Lq, Hkv, D)), ("block_tables", block_tables, _I32, (B, mb)),
+                 ("ctx_lens", ctx_lens, _I32, (B,)), ("q_lens", q_lens, _I32, (B,)),
+                 ("slot_map", slot_map, _I32, (B, Lq)), ("the 4-bit pool", cache.k_codes, _U8, cache.k_codes.shape))
+    workspace = _workspace(workspace, k_new.device, stream)
+    rc = lib().relay_kv_append_q4(_dims(B, Lq, Hkv, D, 0, cache.num_blocks, mb, Hkv), pk, pv, pt, pc, pl, ps, cache._struct,
+                                  workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _check(rc, "relay_kv_append_q4")
     return workspace
 
 
-def _q4_dims(q, Ls, cache, block_tables, ctx_lens, q_lens, dims, scale, max_q_total, ctx_split, sys_range):
-    """The checks and dims that the two calls over a 4-bit pool share."""
+def _q4_call(what, q, sys_k, sys_v, cache, block_tables, ctx_lens, q_lens, out, out_dtype, lse, scale, max_q_total, ctx_split,
+             sys_range, stream, dims):
+    """The checks that the two calls over a 4-bit pool share: the addresses, the output, the dims and the stream."""
     B, Lq, H, D = q.shape
-    _check_cache(cache, D, q.device)
-    if H % cache.Hkv:
-        raise ValueError(f"{H} query heads over the 4-bit pool's {cache.Hkv} KV heads")
-    _table_shapes(B, block_tables, ctx_lens, q_lens)
-    _need(q, "q", torch.float16)
-    _current(q.device)
-    _need(block_tables, "block_tables", torch.int32, q.device)
-    _need(ctx_lens, "ctx_lens", torch.int32, q.device)
-    _opt(q_lens, "q_lens", torch.int32, q.device)
+    Hkv = cache.Hkv
+    Ls = 0 if sys_k is None else sys_k.shape[0]
+    mb = block_tables.shape[1] if block_tables.dim() == 2 else 0
+    dev = q.get_device()
+    try:
+        s = _raw_stream(stream, dev)
+        pq = _at(q, _F16, (B, Lq, H, D), dev)
+        pk, pv = _at(sys_k, _F16, (Ls, Hkv, D), dev), _at(sys_v, _F16, (Ls, Hkv, D), dev)
+        pt, pc, pl = _at(block_tables, _I32, (B, mb), dev), _at(ctx_lens, _I32, (B,), dev), _at(q_lens, _I32, (B,), dev)
+        if out is None:
+            out = _on_stream(stream, torch.empty, (B, Lq, H, D), dtype=out_dtype, device=q.device)
+        po, pe = _at(out, out_dtype, (B, Lq, H, D), dev), _at(lse, _F32, (B, Lq, H), dev)
+        if cache.D != D or H % Hkv or cache.device.index != dev:
+            raise _Mismatch
+    except (_Mismatch, RuntimeError, AssertionError):
+        _check_cache(cache, D, Hkv, H, q.device)
+        f32 = out_dtype is _F32
+        _explain(what, "q", ("q", q, _F16, (B, Lq, H, D)), ("sys_k", sys_k, _F16, (Ls, Hkv, D)),
+                 ("sys_v", sys_v, _F16, (Ls, Hkv, D)), ("block_tables", block_tables, _I32, (B, mb)),
+                 ("ctx_lens", ctx_lens, _I32, (B,)), ("q_lens", q_lens, _I32, (B,)),
+                 ("o_ctx" if f32 else "out", out, out_dtype, (B, Lq, H, D)),
+                 ("lse_ctx" if f32 else "lse_out", lse, _F32, (B, Lq, H)),
+                 ("the 4-bit pool", cache.k_codes, _U8, cache.k_codes.shape))
     if dims is None:
-        dims = make_dims(q, Ls, cache.num_blocks, block_tables.shape[1], scale, max_q_total, ctx_split, sys_range,
-                         cache.Hkv)
-    _check_dims(dims, q, Ls, cache.k_codes, block_tables)
-    _check_kv(dims, cache.k_codes, "the 4-bit pool")
-    return dims
+        dims = make_dims(q, Ls, cache.num_blocks, mb, scale, max_q_total, ctx_split, sys_range, Hkv)
+    elif (dims.B, dims.Lq, dims.H, dims.D, dims.Ls, dims.num_blocks, dims.max_blocks_per_seq, dims.Hkv) != \
+            (B, Lq, H, D, Ls, cache.num_blocks, mb, Hkv):
+        _check_dims(dims, q, Ls, cache.k_codes, block_tables)
+        _check_kv(dims, cache.k_codes, "the 4-bit pool")
+    return dims, pq, pk, pv, pt, pc, pl, out, po, pe, s
 
 
 def relay_attention_decode_q4(q, sys_k, sys_v, cache: Q4Cache, block_tables, ctx_lens, q_lens=None, out=None,
                               lse_out=None, workspace=None, scale=None, max_q_total=0, ctx_split=0, sys_range=0,
                               stream=None, dims=None):
     """relay_attention_decode with the contexts in a 4-bit pool.  Returns out [B, Lq, H, D] fp16."""
-    dev = q.device
-    B, Lq, H, D = q.shape
-    _same(sys_k, sys_v, ("sys_k", "sys_v"))
-    _shape(sys_k, "sys_k", (sys_k.shape[0], cache.Hkv, D))
-    _shape(out, "out", q.shape)
-    _shape(lse_out, "lse_out", (B, Lq, H))
-    dims = _q4_dims(q, sys_k.shape[0], cache, block_tables, ctx_lens, q_lens, dims, scale, max_q_total, ctx_split,
-                    sys_range)
-    _need(sys_k, "sys_k", torch.float16, dev)
-    _need(sys_v, "sys_v", torch.float16, dev)
-    if out is None:
-        out = _on_stream(stream, torch.empty_like, q)
-    _need(out, "out", torch.float16, dev)
-    _opt(lse_out, "lse_out", torch.float32, dev)
-    if workspace is None:
-        workspace = _on_stream(stream, make_workspace_q4, dims, dev)
-    rc = lib().relay_attention_decode_q4(ctypes.byref(dims), _ptr(q), _ptr(sys_k), _ptr(sys_v),
-                                         ctypes.byref(cache._struct), _ptr(block_tables), _ptr(ctx_lens), _ptr(q_lens),
-                                         _ptr(out), _ptr(lse_out), _ptr(workspace), workspace.numel(), _stream(stream))
-    _check(rc, "relay_attention_decode_q4")
+    dims, pq, pk, pv, pt, pc, pl, out, po, pe, s = _q4_call(
+        "relay_attention_decode_q4", q, sys_k, sys_v, cache, block_tables, ctx_lens, q_lens, out, _F16, lse_out, scale,
+        max_q_total, ctx_split, sys_range, stream, dims)
+    workspace = _workspace(workspace, q.device, stream, make_workspace_q4, dims, q.device)
+    rc = lib().relay_attention_decode_q4(dims, pq, pk, pv, cache._struct, pt, pc, pl, po, pe, workspace.data_ptr(),
+                                         workspace.numel(), s)
+    if rc:
+        _check(rc, "relay_attention_decode_q4")
     return out
 
 
 def relay_ctx_attn_q4(q, cache: Q4Cache, block_tables, ctx_lens, q_lens=None, o_ctx=None, lse_ctx=None, workspace=None,
                       scale=None, max_q_total=0, ctx_split=0, stream=None, dims=None):
     """relay_ctx_attn with the contexts in a 4-bit pool.  Returns o_ctx [B, Lq, H, D], lse_ctx [B, Lq, H] fp32."""
-    dev = q.device
-    B, Lq, H, D = q.shape
-    _shape(o_ctx, "o_ctx", q.shape)
-    _shape(lse_ctx, "lse_ctx", (B, Lq, H))
-    dims = _q4_dims(q, 0, cache, block_tables, ctx_lens, q_lens, dims, scale, max_q_total, ctx_split, 0)
-    if o_ctx is None:
-        o_ctx = _on_stream(stream, torch.empty, (B, Lq, H, D), dtype=torch.float32, device=dev)
-    if lse_ctx is None:
-        lse_ctx = _on_stream(stream, torch.empty, (B, Lq, H), dtype=torch.float32, device=dev)
-    _need(o_ctx, "o_ctx", torch.float32, dev)
-    _need(lse_ctx, "lse_ctx", torch.float32, dev)
-    if workspace is None:
-        workspace = _on_stream(stream, make_workspace_q4, dims, dev)
-    rc = lib().relay_ctx_attn_q4(ctypes.byref(dims), _ptr(q), ctypes.byref(cache._struct), _ptr(block_tables),
-                                 _ptr(ctx_lens), _ptr(q_lens), _ptr(o_ctx), _ptr(lse_ctx), _ptr(workspace),
-                                 workspace.numel(), _stream(stream))
-    _check(rc, "relay_ctx_attn_q4")
+    if lse_ctx is None and q.is_cuda:
+        lse_ctx = _on_stream(stream, torch.empty, q.shape[:3], dtype=_F32, device=q.device)
+    dims, pq, _, _, pt, pc, pl, o_ctx, po, pe, s = _q4_call(
+        "relay_ctx_attn_q4", q, None, None, cache, block_tables, ctx_lens, q_lens, o_ctx, _F32, lse_ctx, scale,
+        max_q_total, ctx_split, 0, stream, dims)
+    workspace = _workspace(workspace, q.device, stream, make_workspace_q4, dims, q.device)
+    rc = lib().relay_ctx_attn_q4(dims, pq, cache._struct, pt, pc, pl, po, pe, workspace.data_ptr(), workspace.numel(), s)
+    if rc:
+        _check(rc, "relay_ctx_attn_q4")
     return o_ctx, lse_ctx
 
 
