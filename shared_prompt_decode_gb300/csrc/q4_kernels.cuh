@@ -319,7 +319,8 @@ __device__ __forceinline__ Sched sched_at(int *base, int B)
 }
 
 // Columns of a request: query row i and head c of the group are column i G +
-// c, in tiles of 8 * nt (two tensor-core tiles where one does not hold them).
+// c, in tiles of 8 * nt: one, two or four tensor-core tiles, as many as they
+// fill.
 struct Cols {
     int cols, nt, tiles;
 };
@@ -327,8 +328,9 @@ __host__ __device__ inline Cols cols_of(int ql, int G)
 {
     Cols c;
     c.cols = ql * G;
-    c.nt = c.cols > 8 ? 2 : 1;
-    c.tiles = (c.cols + 8 * c.nt - 1) >> (2 + c.nt);
+    const int lg = c.cols > 16 ? 2 : c.cols > 8 ? 1 : 0;
+    c.nt = 1 << lg;
+    c.tiles = (c.cols + 8 * c.nt - 1) >> (3 + lg);
     return c;
 }
 
@@ -377,9 +379,11 @@ struct Geo {
 #endif
     static constexpr int kW = NT > 1 ? 8 : D == 128 ? (GROUP == 32 && KW > 12 ? 12 : KW) : 16;
     static constexpr int kStep = kPer * PageQ<D, GROUP>::kPage;
-    static constexpr int kFit = (int)((kMaxSmem - offsetof(Smem4, ring)) / (kW * kStep));
+    static constexpr int kQ = NT > 1 ? NT * (D / 32) * 512 : 0;      // a warp's query operands in shared memory
+    static constexpr int kFit = (int)((kMaxSmem - offsetof(Smem4, ring) - kW * kQ) / (kW * kStep));
     static constexpr int kStages = kFit < 6 ? kFit : 6;
     static_assert(kStages >= 2, "ring");
+    static constexpr size_t kSmem = offsetof(Smem4, ring) + (size_t)kW * (kStages * kStep + kQ);
 };
 
 __device__ __forceinline__ void set_request(const Params &p, const Smem4 &s, Seq &q, int b)
@@ -914,53 +918,385 @@ __device__ __forceinline__ void step(unsigned st, const Lane<D, GROUP> &ln, int 
     }
 }
 
-// Writes the partial of a sequence: normalised output and log2-sum-exp per
-// column, rows pr + column.
+// ----------------------------------------------------------------------------- attention: many columns
+// The same step for NT = 2 or 4 tiles of columns, a page at a time, where the
+// tensor cores and the arithmetic per column count for more than the unpacking
+// that the tiles share:
+//  - the query operands stay in shared memory (a lane's fragments of word w of
+//    tile nt side by side), the accumulators take the registers;
+//  - all four code positions of a K word are shifted to the bottom, so that
+//    one accumulator takes them all;
+//  - V's operands are c - 8 (1024 + c as fp16 bits, less 1032: exact), so no
+//    product with eights is needed;
+//  - sum(q) z and sum p (z + 8 s) are products too, over the groups and over
+//    the keys, with sum(q) and z + 8 s as an fp16 number and its remainder.
+template <int D, int GROUP, int NT>
+struct Wide {
+    float o[NT][D / 16][4];         // tiles of code positions 0 (units of 2^-down) and 1 (of 16 times that)
+    float z[NT][4];                 // row i < NG: sum p hi(z + 8 s) of group i, row NG + i: of the remainders
+    Vec<2> m[NT], l[NT];
+    int e;
+};
+constexpr float kQsScale = 1.f / 128.f;      // a group's sum of q fits fp16
+
+// The share's query operands: fragments to shared memory, sums to registers.
+template <int D, int GROUP, int NT>
+__device__ __forceinline__ void wide_q(const Params &p, int lane, const Share &s, int cols, unsigned qsm, unsigned (&qz)[NT])
+{
+    constexpr int WPG = GROUP / 32, NG = D / GROUP;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        const int v = s.tile * 8 * NT + 8 * nt + g;
+        const bool has = v < cols;
+        const int i = s.ql == 1 || !has ? 0 : v / p.G, c = has ? v - i * p.G : 0;
+        const __half *q = p.q + (((size_t)s.b * p.Lq + i) * p.H + s.hk * p.G + c) * D;
+        float sum[NG];
+#pragma unroll
+        for (int gi = 0; gi < NG; gi++) sum[gi] = 0.f;
+#pragma unroll
+        for (int w = 0; w < D / 32; w++) {
+            const int d0 = (w / WPG) * GROUP + t * (GROUP / 4) + 8 * (w % WPG);
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (has) x = *reinterpret_cast<const uint4 *>(q + d0);
+            const unsigned xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&xs[k]));
+                sum[w / WPG] += f.x + f.y;
+            }
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(qsm + ((nt * (D / 32) + w) * 32 + lane) * 16),
+                         "r"(__byte_perm(x.x, x.z, 0x5410)), "r"(__byte_perm(x.y, x.w, 0x5410)),
+                         "r"(__byte_perm(x.x, x.z, 0x7632)), "r"(__byte_perm(x.y, x.w, 0x7632))
+                         : "memory");
+        }
+        // row k of the operand: sums of groups k, then their remainders
+        __half v16[2 * NG];
+#pragma unroll
+        for (int gi = 0; gi < NG; gi++) {
+            float f = sum[gi];
+            f += __shfl_xor_sync(0xffffffffu, f, 1);
+            f += __shfl_xor_sync(0xffffffffu, f, 2);
+            f *= kQsScale;
+            v16[gi] = __float2half_rn(f);
+            v16[NG + gi] = __float2half_rn(f - __half2float(v16[gi]));
+        }
+        unsigned w = 0;
+#pragma unroll
+        for (int k = 0; k < NG; k++)
+            if (t == k) {
+                const __half2 h = __halves2half2(v16[2 * k], v16[2 * k + 1]);
+                w = *reinterpret_cast<const unsigned *>(&h);
+            }
+        qz[nt] = w;
+    }
+    __syncwarp();
+}
+
+// One staged page.  FULL: every column sees all of it.
+template <int D, int GROUP, int NT, bool FULL>
+__device__ __forceinline__ void wide_page(unsigned st, const Lane<D, GROUP> &ln, unsigned qsm, const unsigned (&qz)[NT],
+                                          Wide<D, GROUP, NT> &s, const int (&end)[NT][2], float scale_log2, float slack)
+{
+    using P = PageQ<D, GROUP>;
+    constexpr int NG = P::NG, WPG = GROUP / 32;
+    const int g = ln.lane >> 2, t = ln.lane & 3;
+    const __half2 zero = __floats2half2_rn(0.f, 0.f);
+    float sc[NT][4];
+    {
+        // z sum(q): rows keys, columns of the operand groups (twice: sums and remainders)
+        __half2 h[2][NG];
+        load_pairs<NG>(st + ln.sz, h[0]);
+        load_pairs<NG>(st + ln.sz + 8 * NG * 4, h[1]);
+        unsigned a[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            __half2 z = NG == 1 ? __highs2half2(h[r][0], h[r][0]) : __highs2half2(h[r][0], h[r][NG > 1 ? 1 : 0]);
+            if (NG == 4 && (t & 1)) z = __highs2half2(h[r][NG > 2 ? 2 : 0], h[r][NG > 2 ? 3 : 0]);
+            a[r] = *reinterpret_cast<const unsigned *>(&z);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            mma16816_first(sc[nt], a, qz[nt], 0u);
+#pragma unroll
+            for (int e = 0; e < 4; e++) sc[nt][e] *= 1.f / kQsScale;
+        }
+#pragma unroll
+        for (int gi = 0; gi < NG; gi++) {
+            unsigned w[2][WPG];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const unsigned at = ln.k(st, r, gi * (GROUP / 2));
+                if constexpr (WPG == 4) {
+                    const uint4 x = lds128(at);
+                    w[r][0] = x.x; w[r][1] = x.y; w[r][2] = x.z; w[r][3] = x.w;
+                } else if constexpr (WPG == 2) {
+                    const uint2 x = lds64(at);
+                    w[r][0] = x.x; w[r][1] = x.y;
+                } else {
+                    w[r][0] = lds32(at);
+                }
+            }
+            float acc[NT][4];
+#pragma unroll
+            for (int j = 0; j < WPG; j++) {
+                const unsigned x0 = w[0][j], x1 = w[1][j];
+                const unsigned a0[4] = {x0 & kLoCodes, x1 & kLoCodes, (x0 >> 8) & kLoCodes, (x1 >> 8) & kLoCodes};
+                const unsigned a1[4] = {(x0 >> 4) & kLoCodes, (x1 >> 4) & kLoCodes, (x0 >> 12) & kLoCodes, (x1 >> 12) & kLoCodes};
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    const uint4 b = lds128(qsm + ((nt * (D / 32) + gi * WPG + j) * 32 + ln.lane) * 16);
+                    if (j == 0) mma16816_first(acc[nt], a0, b.x, b.y);
+                    else mma16816(acc[nt], a0, b.x, b.y);
+                    mma16816(acc[nt], a1, b.z, b.w);
+                }
+            }
+            const float f[2] = {__low2float(h[0][gi]) * 0x1p24f, __low2float(h[1][gi]) * 0x1p24f};
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) sc[nt][e] = fmaf(f[e >> 1], acc[nt][e], sc[nt][e]);
+        }
+    }
+    bool moved = false;
+    Vec<2> mn[NT], mu[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 2; e++) {
+            if (!FULL) {
+                if (g >= end[nt][e]) sc[nt][e] = kNegInf;
+                if (g + 8 >= end[nt][e]) sc[nt][2 + e] = kNegInf;
+            }
+            float mx = fmaxf(sc[nt][e], sc[nt][2 + e]);
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float m = s.m[nt][e];
+            const bool move = mx > m + slack;
+            mn[nt][e] = move ? mx : m;
+            mu[nt][e] = mn[nt][e] == kNegInf ? 0.f : -mn[nt][e] * scale_log2;
+            moved = moved || move;
+        }
+    // V's pairs of keys g, g + 8 (the weights) and of the operand's keys (z + 8 s)
+    const unsigned vsz = st + 2 * P::kCodes + P::kSz;
+    __half2 h[2][NG];
+    load_pairs<NG>(vsz + g * NG * 4, h[0]);
+    load_pairs<NG>(vsz + (g + 8) * NG * 4, h[1]);
+    int em = 0;
+#pragma unroll
+    for (int i = 0; i < 2 * NG; i++) em = max(em, scale_exp(h[i / NG][i % NG]));
+    em = max(s.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)em));
+    if (__any_sync(0xffffffffu, moved || em != s.e)) {
+        const float ae = __int_as_float((s.e - em + 127) << 23);
+        s.e = em;
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const float al = ex2(fmaf(s.m[nt][e], scale_log2, mu[nt][e])), ao = al * ae;
+                s.m[nt][e] = mn[nt][e];
+                s.l[nt][e] *= al;
+                s.z[nt][e] *= al;
+                s.z[nt][2 + e] *= al;
+#pragma unroll
+                for (int d = 0; d < D / 16; d++) {
+                    s.o[nt][d][e] *= ao;
+                    s.o[nt][d][2 + e] *= ao;
+                }
+            }
+    }
+    const float down = scale_down(em);
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            sc[nt][e] = ex2(fmaf(sc[nt][e], scale_log2, mu[nt][e & 1]));
+            s.l[nt][e & 1] += sc[nt][e];
+        }
+    {
+        // rows: group i's z + 8 s as fp16, row NG + i: what that leaves
+        unsigned a[4] = {0u, 0u, 0u, 0u};
+        const int gi = g % NG;
+        const bool hi = g < NG, lo = !hi && g < 2 * NG;
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            float z[2];
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const unsigned w = lds32(vsz + ((2 * t + i + 8 * k) * NG + gi) * 4);
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                z[i] = fmaf(8.f, v.x, v.y);
+                // (of a key that some column does not see: it must not meet a zero weight)
+                if (!FULL && !(fabsf(z[i]) < __int_as_float(0x7f800000))) z[i] = 0.f;
+            }
+            __half2 h16 = __floats2half2_rn(z[0], z[1]);
+            if (lo) {
+                const float2 b = __half22float2(h16);
+                h16 = __floats2half2_rn(z[0] - b.x, z[1] - b.y);
+            }
+            if (!hi && !lo) h16 = zero;
+            a[2 * k] = *reinterpret_cast<const unsigned *>(&h16);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+            mma16816(s.z[nt], a, movmatrix_t(pack_half2(sc[nt][0], sc[nt][1])), movmatrix_t(pack_half2(sc[nt][2], sc[nt][3])));
+    }
+    constexpr int kHalf = GROUP == 32 ? 32 : 64;
+    const __half2 bias0 = __floats2half2_rn(-1032.f, -1032.f), bias1 = __floats2half2_rn(-1152.f, -1152.f);
+    auto lo_code = [&](unsigned x) {
+        const unsigned b = (x & kLoCodes) | 0x64006400u;
+        const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&b), bias0);
+        return *reinterpret_cast<const unsigned *>(&r);
+    };
+    auto hi_code = [&](unsigned x) {
+        const unsigned b = (x & kHiCodes) | 0x64006400u;
+        const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&b), bias1);
+        return *reinterpret_cast<const unsigned *>(&r);
+    };
+    unsigned pb[NT][2];
+#pragma unroll
+    for (int hf = 0; hf < D / kHalf; hf++) {
+        const int gi = hf * kHalf / GROUP;
+        if (hf * kHalf % GROUP == 0) {
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                float2 v = __half22float2(h[r][gi]);
+                // (a bad z has left the operand above: the weights carry it)
+                if (!FULL && !(fabsf(fmaf(8.f, v.x, v.y)) < __int_as_float(0x7f800000))) v.x = __int_as_float(0x7fffffff);
+                const float vs = v.x * down;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float w[2];
+#pragma unroll
+                    for (int e = 0; e < 2; e++) {
+                        const bool seen = FULL || g + 8 * r < end[nt][e];
+                        w[e] = seen ? sc[nt][2 * r + e] * vs : 0.f;
+                    }
+                    pb[nt][r] = movmatrix_t(pack_half2(w[0], w[1]));
+                }
+            }
+        }
+        unsigned w[4];
+#pragma unroll
+        for (int k = 0; k < 4; k++) w[k] = lds32(ln.v(st, k, hf * (kHalf / 2)));
+        unsigned x0 = __byte_perm(w[0], w[1], 0x5410), y0 = __byte_perm(w[0], w[1], 0x7632);
+        unsigned x1 = __byte_perm(w[2], w[3], 0x5410), y1 = __byte_perm(w[2], w[3], 0x7632);
+        if constexpr (GROUP == 32) {
+            const int sh = (ln.lane >> 4) * 8;
+            x0 >>= sh; y0 >>= sh; x1 >>= sh; y1 >>= sh;
+            const unsigned a0[4] = {lo_code(x0), lo_code(y0), lo_code(x1), lo_code(y1)};
+            const unsigned a1[4] = {hi_code(x0), hi_code(y0), hi_code(x1), hi_code(y1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++) {
+                mma16816(s.o[nt][2 * hf], a0, pb[nt][0], pb[nt][1]);
+                mma16816(s.o[nt][2 * hf + 1], a1, pb[nt][0], pb[nt][1]);
+            }
+        } else {
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const unsigned x = r ? y0 : x0, y = r ? y1 : x1;
+                const unsigned a0[4] = {lo_code(x), lo_code(x >> 8), lo_code(y), lo_code(y >> 8)};
+                const unsigned a1[4] = {hi_code(x), hi_code(x >> 8), hi_code(y), hi_code(y >> 8)};
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    mma16816(s.o[nt][4 * hf + 2 * r], a0, pb[nt][0], pb[nt][1]);
+                    mma16816(s.o[nt][4 * hf + 2 * r + 1], a1, pb[nt][0], pb[nt][1]);
+                }
+            }
+        }
+    }
+}
+
+// The group term of the lane's column 2t + e, from the operand's rows.
+template <int D, int GROUP, int NT>
+__device__ __forceinline__ float wide_z(const Wide<D, GROUP, NT> &s, int lane, int nt, int gi, int e)
+{
+    constexpr int NG = D / GROUP;
+    const int t = lane & 3;
+    return __shfl_sync(0xffffffffu, s.z[nt][e], 4 * gi + t) + __shfl_sync(0xffffffffu, s.z[nt][e], 4 * (NG + gi) + t);
+}
+
+// Writes a column's partial: normalised output (o times f0, in tiles of code
+// position 1 times f1, plus its group's term) and log2-sum-exp.
+template <int D, int GROUP>
+__device__ __forceinline__ void write_column(const Args &a, int lane, size_t pr, const float (&o)[D / 16][4], int e, float f0,
+                                             float f1, const float (&z)[D / GROUP], float lse)
+{
+    const int g = lane >> 2;
+    float *po = a.p.part_o + pr * D;
+    if constexpr (GROUP == 32) {
+#pragma unroll
+        for (int gi = 0; gi < D / GROUP; gi++)
+#pragma unroll
+            for (int r = 0; r < 2; r++)
+                __stcg(reinterpret_cast<float2 *>(po + 32 * gi + 8 * (g & 3) + 2 * (g >> 2) + 4 * r),
+                       make_float2(o[2 * gi][2 * r + e] * f0 + z[gi], o[2 * gi + 1][2 * r + e] * f1 + z[gi]));
+    } else {
+#pragma unroll
+        for (int hf = 0; hf < D / 64; hf++) {
+            const float zg = z[hf * 64 / GROUP];
+            // tiles: code positions 0, 1, 4, 5 (rows g) and 2, 3, 6, 7 (rows g + 8)
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const float(&x)[4] = o[4 * hf + 2 * r], (&y)[4] = o[4 * hf + 2 * r + 1];
+                __stcg(reinterpret_cast<float4 *>(po + 64 * hf + 8 * g + 4 * r),
+                       make_float4(x[e] * f0 + zg, y[e] * f1 + zg, x[2 + e] * f0 + zg, y[2 + e] * f1 + zg));
+            }
+        }
+    }
+    if (g == 0) __stcg(a.p.part_lse + pr, lse);
+}
+
+// Writes the partial of a share, rows pr0 + column.
 template <int D, int GROUP, int NT, int E>
 __device__ __forceinline__ void write_partial(const Args &a, int lane, int nv, State<D, GROUP, NT, E> &s, size_t pr0)
 {
     constexpr int NG = D / GROUP;
-    const int g = lane >> 2, t = lane & 3;
+    const int t = lane & 3;
     const float up = __int_as_float((24 + s.e - 15 + 127) << 23);      // 2^24 / scale_down
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < E; e++) {
+            float z[NG];
+#pragma unroll
+            for (int gi = 0; gi < NG; gi++) z[gi] = s.z[nt][gi][e];
+            float L = s.l[nt][e];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) {
-                s.l[nt][e] += __shfl_xor_sync(0xffffffffu, s.l[nt][e], off);
+                L += __shfl_xor_sync(0xffffffffu, L, off);
 #pragma unroll
-                for (int gi = 0; gi < NG; gi++) s.z[nt][gi][e] += __shfl_xor_sync(0xffffffffu, s.z[nt][gi][e], off);
+                for (int gi = 0; gi < NG; gi++) z[gi] += __shfl_xor_sync(0xffffffffu, z[gi], off);
             }
+            const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), f0 = up * inv;      // (a NaN goes on)
+#pragma unroll
+            for (int gi = 0; gi < NG; gi++) z[gi] = z[gi] * inv - s.c[nt][gi][e] * f0;
             const int c = 8 * nt + 2 * t + e;
-            if (c >= nv) continue;
-            const size_t pr = pr0 + c;
-            const float L = s.l[nt][e], inv = L == 0.f ? 0.f : __fdividef(1.f, L);      // (a NaN goes on)
-            const float f0 = up * inv, f1 = f0 * 0.0625f;
-            float *po = a.p.part_o + pr * D;
-            if constexpr (GROUP == 32) {
+            if (c < nv)
+                write_column<D, GROUP>(a, lane, pr0 + c, s.o[nt], e, f0, f0 * 0.0625f, z,
+                                       L == 0.f ? kNegInf : fmaf(s.m[nt][e], a.p.scale_log2, lg2(L)));
+        }
+}
+template <int D, int GROUP, int NT>
+__device__ __forceinline__ void write_partial(const Args &a, int lane, int nv, Wide<D, GROUP, NT> &s, size_t pr0)
+{
+    constexpr int NG = D / GROUP;
+    const int t = lane & 3;
+    const float up = __int_as_float((s.e - 15 + 127) << 23);      // 1 / scale_down
 #pragma unroll
-                for (int gi = 0; gi < NG; gi++)
+    for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const float z = s.z[nt][gi][e] * inv - s.c[nt][gi][e] * f0;
-                        __stcg(reinterpret_cast<float2 *>(po + 32 * gi + 8 * (g & 3) + 2 * (g >> 2) + 4 * r),
-                               make_float2(s.o[nt][2 * gi][2 * r + e] * f0 + z, s.o[nt][2 * gi + 1][2 * r + e] * f1 + z));
-                    }
-            } else {
+        for (int e = 0; e < 2; e++) {
+            float L = s.l[nt][e], z[NG];
 #pragma unroll
-                for (int hf = 0; hf < D / 64; hf++) {
-                    const float z = s.z[nt][hf * 64 / GROUP][e] * inv - s.c[nt][hf * 64 / GROUP][e] * f0;
-                    // tiles: code positions 0, 1, 4, 5 (rows g) and 2, 3, 6, 7 (rows g + 8)
+            for (int off = 4; off < 32; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+            const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), f0 = up * inv;
 #pragma unroll
-                    for (int r = 0; r < 2; r++) {
-                        const float(&x)[4] = s.o[nt][4 * hf + 2 * r], (&y)[4] = s.o[nt][4 * hf + 2 * r + 1];
-                        __stcg(reinterpret_cast<float4 *>(po + 64 * hf + 8 * g + 4 * r),
-                               make_float4(x[e] * f0 + z, y[e] * f1 + z, x[2 + e] * f0 + z, y[2 + e] * f1 + z));
-                    }
-                }
-            }
-            if (g == 0) __stcg(a.p.part_lse + pr, L == 0.f ? kNegInf : fmaf(s.m[nt][e], a.p.scale_log2, lg2(L)));
+            for (int gi = 0; gi < NG; gi++) z[gi] = wide_z<D, GROUP, NT>(s, lane, nt, gi, e) * inv;
+            const int c = 8 * nt + 2 * t + e;
+            if (c < nv)
+                write_column<D, GROUP>(a, lane, pr0 + c, s.o[nt], e, f0, f0 * 0.0625f, z,
+                                       L == 0.f ? kNegInf : fmaf(s.m[nt][e], a.p.scale_log2, lg2(L)));
         }
 }
 
@@ -1064,11 +1400,12 @@ struct Loader {
 };
 
 // One share: its steps are in the ring or come.
-template <int D, int GROUP, int NT, int E, int KP, int STAGES>
+template <int D, int GROUP, int E, int KP, int STAGES>
 __device__ __forceinline__ void run_share(const Args &a, Smem4 &sm, const Lane<D, GROUP> &ln, int warp, Chunks &ch, unsigned ring,
                                           Loader<D, GROUP, KP, STAGES> &ld, unsigned &at, int &done, int closed, const Share sh)
 {
     using P = PageQ<D, GROUP>;
+    constexpr int NT = 1;
     const Params &p = a.p;
     const int n = sh.n, ql = sh.ql, cols = ql * p.G;
     unsigned qb[NT][D / 16][2];
@@ -1117,6 +1454,60 @@ __device__ __forceinline__ void run_share(const Args &a, Smem4 &sm, const Lane<D
         ld.fill(a, sm, ln, warp, ch, ring, ++done, closed);
     }
     write_partial<D, GROUP, NT, E>(a, ln.lane, min(8 * NT, cols - v0), s, a.part0 + (long long)sh.part * a.nc);
+}
+
+// One share of a sequence of many columns.
+template <int D, int GROUP, int NT, int KP, int STAGES>
+__device__ __forceinline__ void run_wide(const Args &a, Smem4 &sm, const Lane<D, GROUP> &ln, int warp, Chunks &ch, unsigned ring,
+                                         unsigned qsm, Loader<D, GROUP, KP, STAGES> &ld, unsigned &at, int &done, int closed,
+                                         const Share sh)
+{
+    using P = PageQ<D, GROUP>;
+    const Params &p = a.p;
+    const int n = sh.n, ql = sh.ql, cols = ql * p.G;
+    unsigned qz[NT];
+    wide_q<D, GROUP, NT>(p, ln.lane, sh, cols, qsm, qz);
+    const int v0 = sh.tile * 8 * NT, vlast = min(cols, v0 + 8 * NT) - 1;
+    const int all = ql == 1 ? n : keys_seen(n, ql, v0 / p.G);      // the first row sees least
+    Wide<D, GROUP, NT> s;
+    s.e = 0;
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++) {
+        s.m[nt] = Vec<2>::all(kNegInf);
+        s.l[nt] = Vec<2>::all(0.f);
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            s.z[nt][e] = 0.f;
+#pragma unroll
+            for (int d = 0; d < D / 16; d++) s.o[nt][d][e] = 0.f;
+        }
+    }
+    const int full_end = min(sh.end, all / kBlock);
+    for (int page = sh.page; page < sh.end; page += KP) {
+        if (ld.issued - done == STAGES - 1) cp_async_wait<STAGES - 2>();
+        else cp_async_wait<0>();
+        __syncwarp();
+#pragma unroll 1
+        for (int j = 0; j < KP && page + j < sh.end; j++) {
+            int end[NT][2];
+            if (page + j < full_end) {
+                wide_page<D, GROUP, NT, true>(at + j * P::kPage, ln, qsm, qz, s, end, p.scale_log2, a.slack);
+            } else {
+                const int t = ln.lane & 3;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 2; e++)
+                        end[nt][e] =
+                            (ql == 1 ? n : keys_seen(n, ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G)) - (page + j) * kBlock;
+                wide_page<D, GROUP, NT, false>(at + j * P::kPage, ln, qsm, qz, s, end, p.scale_log2, a.slack);
+            }
+        }
+        __syncwarp();
+        at = at + KP * P::kPage == ring + STAGES * KP * P::kPage ? ring : at + KP * P::kPage;
+        ld.fill(a, sm, ln, warp, ch, ring, ++done, closed);
+    }
+    write_partial<D, GROUP, NT>(a, ln.lane, min(8 * NT, cols - v0), s, a.part0 + (long long)sh.part * a.nc);
 }
 
 // ----------------------------------------------------------------------------- attention: kernels
@@ -1168,6 +1559,7 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     ch.Q = Q;
     if (!bad && first < ch.count) {
         const unsigned ring = smem_u32(s.ring) + warp * (G::kStages * G::kStep);
+        const unsigned qsm = smem_u32(s.ring) + G::kW * (G::kStages * G::kStep) + warp * G::kQ;
         Lane<D, GROUP> ln;
         ln.init(a.pool);
         ch.ask(p);
@@ -1187,10 +1579,20 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
             ld.fill(a, s, ln, warp, ch, ring, done, closed);
             if (ld.opened == closed) break;      // no share is left
             const Share sh = s.share[warp][closed % kShares];
-            if (NT > 1 && sh.ql * p.G > 8)
-                run_share<D, GROUP, NT, E>(a, s, ln, warp, ch, ring, ld, at, done, closed, sh);
-            else
-                run_share<D, GROUP, 1, E>(a, s, ln, warp, ch, ring, ld, at, done, closed, sh);
+            const int cols = sh.ql * p.G;
+            if constexpr (NT == 4) {
+                if (cols > 16) {
+                    run_wide<D, GROUP, 4>(a, s, ln, warp, ch, ring, qsm, ld, at, done, closed, sh);
+                    continue;
+                }
+            }
+            if constexpr (NT > 1) {
+                if (cols > 8) {
+                    run_wide<D, GROUP, 2>(a, s, ln, warp, ch, ring, qsm, ld, at, done, closed, sh);
+                    continue;
+                }
+            }
+            run_share<D, GROUP, E>(a, s, ln, warp, ch, ring, ld, at, done, closed, sh);
         }
         cp_async_wait<0>();
     }

@@ -85,7 +85,7 @@ cudaError_t prepare_kernel(int *occ)
 
 // The 4-bit context kernel of a shape: instances for D, the group size, and
 // the columns (query rows times query heads of a KV head) that a request may
-// bring: one, up to 8, more.
+// bring: one, up to 8, up to 16, more.
 struct Q4Kernel {
     void (*fn)(const q4::Args);
     int warps;
@@ -95,12 +95,15 @@ template <int D, int GROUP, int NT, int E>
 Q4Kernel q4_instance()
 {
     using G = q4::Geo<D, GROUP, NT>;
-    return {q4::ctx_kernel<D, GROUP, NT, E>, G::kW, offsetof(q4::Smem4, ring) + (size_t)G::kW * G::kStages * G::kStep};
+    return {q4::ctx_kernel<D, GROUP, NT, E>, G::kW, G::kSmem};
 }
 template <int D, int GROUP>
 Q4Kernel q4_instance(long long cols)
 {
-    return cols > 8 ? q4_instance<D, GROUP, 2, 2>() : cols > 1 ? q4_instance<D, GROUP, 1, 2>() : q4_instance<D, GROUP, 1, 1>();
+    return cols > 16 ? q4_instance<D, GROUP, 4, 2>()
+         : cols > 8  ? q4_instance<D, GROUP, 2, 2>()
+         : cols > 1  ? q4_instance<D, GROUP, 1, 2>()
+                     : q4_instance<D, GROUP, 1, 1>();
 }
 Q4Kernel q4_kernel(int D, int group, long long cols)
 {
@@ -124,7 +127,7 @@ cudaError_t prepare_q4()
     cudaError_t e = cudaSuccess;
     for (int D : {64, 128}) {
         for (int group : {32, 64, 128})
-            for (int cols : {1, 8, 9}) {
+            for (int cols : {1, 8, 16, 17}) {
                 if (group > D || e != cudaSuccess) continue;
                 const Q4Kernel k = q4_kernel(D, group, cols);
                 e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
@@ -1091,9 +1094,10 @@ PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
     pl.sys.ctx_tc = false;
     pl.sys.ctx_pairs = 0;
     pl.sys.n_tc_ctx = 0;
-    const long long cols = (long long)d->Lq * G, tiles = cols <= 8 ? 1 : (cols + 15) / 16;
-    const long long seqs = kv_heads(d) * std::min((long long)d->B * tiles, (long long)pl.sys.Mtot * G / 16 + d->B);
-    pl.nc = (int)std::min(cols, cols <= 8 ? 8ll : 16ll);
+    // a request of c columns has ceil(c / 32) sequences a KV head, one up to 32
+    const long long cols = (long long)d->Lq * G, tiles = (cols + 31) / 32;
+    const long long seqs = kv_heads(d) * std::min((long long)d->B * tiles, (long long)pl.sys.Mtot * G / 32 + d->B);
+    pl.nc = (int)std::min(cols, cols <= 8 ? 8ll : cols <= 16 ? 16ll : 32ll);
     pl.q_min = kQ4MinPages;
     const double line = (double)d->B * kv_heads(d) * tiles * d->max_blocks_per_seq;
     const long long chunks = (long long)std::min(line / kQ4MinPages + 1, 4.0 * kQ4MaxWarps * sms + 1);
