@@ -300,11 +300,13 @@ struct Args {
     int queue;                // every chunk from the queue (a grid in front has some of the SMs), else the first static
     long long part0;          // first partial row of the contexts
     float slack;              // kSlack in units of q . k
+    long long rows0;          // first partial row of the prompt chunks: (split * max_q_total + row) * H + head
+    int rows_least;           // pages of a chunk's split, at least
 };
 
-// Handed from the context kernel to the merge kernel.
+// Handed to the merge kernel (the words of Sched's header: bad, Q, the pages
+// of a prompt chunk's split).
 struct Sched {
-    int bad, Q;
     long long *pre;           // [B + 1] pages of the line before request b
     int *qo, *seq;            // [B + 1] query rows and sequences before it
 };
@@ -317,6 +319,13 @@ __device__ __forceinline__ Sched sched_at(int *base, int B)
     s.seq = s.qo + B + 1;
     return s;
 }
+
+// Requests of more than kRowsMin columns are not on the line: they have CTAs of
+// their own (rows_kernel).
+constexpr int kRowsMin = 32, kRowsTile = 128, kRowsKeys = 64;
+constexpr int kVzRow = kRowsKeys + 8;      // (rows of halves that meet no bank twice)
+constexpr int CTRL_Q4_ROWS = 7;      // ctrl word: row items taken
+__host__ __device__ inline bool by_rows(long long cols) { return cols > kRowsMin; }
 
 // Columns of a request: query row i and head c of the group are column i G +
 // c, in tiles of 8 * nt: one, two or four tensor-core tiles, as many as they
@@ -457,7 +466,7 @@ __device__ void build_line(const Params &p, Smem4 &s)
             if (ql[k] < 0 || ql[k] > p.Lq) { flags |= FLAG_BAD_Q_LEN; ql[k] = 0; }
             if (n[k] < 0 || n[k] > p.max_blocks * kBlock) { flags |= FLAG_BAD_CTX_LEN; ql[k] = n[k] = 0; }
         }
-        sq[k] = p.Hkv * cols_of(ql[k], p.G).tiles;
+        sq[k] = by_rows(ql[k] * p.G) ? 0 : p.Hkv * cols_of(ql[k], p.G).tiles;
         pg[k] = (long long)sq[k] * ((n[k] + kBlock - 1) / kBlock);
         sum_q += ql[k];
         sum_s += sq[k];
@@ -1601,6 +1610,589 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
+// ----------------------------------------------------------------------------- attention: prompt chunks
+// Requests of more than kRowsMin columns: a CTA takes 128 columns of one KV
+// head against a range of the context, and the unpacking is shared by all of
+// them.  A stage is 64 keys: every thread fetches its own 16-byte pieces of
+// the codes and of the pairs some stages ahead, unpacks them into fp16 tiles
+// (K as c * 2^-24, V as c - 8, both exact) and tables of scales, and the eight
+// warps, 16 columns each, run over the tiles like over fp16 ones:
+//     S = sum over groups  s_g[key] (Q C_g^T)  +  sum(q) z   (one product more)
+//     O_g += (P s_g) (C_g - 8),   Z += P (z + 8 s)           (one product more)
+// The tiles hold a word's eight dimensions in the order of the unpacking, 0 4
+// 1 5 2 6 3 7; Q is read in that order and the output written back from it.
+
+struct RowItems {
+    int qo[kMaxB + 1];        // query rows before request b
+    int it[kMaxB + 1];        // items before request b
+    long long sum[8];
+    int sum_q[8];
+    int bad, next;
+};
+
+template <int D, int GROUP>
+struct RowsSmem {
+    static constexpr int NG = D / GROUP;
+    static constexpr int kCodes = kRowsKeys * D / 2;               // bytes of a stage's K or V codes
+    static constexpr int kRaw = 2 * kCodes + 2 * kRowsKeys * NG * 4;
+    static constexpr int kStages = 4;
+    struct alignas(256) Tiles {
+        __half k[kRowsKeys * D], v[kRowsKeys * D];
+        float kf[NG * kRowsKeys], vf[NG * kRowsKeys];      // scales of a group's keys: 2^24 s / 128, s
+        __half kz[kRowsKeys * 8];                          // a key's z of the groups, twice
+        __half vz[8 * kVzRow];                             // z + 8 s of group i, row NG + i: its remainder
+    };
+    Tiles t[2];
+    alignas(128) unsigned char raw[kStages * kRaw];
+    int e[4];                                              // largest scale_exp of stage i mod 4
+    RowItems s;
+};
+
+// Pages of a split: about three items an SM.
+__device__ __forceinline__ int split_pages(long long work, int grid, int least)
+{
+    return ((int)max((long long)least, min(256ll, (work + 3 * grid - 1) / (3 * grid))) + 3) / 4 * 4;      // whole stages
+}
+__device__ __forceinline__ int rows_tiles(int cols) { return (cols + kRowsTile - 1) / kRowsTile; }
+
+// The items of the batch (256 threads): items prefix, and the split.
+__device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int least)
+{
+    constexpr int PER = kMaxB / 256;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int ql[PER], pages[PER], sum_q = 0, bad = 0;
+    long long work = 0;
+    if (tid == 0) s.bad = 0;
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int b = tid * PER + k;
+        ql[k] = pages[k] = 0;
+        if (b < p.B) {
+            ql[k] = p.q_lens ? p.q_lens[b] : p.Lq;
+            const int n = p.ctx_lens[b];
+            if (ql[k] < 0 || ql[k] > p.Lq || n < 0 || n > p.max_blocks * kBlock) bad = 1;      // (the context kernel reports it)
+            else pages[k] = (n + kBlock - 1) / kBlock;
+        }
+        sum_q += ql[k];
+        if (by_rows(ql[k] * p.G)) work += (long long)p.Hkv * rows_tiles(ql[k] * p.G) * pages[k];
+    }
+    int iq = sum_q;
+    long long iw = work;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, iq, off);
+        const long long tw = __shfl_up_sync(0xffffffffu, iw, off);
+        if (lane >= off) { iq += t; iw += tw; }
+    }
+    if (lane == 31) {
+        s.sum_q[warp] = iq;
+        s.sum[warp] = iw;
+    }
+    __syncthreads();
+    if (bad) s.bad = 1;
+    int bq = iq - sum_q;
+    long long total = 0;
+    for (int j = 0; j < 8; j++) {
+        if (j < warp) bq += s.sum_q[j];
+        total += s.sum[j];
+    }
+    const int split = split_pages(total, gridDim.x, least);
+    int n_it[PER], sum_i = 0;
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int b = tid * PER + k;
+        if (b < p.B) s.qo[b] = bq;
+        bq += ql[k];
+        n_it[k] = by_rows(ql[k] * p.G) ? p.Hkv * rows_tiles(ql[k] * p.G) * ((pages[k] + split - 1) / split) : 0;
+        sum_i += n_it[k];
+    }
+    if (tid == 255) s.qo[p.B] = bq;
+    __syncthreads();      // (the sums have been read)
+    int ii = sum_i;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, ii, off);
+        if (lane >= off) ii += t;
+    }
+    if (lane == 31) s.sum_q[warp] = ii;
+    __syncthreads();
+    int bi = ii - sum_i;
+    for (int j = 0; j < warp; j++) bi += s.sum_q[j];
+#pragma unroll
+    for (int k = 0; k < PER; k++) {
+        const int b = tid * PER + k;
+        if (b < p.B) s.it[b] = bi;
+        bi += n_it[k];
+    }
+    if (tid == 255) s.it[p.B] = bi;
+    __syncthreads();
+    return split;
+}
+
+// A stage's pieces of one thread: D / 64 pieces of codes, and a piece of the
+// pairs for the first 32 NG threads.
+template <int D, int GROUP>
+struct Pieces {
+    using S = RowsSmem<D, GROUP>;
+    static constexpr int kN = D * 4 / 256;             // pieces of codes
+    static constexpr int kPerRow = D / 32;
+    // piece i: K or V, key of the stage, 32 dimensions
+    static __device__ __forceinline__ void where(int i, int &kv, int &key, int &ch)
+    {
+        const int c = threadIdx.x + 256 * i;
+        kv = c / (kRowsKeys * kPerRow);
+        key = c / kPerRow % kRowsKeys;
+        ch = c % kPerRow;
+    }
+    static __device__ __forceinline__ void where_sz(int &kv, int &first)      // first pair, of 64 * NG
+    {
+        kv = threadIdx.x / (16 * S::NG);
+        first = threadIdx.x % (16 * S::NG) * 4;
+    }
+    // block ids of its pieces in the stage from page `page` on (-1: none or bad)
+    int blk[kN], blk_sz;
+    __device__ __forceinline__ void ids(const Params &p, const int *table, int page, int end)
+    {
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            int kv, key, ch;
+            where(i, kv, key, ch);
+            blk[i] = id(p, table, page + key / kBlock, end);
+        }
+        int kv, first;
+        where_sz(kv, first);
+        blk_sz = kv < 2 ? id(p, table, page + first / (kBlock * S::NG), end) : -1;
+    }
+    static __device__ __forceinline__ int id(const Params &p, const int *table, int page, int end)
+    {
+        int blk = -1;
+        if (page < end) {
+            blk = table[page];
+            if ((unsigned)blk >= (unsigned)p.num_blocks) {
+                atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
+                blk = -1;
+            }
+        }
+        return blk;
+    }
+    __device__ __forceinline__ void fetch(const Params &p, const Pool &pool, unsigned raw, int hk, int page, int n) const
+    {
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            int kv, key, ch;
+            where(i, kv, key, ch);
+            const size_t row = ((size_t)max(blk[i], 0) * p.Hkv + hk) * kBlock + key % kBlock;
+            copy16(raw + (threadIdx.x + 256 * i) * 16, (kv ? pool.v : pool.k) + row * (D / 2) + 16 * ch, blk[i] >= 0 ? 16 : 0, true);
+        }
+        int kv, first;
+        where_sz(kv, first);
+        const int in = first % (kBlock * S::NG);
+        const __half2 *src = (kv ? pool.vsz : pool.ksz) + ((size_t)max(blk_sz, 0) * p.Hkv + hk) * kBlock * S::NG + in;
+        // pairs of tokens behind the last one read as zero
+        const int rows = n - (page + first / (kBlock * S::NG)) * kBlock;
+        const int bytes = blk_sz < 0 ? 0 : min(16, max(0, (rows * S::NG - in) * 4));
+        copy16(raw + 2 * S::kCodes + threadIdx.x * 16, src, bytes, kv < 2);
+    }
+    // its pieces into the tiles
+    static __device__ __forceinline__ void unpack(typename S::Tiles &t, int *e, unsigned raw)
+    {
+        const __half2 bias = __floats2half2_rn(-1032.f, -1032.f);
+#pragma unroll
+        for (int i = 0; i < kN; i++) {
+            int kv, key, ch;
+            where(i, kv, key, ch);
+            const uint4 x = lds128(raw + (threadIdx.x + 256 * i) * 16);
+            const unsigned w[4] = {x.x, x.y, x.z, x.w};
+            __half *tile = kv ? t.v : t.k;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                unsigned o[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const unsigned c = (w[j] >> (4 * k)) & kLoCodes;
+                    if (kv) {
+                        const unsigned m = c | 0x64006400u;
+                        const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&m), bias);
+                        o[k] = *reinterpret_cast<const unsigned *>(&r);
+                    } else {
+                        o[k] = c;
+                    }
+                }
+                *reinterpret_cast<uint4 *>(tile + swz<D>(key, 4 * ch + j)) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        int kv, first, em = 0;
+        where_sz(kv, first);
+        if (kv < 2) {
+            const uint4 x = lds128(raw + 2 * S::kCodes + threadIdx.x * 16);
+            const unsigned w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const __half2 h = *reinterpret_cast<const __half2 *>(&w[j]);
+                const float2 f = __half22float2(h);
+                const int key = (first + j) / S::NG, gi = (first + j) % S::NG;
+                if (kv) {
+                    const float z = fmaf(8.f, f.x, f.y);
+                    const __half z16 = __float2half_rn(z);
+                    t.vf[gi * kRowsKeys + key] = f.x;
+                    t.vz[gi * kVzRow + key] = z16;
+                    t.vz[(S::NG + gi) * kVzRow + key] = __float2half_rn(z - __half2float(z16));
+                    em = max(em, scale_exp(h));
+                } else {
+                    t.kf[gi * kRowsKeys + key] = f.x * (0x1p24f * kQsScale);
+                    t.kz[key * 8 + gi] = t.kz[key * 8 + S::NG + gi] = __high2half(h);
+                }
+            }
+        }
+        em = (int)__reduce_max_sync(0xffffffffu, (unsigned)em);
+        if (em > 0 && (threadIdx.x & 31) == 0) atomicMax(e, em);
+    }
+};
+
+// A warp's 16 columns (rows g and g + 8 of its tiles).
+template <int D>
+struct RowsState {
+    float o[D / 8][4];
+    float z[4];               // columns 2t, 2t + 1: sum p hi(z + 8 s) of groups, then of the remainders
+    float m[2], l[2];
+    int e;
+};
+
+__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4_t(unsigned (&r)[4], unsigned a)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
+}
+
+// One stage for one warp.  FULL: every column sees every key of it.
+template <int D, int GROUP, bool FULL>
+__device__ __forceinline__ void rows_stage(const typename RowsSmem<D, GROUP>::Tiles &T, int stage_e, int lane,
+                                           const unsigned (&qf)[D / 16][4], const unsigned (&qz)[2], const int (&end)[2],
+                                           int key0, RowsState<D> &s, float scale, float slack)
+{
+    constexpr int NG = D / GROUP, KN = kRowsKeys / 8, NT = D / 8;
+    const int g = lane >> 2, t = lane & 3;
+    // addresses of swz(row, chunk): the chunk is an exclusive or away from the row's first one
+    const int kr = (lane & 7) + ((lane >> 4) << 3), vr = (lane & 7) + (((lane >> 3) & 1) << 3);
+    const unsigned ka = smem_u32(T.k) + kr * (2 * D) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
+    const unsigned va = smem_u32(T.v) + vr * (2 * D) + (((lane >> 4) ^ (lane & 7)) << 4);
+    float sc[KN][4];
+    const unsigned az[4] = {qz[0], qz[1], 0u, 0u};
+#pragma unroll
+    for (int nn = 0; nn < KN; nn++)
+        mma16816_first(sc[nn], az, *reinterpret_cast<const unsigned *>(&T.kz[(8 * nn + g) * 8 + 2 * t]), 0u);
+#pragma unroll
+    for (int gi = 0; gi < NG; gi++)
+#pragma unroll
+        for (int np = 0; np < KN / 2; np++) {
+            float acc[2][4];
+#pragma unroll
+            for (int kk = 0; kk < GROUP / 16; kk++) {
+                const int kt = gi * (GROUP / 16) + kk;
+                unsigned b[4];
+                ldsm4(b, (ka ^ (kt << 5)) + np * 16 * (2 * D));
+                if (kk == 0) {
+                    mma16816_first(acc[0], qf[kt], b[0], b[1]);
+                    mma16816_first(acc[1], qf[kt], b[2], b[3]);
+                } else {
+                    mma16816(acc[0], qf[kt], b[0], b[1]);
+                    mma16816(acc[1], qf[kt], b[2], b[3]);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const float2 f = *reinterpret_cast<const float2 *>(&T.kf[gi * kRowsKeys + 16 * np + 8 * h + 2 * t]);
+                float(&x)[4] = sc[2 * np + h];
+                x[0] = fmaf(acc[h][0], f.x, x[0]);
+                x[1] = fmaf(acc[h][1], f.y, x[1]);
+                x[2] = fmaf(acc[h][2], f.x, x[2]);
+                x[3] = fmaf(acc[h][3], f.y, x[3]);
+            }
+        }
+    if (!FULL) {
+#pragma unroll
+        for (int nn = 0; nn < KN; nn++)
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                if (key0 + 8 * nn + 2 * t + (e & 1) >= end[e >> 1]) sc[nn][e] = kNegInf;
+    }
+    bool moved = false;
+    float mn[2], mu[2];
+#pragma unroll
+    for (int r = 0; r < 2; r++) {
+        float mx = kNegInf;
+#pragma unroll
+        for (int nn = 0; nn < KN; nn++) mx = fmaxf(mx, fmaxf(sc[nn][2 * r], sc[nn][2 * r + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const bool move = mx > s.m[r] + slack;
+        mn[r] = move ? mx : s.m[r];
+        mu[r] = mn[r] == kNegInf ? 0.f : -mn[r] * scale;
+        moved = moved || move;
+    }
+    const int em = max(s.e, stage_e);
+    if (__any_sync(0xffffffffu, moved || em != s.e)) {
+        const float ae = __int_as_float((s.e - em + 127) << 23);
+        s.e = em;
+#pragma unroll
+        for (int r = 0; r < 2; r++) {
+            const float al = ex2(fmaf(s.m[r], scale, mu[r])), ao = al * ae;
+            s.m[r] = mn[r];
+            s.l[r] *= al;
+            s.z[2 * r] *= al;
+            s.z[2 * r + 1] *= al;
+#pragma unroll
+            for (int d = 0; d < NT; d++) {
+                s.o[d][2 * r] *= ao;
+                s.o[d][2 * r + 1] *= ao;
+            }
+        }
+    }
+    const float down = scale_down(em);
+#pragma unroll
+    for (int nn = 0; nn < KN; nn++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            sc[nn][e] = ex2(fmaf(sc[nn][e], scale, mu[e >> 1]));
+            s.l[e >> 1] += sc[nn][e];
+        }
+    // the group terms; an unseen key's may be a NaN, which must not meet its zero weight
+#pragma unroll
+    for (int ks = 0; ks < KN / 2; ks++) {
+        const unsigned pa[4] = {pack_half2(sc[2 * ks][0], sc[2 * ks][1]), pack_half2(sc[2 * ks][2], sc[2 * ks][3]),
+                                pack_half2(sc[2 * ks + 1][0], sc[2 * ks + 1][1]), pack_half2(sc[2 * ks + 1][2], sc[2 * ks + 1][3])};
+        unsigned bz[2];
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            bz[h] = *reinterpret_cast<const unsigned *>(&T.vz[g * kVzRow + 16 * ks + 8 * h + 2 * t]);
+            if (!FULL) {
+                if ((bz[h] & 0x7c00u) == 0x7c00u) bz[h] &= 0xffff0000u;
+                if ((bz[h] & 0x7c000000u) == 0x7c000000u) bz[h] &= 0x0000ffffu;
+            }
+        }
+        mma16816(s.z, pa, bz[0], bz[1]);
+    }
+    if (FULL) {
+#pragma unroll
+        for (int nn = 0; nn < KN; nn++)
+#pragma unroll
+            for (int e = 0; e < 4; e++) sc[nn][e] *= down;
+    }
+#pragma unroll
+    for (int gi = 0; gi < NG; gi++)
+#pragma unroll
+        for (int ks = 0; ks < KN / 2; ks++) {
+            unsigned pa[4];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int nn = 2 * ks + h, key = 8 * nn + 2 * t;
+                float2 f = *reinterpret_cast<const float2 *>(&T.vf[gi * kRowsKeys + key]);
+                float w[4];
+                if (FULL) {
+                    w[0] = sc[nn][0] * f.x;
+                    w[1] = sc[nn][1] * f.y;
+                    w[2] = sc[nn][2] * f.x;
+                    w[3] = sc[nn][3] * f.y;
+                } else {
+                    // a group whose z left the operand above has a NaN weight where the key is seen
+                    const unsigned b = *reinterpret_cast<const unsigned *>(&T.vz[gi * kVzRow + key]);
+                    if ((b & 0x7c00u) == 0x7c00u) f.x = __int_as_float(0x7fffffff);
+                    if ((b & 0x7c000000u) == 0x7c000000u) f.y = __int_as_float(0x7fffffff);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        w[e] = key0 + key + (e & 1) < end[e >> 1] ? sc[nn][e] * ((e & 1 ? f.y : f.x) * down) : 0.f;
+                }
+                pa[2 * h] = pack_half2(w[0], w[1]);
+                pa[2 * h + 1] = pack_half2(w[2], w[3]);
+            }
+#pragma unroll
+            for (int dd = 0; dd < GROUP / 16; dd++) {
+                const int dp = gi * (GROUP / 16) + dd;
+                unsigned b[4];
+                ldsm4_t(b, (va ^ (dp << 5)) + ks * 16 * (2 * D));
+                mma16816(s.o[2 * dp], pa, b[0], b[1]);
+                mma16816(s.o[2 * dp + 1], pa, b[2], b[3]);
+            }
+        }
+}
+
+template <int D, int GROUP>
+__global__ void __launch_bounds__(256, 1) rows_kernel(const __grid_constant__ Args a)
+{
+    using S = RowsSmem<D, GROUP>;
+    constexpr int NG = S::NG, KT = D / 16, NT = D / 8;
+    extern __shared__ __align__(256) unsigned char smem_rows[];
+    S &sm = *reinterpret_cast<S *>(smem_rows);
+    const Params &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    for (int k = 0; k < 2; k++) {      // rows and columns that no group has
+        for (int i = tid; i < kRowsKeys * 8; i += 256) sm.t[k].kz[i] = __ushort_as_half(0);
+        for (int i = tid; i < 8 * kVzRow; i += 256) sm.t[k].vz[i] = __ushort_as_half(0);
+    }
+    const int split = build_rows(p, sm.s, a.rows_least);
+    if (blockIdx.x == 0 && tid == 0) p.sched[2] = split;
+    const bool run = !sm.s.bad && sm.s.qo[p.B] <= p.max_q_total;
+    const int n_items = run ? sm.s.it[p.B] : 0;
+    const unsigned raw = smem_u32(sm.raw);
+    const float scale = p.scale_log2 * (1.f / kQsScale), slack = a.slack * kQsScale;
+
+    for (int item = blockIdx.x; item < n_items;) {
+        const int b = find_owner(sm.s.it, p.B, item);
+        const int n = p.ctx_lens[b], ql = sm.s.qo[b + 1] - sm.s.qo[b], cols = ql * p.G, pages = (n + kBlock - 1) / kBlock;
+        const int tiles = rows_tiles(cols);
+        int j = item - sm.s.it[b];
+        const int hk = j % p.Hkv;      // (KV heads next to each other: they share the split's length)
+        j /= p.Hkv;
+        const int tile = j % tiles, part = j / tiles;
+        const int v0 = tile * kRowsTile, vlast = min(cols, v0 + kRowsTile) - 1;
+        const int page0 = part * split;
+        const int end_page = min(min(page0 + split, pages), (keys_seen(n, ql, vlast / p.G) + kBlock - 1) / kBlock);
+        const int n_st = end_page > page0 ? (end_page - page0 + 3) / 4 : 0;
+        const int *table = p.block_tables + (size_t)b * p.max_blocks;
+        Pieces<D, GROUP> pc;
+        pc.ids(p, table, page0, end_page);
+        int fetched = 0;
+        auto fetch = [&]() {
+            if (fetched < n_st) {
+                pc.fetch(p, a.pool, raw + fetched % S::kStages * S::kRaw, hk, page0 + 4 * fetched, n);
+                fetched++;
+                if (fetched < n_st) pc.ids(p, table, page0 + 4 * fetched, end_page);
+            }
+            cp_async_commit();
+        };
+        for (int k = 0; k < S::kStages - 1; k++) fetch();
+
+        // the warp's 16 columns: rows g and g + 8 of its tiles
+        const int vw = v0 + 16 * warp;
+        const bool active = vw <= vlast;
+        unsigned qf[KT][4], qz[2];
+        int end[2];
+        const int key_end = end_page * kBlock;      // the split's keys end here
+        const int least = min(key_end, keys_seen(n, ql, min(vw, vlast) / p.G));
+        const int most = min(key_end, keys_seen(n, ql, min(vw + 15, vlast) / p.G));
+        {
+            const __half *q[2];
+            float sum[2][NG];
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                const int v = vw + g + 8 * r;
+                const int i = v / p.G, c = v - i * p.G;
+                q[r] = v <= vlast ? p.q + (((size_t)b * p.Lq + i) * p.H + hk * p.G + c) * D : nullptr;
+                end[r] = min(key_end, keys_seen(n, ql, min(v, vlast) / p.G));
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++) sum[r][gi] = 0.f;
+            }
+#pragma unroll
+            for (int kt = 0; kt < KT; kt++)
+#pragma unroll
+                for (int x = 0; x < 4; x++) {      // rows g, g + 8; words 2 kt, 2 kt + 1: dimensions t, t + 4
+                    const __half *src = q[x & 1];
+                    const int d = 16 * kt + 8 * (x >> 1) + t;
+                    __half2 h = __floats2half2_rn(0.f, 0.f);
+                    if (src) h = __halves2half2(src[d], src[d + 4]);
+                    qf[kt][x] = *reinterpret_cast<const unsigned *>(&h);
+                    const float2 f = __half22float2(h);
+                    sum[x & 1][16 * kt / GROUP] += f.x + f.y;
+                }
+            // the row's sums of the groups, then their remainders: columns 2t, 2t + 1 of the operand
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                __half w[2] = {__ushort_as_half(0), __ushort_as_half(0)};
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++) {
+                    float f = sum[r][gi];
+                    f += __shfl_xor_sync(0xffffffffu, f, 1);
+                    f += __shfl_xor_sync(0xffffffffu, f, 2);
+                    f *= kQsScale;
+                    const __half hi = __float2half_rn(f), lo = __float2half_rn(f - __half2float(hi));
+#pragma unroll
+                    for (int x = 0; x < 2; x++) {
+                        if (2 * t + x == gi) w[x] = hi;
+                        if (2 * t + x == NG + gi) w[x] = lo;
+                    }
+                }
+                const __half2 h = __halves2half2(w[0], w[1]);
+                qz[r] = *reinterpret_cast<const unsigned *>(&h);
+            }
+        }
+        RowsState<D> s;
+        s.e = 0;
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            s.z[e] = 0.f;
+#pragma unroll
+            for (int d = 0; d < NT; d++) s.o[d][e] = 0.f;
+        }
+        s.m[0] = s.m[1] = kNegInf;
+        s.l[0] = s.l[1] = 0.f;
+        if (tid < 4) sm.e[tid] = 0;
+        __syncthreads();
+        if (n_st > 0) {
+            cp_async_wait<S::kStages - 2>();
+            Pieces<D, GROUP>::unpack(sm.t[0], &sm.e[0], raw);
+            fetch();
+        }
+        __syncthreads();
+        for (int st = 0; st < n_st; st++) {
+            if (st + 1 < n_st) {
+                cp_async_wait<S::kStages - 2>();
+                Pieces<D, GROUP>::unpack(sm.t[(st + 1) & 1], &sm.e[(st + 1) & 3], raw + (st + 1) % S::kStages * S::kRaw);
+                fetch();
+            }
+            const int key0 = (page0 + 4 * st) * kBlock;
+            if (tid == 0) sm.e[(st + 2) & 3] = 0;      // (last read two stages ago, written in the next one)
+            if (active && key0 < most) {
+                if (key0 + kRowsKeys <= least)
+                    rows_stage<D, GROUP, true>(sm.t[st & 1], sm.e[st & 3], lane, qf, qz, end, key0, s, scale, slack);
+                else
+                    rows_stage<D, GROUP, false>(sm.t[st & 1], sm.e[st & 3], lane, qf, qz, end, key0, s, scale, slack);
+            }
+            __syncthreads();
+        }
+        cp_async_wait<0>();
+        if (active) {
+            const float up = __int_as_float((s.e - 15 + 127) << 23);      // 1 / scale_down
+#pragma unroll
+            for (int r = 0; r < 2; r++) {
+                float L = s.l[r];
+                L += __shfl_xor_sync(0xffffffffu, L, 1);
+                L += __shfl_xor_sync(0xffffffffu, L, 2);
+                const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), f = up * inv;
+                float zg[NG];
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++) {
+                    // columns gi and NG + gi of the row, two to a lane
+                    const float hi = __shfl_sync(0xffffffffu, s.z[2 * r + gi % 2], (lane & ~3) + gi / 2);
+                    const float lo = __shfl_sync(0xffffffffu, s.z[2 * r + (NG + gi) % 2], (lane & ~3) + (NG + gi) / 2);
+                    zg[gi] = (hi + lo) * inv;
+                }
+                const int v = vw + g + 8 * r;
+                if (v > vlast) continue;
+                const int i = v / p.G, h = hk * p.G + v - i * p.G;
+                const size_t pr = (size_t)a.rows0 + ((size_t)part * p.max_q_total + sm.s.qo[b] + i) * p.H + h;
+                float *po = p.part_o + pr * D;
+#pragma unroll
+                for (int d = 0; d < NT; d++) {
+                    __stcg(po + 8 * d + t, s.o[d][2 * r] * f + zg[8 * d / GROUP]);
+                    __stcg(po + 8 * d + t + 4, s.o[d][2 * r + 1] * f + zg[8 * d / GROUP]);
+                }
+                if (t == 0) __stcg(p.part_lse + pr, L == 0.f ? kNegInf : fmaf(s.m[r], scale, lg2(L)));
+            }
+        }
+        if (tid == 0) sm.s.next = (int)(gridDim.x + atomicAdd(&p.ctrl[CTRL_Q4_ROWS], 1u));
+        __syncthreads();
+        item = sm.s.next;
+        __syncthreads();
+    }
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+}
+
 // The prompt's partials beside it: the system items of the fp16 path (row
 // teams, the prompt read once per batch), in a grid of their own that lets the
 // context kernel start at once.
@@ -1656,6 +2248,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
     if (blockIdx.x == 0 && threadIdx.x == 0) {
         p.ctrl[CTRL_ROW_ITEMS] = 0u;
         p.ctrl[CTRL_DEC_ITEMS] = 0u;
+        p.ctrl[CTRL_Q4_ROWS] = 0u;
     }
     const Sched sc = sched_at(p.sched, p.B);
     const int w = blockIdx.x * kRows + warp / WPR, r = w / p.H, h = w - r * p.H;
@@ -1695,10 +2288,17 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
             c0 = f / Q;
             c1 = (f + pages - 1) / Q;
         }
-        const int n_sys = has_sys(p.mode) ? p.R_sys : 0, n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
+        const int n_sys = has_sys(p.mode) ? p.R_sys : 0;
+        int n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
         const size_t sys0 = sys_slot(p, 0, r, h), sys_st = (size_t)p.max_q_total * p.H;
-        const size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col;
-        auto slot = [&](int j) { return j < n_sys ? sys0 + j * sys_st : ctx0 + (size_t)(j - n_sys) * a.nc; };
+        size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col, ctx_st = a.nc;
+        if (by_rows(c.cols)) {
+            const int split = __ldcg(p.sched + 2);
+            n_parts = n_sys + (pages + split - 1) / split;
+            ctx0 = (size_t)a.rows0 + (size_t)r * p.H + h;
+            ctx_st = sys_st;
+        }
+        auto slot = [&](int j) { return j < n_sys ? sys0 + j * sys_st : ctx0 + (size_t)(j - n_sys) * ctx_st; };
         // this warp's parts: part, part + WPR, ...
         const int mine = (n_parts - part + WPR - 1) / WPR;
         for (int j0 = 0; j0 < mine; j0 += 32) {

@@ -112,6 +112,18 @@ Q4Kernel q4_kernel(int D, int group, long long cols)
     return group == 64 ? q4_instance<64, 64>(cols) : q4_instance<64, 32>(cols);
 }
 
+// The kernel of the prompt chunks in front of it.
+template <int D, int GROUP>
+Q4Kernel rows_instance()
+{
+    return {q4::rows_kernel<D, GROUP>, 8, sizeof(q4::RowsSmem<D, GROUP>)};
+}
+Q4Kernel rows_kernel(int D, int group)
+{
+    if (D == 128) return group == 128 ? rows_instance<128, 128>() : group == 64 ? rows_instance<128, 64>() : rows_instance<128, 32>();
+    return group == 64 ? rows_instance<64, 64>() : rows_instance<64, 32>();
+}
+
 // The kernel of the prompt's items beside it, for the key groups of a tile
 // (row_class; other values: any).
 using PromptKernel = void (*)(const Params);
@@ -129,8 +141,9 @@ cudaError_t prepare_q4()
         for (int group : {32, 64, 128})
             for (int cols : {1, 8, 16, 17}) {
                 if (group > D || e != cudaSuccess) continue;
-                const Q4Kernel k = q4_kernel(D, group, cols);
-                e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
+                for (const Q4Kernel &k : {q4_kernel(D, group, cols), rows_kernel(D, group)})
+                    if (e == cudaSuccess)
+                        e = cudaFuncSetAttribute(k.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)k.smem);
             }
         for (int kg : {0, 1, 2, 4})
             if (e == cudaSuccess)
@@ -1067,11 +1080,14 @@ relay_status_t check_q4(const relay_dims_t *d, const relay_q4_cache_t *c)
 // plan, then room for every chunk and every sequence of the line (q4::Args).
 struct PlanQ4 {
     Plan sys;
-    int nc = 0, q_min = 0;
+    int nc = 0, q_min = 0, rows_least = 0;
+    size_t rows0 = 0;
     size_t off_part_o = 0, off_part_lse = 0, total = 0;
 };
 constexpr int kQ4MinPages = 4;        // pages of a chunk, at least
 constexpr int kQ4MaxWarps = 16;       // warps of a context CTA, at most
+constexpr int kQ4RowsParts = 8;       // splits of a prompt chunk's context, at most
+constexpr int kQ4RowsPages = 32;      // pages of a split, at least
 
 PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
 {
@@ -1101,7 +1117,10 @@ PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
     pl.q_min = kQ4MinPages;
     const double line = (double)d->B * kv_heads(d) * tiles * d->max_blocks_per_seq;
     const long long chunks = (long long)std::min(line / kQ4MinPages + 1, 4.0 * kQ4MaxWarps * sms + 1);
-    const size_t rows = pl.sys.dec_base + (size_t)(chunks + seqs) * pl.nc;
+    pl.rows0 = pl.sys.dec_base + (size_t)(chunks + seqs) * pl.nc;
+    pl.rows_least = std::max(kQ4RowsPages, (d->max_blocks_per_seq + kQ4RowsParts - 1) / kQ4RowsParts);
+    const size_t parts = q4::by_rows(cols) ? (d->max_blocks_per_seq + pl.rows_least - 1) / pl.rows_least : 0;
+    const size_t rows = pl.rows0 + parts * pl.sys.Mtot * d->H;
     pl.off_part_o = pl.sys.off_sched + (q4::sched_bytes(d->B) + 255) / 256 * 256;
     pl.off_part_lse = pl.off_part_o + (rows * d->D * sizeof(float) + 255) / 256 * 256;
     pl.total = pl.off_part_lse + (rows * sizeof(float) + 255) / 256 * 256;
@@ -1144,6 +1163,8 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     a.nc = pl.nc;
     a.q_min = pl.q_min;
     a.part0 = (long long)pl.sys.dec_base;
+    a.rows0 = (long long)pl.rows0;
+    a.rows_least = pl.rows_least;
     a.slack = q4::kSlack / p.scale_log2;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1166,18 +1187,26 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
         if (cudaGetLastError() != cudaSuccess) return RELAY_ERR_CUDA;
         front = true;
     }
-    const Q4Kernel k = q4_kernel(d->D, cache->group, cols);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(dev->sms);
-    cfg.blockDim = dim3(32 * k.warps);
-    cfg.dynamicSmemBytes = k.smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = front ? 1 : 0;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k.fn, a);
+    auto launch = [&](const Q4Kernel &k) {
+        cfg.blockDim = dim3(32 * k.warps);
+        cfg.dynamicSmemBytes = k.smem;
+        cfg.numAttrs = front ? 1 : 0;
+        front = true;
+        return cudaLaunchKernelEx(&cfg, k.fn, a);
+    };
+    cudaError_t e = cudaSuccess;
+    if (q4::by_rows(cols)) {      // some request may be a prompt chunk
+        a.queue = 1;
+        e = launch(rows_kernel(d->D, cache->group));
+    }
+    if (e == cudaSuccess) e = launch(q4_kernel(d->D, cache->group, cols));
     if (e == cudaSuccess) {
         const long long rows = (long long)p.max_q_total * d->H;
         const bool shared = rows <= 32ll * dev->sms;      // (row, head) pairs: fewer than the GPU holds warps

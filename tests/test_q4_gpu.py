@@ -321,6 +321,14 @@ def test_long_contexts_of_one_request():
     check(c, run(c))
 
 
+def test_prompt_chunks_over_long_contexts():
+    """Prompt chunks whose contexts go to several splits, of a length that is no multiple of the kernel's stage."""
+    c = Case([4400, 700, 2100], [40, 1, 140], 2, 2, 128, 128, 20, seed=5)
+    check(c, run(c))
+    c = Case([2500, 4337], [50, 33], 6, 3, 64, 32, 0, seed=6)
+    check(c, run(c, "ctx"), "ctx")
+
+
 def test_many_requests():
     r = np.random.default_rng(8)
     c = Case(list(r.integers(0, 60, 512)), [1] * 512, 2, 1, 64, 32, 40, seed=9)
