@@ -302,6 +302,7 @@ struct Args {
     float slack;              // kSlack in units of q . k
     long long rows0;          // first partial row of the prompt chunks: (split * max_q_total + row) * H + head
     int rows_least;           // pages of a chunk's split, at least
+    int rows_max;             // columns of a request on the line, at most
 };
 
 // Handed to the merge kernel (the words of Sched's header: bad, Q, the pages
@@ -320,12 +321,11 @@ __device__ __forceinline__ Sched sched_at(int *base, int B)
     return s;
 }
 
-// Requests of more than kRowsMin columns are not on the line: they have CTAs of
-// their own (rows_kernel).
-constexpr int kRowsMin = 32, kRowsTile = 128, kRowsKeys = 64;
+// Requests of more than Args::rows_max columns are not on the line: they have
+// CTAs of their own (rows_kernel).
+constexpr int kRowsTile = 128, kRowsKeys = 64;
 constexpr int kVzRow = kRowsKeys + 8;      // (rows of halves that meet no bank twice)
 constexpr int CTRL_Q4_ROWS = 7;      // ctrl word: row items taken
-__host__ __device__ inline bool by_rows(long long cols) { return cols > kRowsMin; }
 
 // Columns of a request: query row i and head c of the group are column i G +
 // c, in tiles of 8 * nt: one, two or four tensor-core tiles, as many as they
@@ -448,7 +448,7 @@ __device__ __forceinline__ int pages_seen(const Params &p, const Seq &q)
 
 // The line of the batch, built by the whole CTA (W warps).
 template <int W>
-__device__ void build_line(const Params &p, Smem4 &s)
+__device__ void build_line(const Params &p, Smem4 &s, int rows_max)
 {
     constexpr int PER = (kMaxB + 32 * W - 1) / (32 * W);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -466,7 +466,7 @@ __device__ void build_line(const Params &p, Smem4 &s)
             if (ql[k] < 0 || ql[k] > p.Lq) { flags |= FLAG_BAD_Q_LEN; ql[k] = 0; }
             if (n[k] < 0 || n[k] > p.max_blocks * kBlock) { flags |= FLAG_BAD_CTX_LEN; ql[k] = n[k] = 0; }
         }
-        sq[k] = by_rows(ql[k] * p.G) ? 0 : p.Hkv * cols_of(ql[k], p.G).tiles;
+        sq[k] = ql[k] * p.G > rows_max ? 0 : p.Hkv * cols_of(ql[k], p.G).tiles;
         pg[k] = (long long)sq[k] * ((n[k] + kBlock - 1) / kBlock);
         sum_q += ql[k];
         sum_s += sq[k];
@@ -1536,7 +1536,7 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     ch.count = 1;      // (asked for before the number of chunks is known)
     ch.queue0 = 0;
     if (a.queue) ch.ask(p);
-    build_line<G::kW>(p, s);
+    build_line<G::kW>(p, s, a.rows_max);
     const long long total = s.pre[p.B], workers = (long long)gridDim.x * G::kW;
     // pages of a chunk: one chunk a warp up to 24 pages (two where the warps
     // do not start together), then two or three: finer ones balance better,
@@ -1611,7 +1611,7 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
 }
 
 // ----------------------------------------------------------------------------- attention: prompt chunks
-// Requests of more than kRowsMin columns: a CTA takes 128 columns of one KV
+// Requests of more columns than the line takes: a CTA takes 128 columns of one KV
 // head against a range of the context, and the unpacking is shared by all of
 // them.  A stage is 64 keys: every thread fetches its own 16-byte pieces of
 // the codes and of the pairs some stages ahead, unpacks them into fp16 tiles
@@ -1656,7 +1656,7 @@ __device__ __forceinline__ int split_pages(long long work, int grid, int least)
 __device__ __forceinline__ int rows_tiles(int cols) { return (cols + kRowsTile - 1) / kRowsTile; }
 
 // The items of the batch (256 threads): items prefix, and the split.
-__device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int least)
+__device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int least, int rows_max)
 {
     constexpr int PER = kMaxB / 256;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -1674,7 +1674,7 @@ __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int leas
             else pages[k] = (n + kBlock - 1) / kBlock;
         }
         sum_q += ql[k];
-        if (by_rows(ql[k] * p.G)) work += (long long)p.Hkv * rows_tiles(ql[k] * p.G) * pages[k];
+        if (ql[k] * p.G > rows_max) work += (long long)p.Hkv * rows_tiles(ql[k] * p.G) * pages[k];
     }
     int iq = sum_q;
     long long iw = work;
@@ -1703,7 +1703,7 @@ __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int leas
         const int b = tid * PER + k;
         if (b < p.B) s.qo[b] = bq;
         bq += ql[k];
-        n_it[k] = by_rows(ql[k] * p.G) ? p.Hkv * rows_tiles(ql[k] * p.G) * ((pages[k] + split - 1) / split) : 0;
+        n_it[k] = ql[k] * p.G > rows_max ? p.Hkv * rows_tiles(ql[k] * p.G) * ((pages[k] + split - 1) / split) : 0;
         sum_i += n_it[k];
     }
     if (tid == 255) s.qo[p.B] = bq;
@@ -2035,7 +2035,7 @@ __global__ void __launch_bounds__(256, 1) rows_kernel(const __grid_constant__ Ar
         for (int i = tid; i < kRowsKeys * 8; i += 256) sm.t[k].kz[i] = __ushort_as_half(0);
         for (int i = tid; i < 8 * kVzRow; i += 256) sm.t[k].vz[i] = __ushort_as_half(0);
     }
-    const int split = build_rows(p, sm.s, a.rows_least);
+    const int split = build_rows(p, sm.s, a.rows_least, a.rows_max);
     if (blockIdx.x == 0 && tid == 0) p.sched[2] = split;
     const bool run = !sm.s.bad && sm.s.qo[p.B] <= p.max_q_total;
     const int n_items = run ? sm.s.it[p.B] : 0;
@@ -2292,7 +2292,7 @@ __global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args
         int n_parts = n_sys + (pages > 0 ? (int)(c1 - c0) + 1 : 0);
         const size_t sys0 = sys_slot(p, 0, r, h), sys_st = (size_t)p.max_q_total * p.H;
         size_t ctx0 = (size_t)a.part0 + (size_t)(c0 + seq + at) * a.nc + col, ctx_st = a.nc;
-        if (by_rows(c.cols)) {
+        if (c.cols > a.rows_max) {
             const int split = __ldcg(p.sched + 2);
             n_parts = n_sys + (pages + split - 1) / split;
             ctx0 = (size_t)a.rows0 + (size_t)r * p.H + h;

@@ -1081,6 +1081,8 @@ relay_status_t check_q4(const relay_dims_t *d, const relay_q4_cache_t *c)
 struct PlanQ4 {
     Plan sys;
     int nc = 0, q_min = 0, rows_least = 0;
+    int rows_max = INT_MAX;               // columns of a request on the line, at most
+    long long line_cols = 0;              // ... that this shape has
     size_t rows0 = 0;
     size_t off_part_o = 0, off_part_lse = 0, total = 0;
 };
@@ -1110,16 +1112,20 @@ PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
     pl.sys.ctx_tc = false;
     pl.sys.ctx_pairs = 0;
     pl.sys.n_tc_ctx = 0;
-    // a request of c columns has ceil(c / 32) sequences a KV head, one up to 32
-    const long long cols = (long long)d->Lq * G, tiles = (cols + 31) / 32;
-    const long long seqs = kv_heads(d) * std::min((long long)d->B * tiles, (long long)pl.sys.Mtot * G / 32 + d->B);
-    pl.nc = (int)std::min(cols, cols <= 8 ? 8ll : cols <= 16 ? 16ll : 32ll);
+    // Up to 32 columns a request is one sequence a KV head.  With more (prompt
+    // chunks), the requests of several rows go to the row items, and the line
+    // keeps what the columns of single rows need anyway.
+    const long long cols = (long long)d->Lq * G;
+    if (cols > 32) pl.rows_max = G <= 8 ? 8 : G <= 16 ? 16 : 32;
+    pl.line_cols = std::min<long long>(cols, pl.rows_max);
+    const long long seqs = (long long)kv_heads(d) * d->B;
+    pl.nc = (int)pl.line_cols;
     pl.q_min = kQ4MinPages;
-    const double line = (double)d->B * kv_heads(d) * tiles * d->max_blocks_per_seq;
+    const double line = (double)seqs * d->max_blocks_per_seq;
     const long long chunks = (long long)std::min(line / kQ4MinPages + 1, 4.0 * kQ4MaxWarps * sms + 1);
     pl.rows0 = pl.sys.dec_base + (size_t)(chunks + seqs) * pl.nc;
     pl.rows_least = std::max(kQ4RowsPages, (d->max_blocks_per_seq + kQ4RowsParts - 1) / kQ4RowsParts);
-    const size_t parts = q4::by_rows(cols) ? (d->max_blocks_per_seq + pl.rows_least - 1) / pl.rows_least : 0;
+    const size_t parts = cols > pl.rows_max ? (d->max_blocks_per_seq + pl.rows_least - 1) / pl.rows_least : 0;
     const size_t rows = pl.rows0 + parts * pl.sys.Mtot * d->H;
     pl.off_part_o = pl.sys.off_sched + (q4::sched_bytes(d->B) + 255) / 256 * 256;
     pl.off_part_lse = pl.off_part_o + (rows * d->D * sizeof(float) + 255) / 256 * 256;
@@ -1136,8 +1142,8 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     if (!aligned(ws, 256)) return RELAY_ERR_INVALID_ARG;
     if (ws_bytes < make_plan_q4(d, mode, 1).total) return RELAY_ERR_WORKSPACE;
     if (!p.q_lens && (long long)d->B * d->Lq > make_plan(d, mode, 1).Mtot) return RELAY_ERR_INVALID_ARG;
-    const long long cols = (long long)d->Lq * (d->H / kv_heads(d));
-    if ((double)kv_heads(d) * ((cols + 7) / 8) * d->max_blocks_per_seq > INT_MAX ||
+    // 32-bit positions within a request, and pages of a head
+    if ((double)kv_heads(d) * ((double)d->Lq * (d->H / kv_heads(d)) / 8 + 1) * d->max_blocks_per_seq > INT_MAX ||
         (double)d->num_blocks * kv_heads(d) > INT_MAX)
         return RELAY_ERR_UNSUPPORTED;
     const DevInfo *dev = nullptr;
@@ -1165,6 +1171,7 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     a.part0 = (long long)pl.sys.dec_base;
     a.rows0 = (long long)pl.rows0;
     a.rows_least = pl.rows_least;
+    a.rows_max = pl.rows_max;
     a.slack = q4::kSlack / p.scale_log2;
 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -1202,11 +1209,11 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
         return cudaLaunchKernelEx(&cfg, k.fn, a);
     };
     cudaError_t e = cudaSuccess;
-    if (q4::by_rows(cols)) {      // some request may be a prompt chunk
+    if (pl.rows_max < INT_MAX) {      // some request may be a prompt chunk
         a.queue = 1;
         e = launch(rows_kernel(d->D, cache->group));
     }
-    if (e == cudaSuccess) e = launch(q4_kernel(d->D, cache->group, cols));
+    if (e == cudaSuccess) e = launch(q4_kernel(d->D, cache->group, pl.line_cols));
     if (e == cudaSuccess) {
         const long long rows = (long long)p.max_q_total * d->H;
         const bool shared = rows <= 32ll * dev->sms;      // (row, head) pairs: fewer than the GPU holds warps
