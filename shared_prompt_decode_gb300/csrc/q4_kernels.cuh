@@ -284,6 +284,35 @@ __device__ __forceinline__ void copy16(unsigned to, const void *from, int n, boo
                  "l"(from), "r"(n), "r"((unsigned)go)
                  : "memory");
 }
+// A lane's pieces of one page's codes: N of K and N of V, 512 bytes apart
+// (V's behind the page's K codes), n bytes each.
+template <int N, int CODES, bool ALWAYS>
+__device__ __forceinline__ void copy_codes(unsigned to, const void *k, const void *v, int n, bool go)
+{
+    static_assert(N == 1 || N == 2, "D = 64, 128");
+    if constexpr (ALWAYS) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %3;\n cp.async.cg.shared.global [%0 + %4], [%2], 16, %3;" ::"r"(to),
+                     "l"(k), "l"(v), "r"(n), "n"(CODES)
+                     : "memory");
+        if constexpr (N == 2)
+            asm volatile("cp.async.cg.shared.global [%0 + 512], [%1 + 512], 16, %3;\n"
+                         " cp.async.cg.shared.global [%0 + %4], [%2 + 512], 16, %3;" ::"r"(to),
+                         "l"(k), "l"(v), "r"(n), "n"(CODES + 512)
+                         : "memory");
+    } else if constexpr (N == 2) {
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+                     " @p cp.async.cg.shared.global [%0], [%1], 16, %3;\n @p cp.async.cg.shared.global [%0 + %5], [%2], 16, %3;\n"
+                     " @p cp.async.cg.shared.global [%0 + 512], [%1 + 512], 16, %3;\n"
+                     " @p cp.async.cg.shared.global [%0 + %6], [%2 + 512], 16, %3; }" ::"r"(to),
+                     "l"(k), "l"(v), "r"(n), "r"((unsigned)go), "n"(CODES), "n"(CODES + 512)
+                     : "memory");
+    } else {
+        asm volatile("{ .reg .pred p; setp.ne.u32 p, %4, 0;\n"
+                     " @p cp.async.cg.shared.global [%0], [%1], 16, %3;\n @p cp.async.cg.shared.global [%0 + %5], [%2], 16, %3; }" ::"r"(to),
+                     "l"(k), "l"(v), "r"(n), "r"((unsigned)go), "n"(CODES)
+                     : "memory");
+    }
+}
 
 // ----------------------------------------------------------------------------- attention: work
 // The context work as one line of pages: for every request, KV head and tile
@@ -379,14 +408,8 @@ struct Smem4 {
 constexpr size_t kMaxSmem = 227 * 1024;
 template <int D, int GROUP, int NT>
 struct Geo {
-#ifndef KPER
-#define KPER 2
-#endif
-    static constexpr int kPer = NT > 1 || (D == 128 && GROUP == 32) ? 2 : KPER;
-#ifndef KW
-#define KW 12
-#endif
-    static constexpr int kW = NT > 1 ? 8 : D == 128 ? (GROUP == 32 && KW > 12 ? 12 : KW) : 16;
+    static constexpr int kPer = 2;
+    static constexpr int kW = NT > 1 ? 8 : D == 128 ? 12 : 16;
     static constexpr int kStep = kPer * PageQ<D, GROUP>::kPage;
     static constexpr int kQ = NT > 1 ? NT * (D / 32) * 512 : 0;      // a warp's query operands in shared memory
     static constexpr int kFit = (int)((kMaxSmem - offsetof(Smem4, ring) - kW * kQ) / (kW * kStep));
@@ -650,7 +673,7 @@ __device__ __forceinline__ void q_sums(const unsigned (&qb)[NT][D / 16][2], Vec<
 // tokens.  The codes are copied whole (what lies behind the last token is a
 // number either way); the pairs of further tokens read as zero, so that
 // nothing of them is left.  A block id of -1 (block_ids) reads as zero.
-template <int D, int GROUP>
+template <int D, int GROUP, bool ALWAYS>
 __device__ __forceinline__ void load_page(const Params &p, const Pool &pool, const Lane<D, GROUP> &ln, unsigned st, int blk,
                                           int hk, int rows, bool go)
 {
@@ -659,12 +682,7 @@ __device__ __forceinline__ void load_page(const Params &p, const Pool &pool, con
     const unsigned page = max(blk, 0) * p.Hkv + hk;      // the host keeps the pool below 2^31 of them
     const unsigned long long off = (unsigned long long)page * P::kCodes + ln.at;
     const unsigned char *kc = pool.k + off, *vc = pool.v + off;
-    const unsigned to = st + ln.to;
-#pragma unroll
-    for (int k = 0; k < P::kCodes / 512; k++) {
-        copy16(to + 512 * k, kc + 512 * k, all, go);
-        copy16(to + P::kCodes + 512 * k, vc + 512 * k, all, go);
-    }
+    copy_codes<P::kCodes / 512, P::kCodes, ALWAYS>(st + ln.to, kc, vc, all, go);
     constexpr int kChunks = P::kSz / 16;      // of K, then of V
     const int n = min(all, max(0, rows * P::NG * 4 - 16 * (ln.lane % kChunks)));
     copy16(st + 2 * P::kCodes + 16 * ln.lane, ln.szc + (unsigned long long)page * P::kSz, n, go && ln.lane < 2 * kChunks);
@@ -1396,10 +1414,12 @@ struct Loader {
                 window = page;
                 blk = block_id(a.p, table, window + ln.lane, end);
             }
+            load_page<D, GROUP, true>(a.p, a.pool, ln, at, __shfl_sync(0xffffffffu, blk, page - window), hk, n - page * kBlock,
+                                      true);
 #pragma unroll
-            for (int j = 0; j < KP; j++)
-                load_page<D, GROUP>(a.p, a.pool, ln, at + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window), hk,
-                                    n - (page + j) * kBlock, j == 0 || page + j < end);
+            for (int j = 1; j < KP; j++)
+                load_page<D, GROUP, false>(a.p, a.pool, ln, at + j * P::kPage, __shfl_sync(0xffffffffu, blk, page + j - window),
+                                           hk, n - (page + j) * kBlock, page + j < end);
             page += KP;
             at = at + KP * P::kPage == ring + STAGES * KP * P::kPage ? ring : at + KP * P::kPage;
             issued++;
@@ -1542,10 +1562,7 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     // do not start together), then two or three: finer ones balance better,
     // and cost partials
     const long long per = (total + workers - 1) / workers;
-#ifndef PARTS
-#define PARTS (per <= 24 ? 1 + a.queue : 2 + a.queue)
-#endif
-    const int parts = PARTS;
+    const int parts = per <= 24 ? 1 + a.queue : 2 + a.queue;
     const int Q = (int)max((long long)a.q_min, (total + workers * parts - 1) / (workers * parts));
     const unsigned bad = (unsigned)s.bad | (s.qo[p.B] > p.max_q_total ? FLAG_Q_TOTAL : 0u);
     if (blockIdx.x == 0) {
@@ -2209,10 +2226,9 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         const int b = threadIdx.x * PER + k;
         ql[k] = 0;
         if (b < p.B) {
-            ql[k] = p.q_lens ? p.q_lens[b] : p.Lq;
-            const int n = p.ctx_lens[b];
             // a bad length fails the whole call (the context kernel reports it)
-            if (ql[k] < 0 || ql[k] > p.Lq || n < 0 || n > p.max_blocks * kBlock) ql[k] = 0;
+            ql[k] = p.q_lens ? p.q_lens[b] : p.Lq;
+            if (ql[k] < 0 || ql[k] > p.Lq) ql[k] = 0;
         }
     }
     block_scan<D, PER>(ql, s.qo, p.B, s);
@@ -2234,10 +2250,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 // context's partials by their log-sum-exps, as merge_kernel of the fp16 path
 // does.  With few rows it is one memory round trip after another, so four
 // warps share a row's parts; with many rows one warp a row moves the bytes.
-template <int D, int WPR>
-__global__ void __launch_bounds__(256) merge_kernel(const __grid_constant__ Args a)
+template <int D, int WPR, int CH>
+__global__ void __launch_bounds__(256, CH > 8 ? 2 : 3) merge_kernel(const __grid_constant__ Args a)
 {
-    constexpr int V = D / 32, CH = 8, kRows = 8 / WPR;
+    constexpr int V = D / 32, kRows = 8 / WPR;      // CH: partial rows in flight per warp
     constexpr float kLn2 = 0.69314718055994531f;
     __shared__ int qo[kMaxB + 1];
     __shared__ float sm_m[8], sm_w[8];

@@ -1098,14 +1098,10 @@ PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
     relay_dims_t ds = *d;
     const long long rows_v = (long long)(d->max_q_total > 0 ? d->max_q_total : d->B * d->Lq) * G;
     if (mode == MODE_FUSED && d->Ls > 0 && d->sys_range == 0 && !(d->D == 128 && rows_v > kTcMinRows)) {
-        // the prompt's items beside the contexts: a team each on half the SMs
-        // (there is no other work for the teams of such a CTA), but ranges of
-        // at least 128 keys
+        // the prompt's items run alone (the contexts follow on each SM as its
+        // CTA leaves): a team each, but ranges of at least 128 keys
         const long long tiles = (rows_v + kTileM - 1) / kTileM;
-        #ifndef WANTMUL
-#define WANTMUL 2
-#endif
-        const long long want = std::max(1ll, WANTMUL * (long long)sms / (kv_heads(d) * tiles));
+        const long long want = std::max(1ll, (long long)kTeams * sms / (kv_heads(d) * tiles));
         ds.sys_range = std::max(128, round_up((int)((d->Ls + want - 1) / want), kTileK));
     }
     pl.sys = make_plan(&ds, mode, sms);
@@ -1183,14 +1179,7 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
         a.queue = 1;
     } else if (mode == MODE_FUSED && p.R_sys > 0) {
         const int kg = p.q_lens || d->Lq != 1 ? 0 : row_class(d, pl.sys, MODE_SYS, p.G, false);
-        const long long items = (long long)p.Hkv * (((long long)p.max_q_total * p.G + kTileM - 1) / kTileM) * p.R_sys;
-#ifndef HALFGRID
-        const int grid = dev->sms;
-#else
-        const int grid = (int)std::min<long long>((items + kTeams - 1) / kTeams, dev->sms);
-#endif
-        a.queue = grid < dev->sms;
-        prompt_kernel(d->D, kg)<<<grid, kThreads, d->D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>), s>>>(p);
+        prompt_kernel(d->D, kg)<<<dev->sms, kThreads, d->D == 128 ? sizeof(Smem<128>) : sizeof(Smem<64>), s>>>(p);
         if (cudaGetLastError() != cudaSuccess) return RELAY_ERR_CUDA;
         front = true;
     }
@@ -1216,13 +1205,17 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     if (e == cudaSuccess) e = launch(q4_kernel(d->D, cache->group, pl.line_cols));
     if (e == cudaSuccess) {
         const long long rows = (long long)p.max_q_total * d->H;
-        const bool shared = rows <= 32ll * dev->sms;      // (row, head) pairs: fewer than the GPU holds warps
-        cfg.gridDim = dim3((unsigned)(shared ? (rows + 1) / 2 : (rows + 7) / 8));
+        // a few rows: four warps each; up to a GPU full of warps: one each, with all
+        // of a row's usual partials in flight; more: fewer in flight, more warps
+        const int wpr = rows <= 2ll * dev->sms ? 4 : 1;
+        const bool deep = rows <= 32ll * dev->sms;
+        cfg.gridDim = dim3((unsigned)((rows + 8 / wpr - 1) / (8 / wpr)));
         cfg.blockDim = dim3(256);
         cfg.dynamicSmemBytes = 0;
         cfg.numAttrs = 1;
-        void (*fn)(const q4::Args) = d->D == 128 ? (shared ? q4::merge_kernel<128, 4> : q4::merge_kernel<128, 1>)
-                                                 : (shared ? q4::merge_kernel<64, 4> : q4::merge_kernel<64, 1>);
+        void (*fn)(const q4::Args);
+        if (d->D == 128) fn = wpr == 4 ? q4::merge_kernel<128, 4, 8> : deep ? q4::merge_kernel<128, 1, 16> : q4::merge_kernel<128, 1, 8>;
+        else fn = wpr == 4 ? q4::merge_kernel<64, 4, 8> : deep ? q4::merge_kernel<64, 1, 16> : q4::merge_kernel<64, 1, 8>;
         e = cudaLaunchKernelEx(&cfg, fn, a);
     }
     if (e != cudaSuccess) {
@@ -1444,12 +1437,19 @@ relay_status_t relay_rope_axes(const relay_dims_t *dims, const void *q, const vo
     a.H = dims->H;
     a.Hkv = k_new ? kv_heads(dims) : 0;
     a.Ls = dims->Ls;
-    for (int j = 0; j < half; j++) {
-        // below a sixth of a turn per position, so the fraction fits 64 bits
-        const double turns = std::pow((double)base, -2.0 * j / dims->D) / 6.283185307179586476925286766559;
-        a.turn[j] = (unsigned long long)std::ldexp(turns, 64);
-        a.axis[j] = pair_axis[j];
+    // the turns of the last base and head dimension (a model has one)
+    static thread_local struct { float base = 0.f; int D = 0; unsigned long long turn[kMaxRopePairs]; } table;
+    if (table.base != base || table.D != dims->D) {
+        for (int j = 0; j < half; j++) {
+            // below a sixth of a turn per position, so the fraction fits 64 bits
+            const double turns = std::pow((double)base, -2.0 * j / dims->D) / 6.283185307179586476925286766559;
+            table.turn[j] = (unsigned long long)std::ldexp(turns, 64);
+        }
+        table.base = base;
+        table.D = dims->D;
     }
+    std::copy(table.turn, table.turn + half, a.turn);
+    std::copy(pair_axis, pair_axis + half, a.axis);
     a.q = static_cast<const __half *>(q);
     a.k = static_cast<const __half *>(k_new);
     a.q_out = static_cast<__half *>(q_out);
