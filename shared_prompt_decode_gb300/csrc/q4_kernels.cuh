@@ -831,34 +831,36 @@ __device__ __forceinline__ void step(unsigned st, const Lane<D, GROUP> &ln, int 
             for (int nt = 0; nt < NT; nt++) sc[j][nt][0] = sc[j][nt][1] = Vec<E>::all(kNegInf);
         }
     }
-    // online softmax per column (keys over the lanes' g), the running maximum
-    // in units of q . k (the scale is positive)
+    // Online softmax per column (keys over the lanes' g).  The reference of the
+    // weights moves only when some score is past it by more than 2^kSlack (up
+    // to that the weights are as exact), and the V scales' common power of
+    // two, which makes p s / 2^e fill fp16 from the top, only when a scale is
+    // past it: the lanes look at their own keys, and one vote in most steps
+    // finds that nothing has moved.  (m is in units of q . k; the softmax scale
+    // is positive.)
+    if (!FULL) {
+#pragma unroll
+        for (int j = 0; j < KP; j++)
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    if (16 * j + g >= end[nt][e]) sc[j][nt][0][e] = kNegInf;
+                    if (16 * j + g + 8 >= end[nt][e]) sc[j][nt][1][e] = kNegInf;
+                }
+    }
+    Vec<E> mx[NT];
     bool moved = false;
-    Vec<E> mn[NT], mu[NT];      // (mu: minus the maximum, in powers of two)
 #pragma unroll
     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
         for (int e = 0; e < E; e++) {
-            float mx = kNegInf;
+            float x = kNegInf;
 #pragma unroll
-            for (int j = 0; j < KP; j++) {
-                if (!FULL) {
-                    if (16 * j + g >= end[nt][e]) sc[j][nt][0][e] = kNegInf;
-                    if (16 * j + g + 8 >= end[nt][e]) sc[j][nt][1][e] = kNegInf;
-                }
-                mx = fmaxf(mx, fmaxf(sc[j][nt][0][e], sc[j][nt][1][e]));
-            }
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            // a reference that the maximum has left by less than 2^kSlack is
-            // kept: weights up to that are as exact, and most steps rescale nothing
-            const float m = s.m[nt][e];
-            const bool move = mx > m + slack;      // (always, from minus infinity to a number)
-            mn[nt][e] = move ? mx : m;
-            mu[nt][e] = mn[nt][e] == kNegInf ? 0.f : -mn[nt][e] * scale_log2;
-            moved = moved || move;
+            for (int j = 0; j < KP; j++) x = fmaxf(x, fmaxf(sc[j][nt][0][e], sc[j][nt][1][e]));
+            mx[nt][e] = x;
+            moved = moved || x > s.m[nt][e] + slack;      // (any number is past minus infinity)
         }
-    // the V scales' common power of two: p s / 2^e fills fp16 from the top
     __half2 h[KP][2][NG];
     int em = 0;
 #pragma unroll
@@ -878,16 +880,20 @@ __device__ __forceinline__ void step(unsigned st, const Lane<D, GROUP> &ln, int 
         for (int i = 1; i < KP * 2 * NG; i++) top = __hmax2(top, __habs2(h[i / (2 * NG)][i / NG % 2][i % NG]));
         em = scale_exp(top);
     }
-    em = max(s.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)em));
-    if (__any_sync(0xffffffffu, moved || em != s.e)) {
+    if (__any_sync(0xffffffffu, moved || em > s.e)) {
+        em = max(s.e, (int)__reduce_max_sync(0xffffffffu, (unsigned)em));
         const float ae = __int_as_float((s.e - em + 127) << 23);
         s.e = em;
 #pragma unroll
         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
             for (int e = 0; e < E; e++) {
-                const float al = ex2(fmaf(s.m[nt][e], scale_log2, mu[nt][e])), ao = al * ae;
-                s.m[nt][e] = mn[nt][e];
+                float x = mx[nt][e];
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+                const float old = s.m[nt][e], m = fmaxf(old, x);
+                s.m[nt][e] = m;
+                const float al = m == kNegInf ? 1.f : ex2((old - m) * scale_log2), ao = al * ae;
                 s.l[nt][e] *= al;
 #pragma unroll
                 for (int gi = 0; gi < NG; gi++) {
@@ -901,6 +907,12 @@ __device__ __forceinline__ void step(unsigned st, const Lane<D, GROUP> &ln, int 
                 }
             }
     }
+    Vec<E> mu[NT];      // minus the reference, in powers of two
+#pragma unroll
+    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+        for (int e = 0; e < E; e++) mu[nt][e] = s.m[nt][e] == kNegInf ? 0.f : -s.m[nt][e] * scale_log2;
+    em = s.e;
     const float down = scale_down(em);
 #pragma unroll
     for (int j = 0; j < KP; j++) {
