@@ -27,6 +27,7 @@
 
 #include "relay_kernels.cuh"
 #include "step_kernels.cuh"
+#include "sys_tc.cuh"
 
 namespace relay {
 namespace q4 {
@@ -353,7 +354,6 @@ __device__ __forceinline__ Sched sched_at(int *base, int B)
 // Requests of more than Args::rows_max columns are not on the line: they have
 // CTAs of their own (rows_kernel).
 constexpr int kRowsTile = 128, kRowsKeys = 64;
-constexpr int kVzRow = kRowsKeys + 8;      // (rows of halves that meet no bank twice)
 constexpr int CTRL_Q4_ROWS = 7;      // ctrl word: row items taken
 
 // Columns of a request: query row i and head c of the group are column i G +
@@ -1640,42 +1640,84 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
 }
 
 // ----------------------------------------------------------------------------- attention: prompt chunks
-// Requests of more columns than the line takes: a CTA takes 128 columns of one KV
-// head against a range of the context, and the unpacking is shared by all of
-// them.  A stage is 64 keys: every thread fetches its own 16-byte pieces of
-// the codes and of the pairs some stages ahead, unpacks them into fp16 tiles
-// (K as c * 2^-24, V as c - 8, both exact) and tables of scales, and the eight
-// warps, 16 columns each, run over the tiles like over fp16 ones:
-//     S = sum over groups  s_g[key] (Q C_g^T)  +  sum(q) z   (one product more)
-//     O_g += (P s_g) (C_g - 8),   Z += P (z + 8 s)           (one product more)
+// Requests of more columns than the line takes: a dense contraction, on the
+// 5th-generation tensor cores.  A CTA takes 128 columns of one KV head (a TMEM
+// lane each) against a range of the context, 64 keys a stage, two stages at a
+// time.  Its warps:
+//   0-3, 4-7   softmax of the even and of the odd stages, each with a reference,
+//              a sum and an O of its own (joined at the item's end): thread t of
+//              them has column t, so a maximum needs no other lane.  One thread
+//              of each issues the products: a stage's P V, then, when P has been
+//              read, the Q K^T of the stage after the next in its place.
+//   8-11       unpack K: codes and pairs come from global memory to registers
+//              a stage ahead, and go to shared memory as fp16 tiles (128-byte
+//              swizzle).
+//   12-15      unpack V.
+// With c the codes and s = s' + s" a scale cut after 7 bits, c s' and c s" are
+// exact in fp16, and so is S but for its fp32 sums:
+//     S = Q (c s')^T + Q (c s")^T + sum(q) z^T      (M 128, N 64, K 2 D + 16)
+//     O += P V                                      (V = fma(c, s, z): one fp16 rounding, as P has)
+// sum(q) of a group is two halves and 2^-7 of itself, z 2^7 of itself.  P (fp16)
+// takes the place of its S in TMEM.
+// What fp16 does not hold is kept out of the tiles: a key whose K or V would
+// leave its range is stored 2^-11 or 2^-5 of itself, with a bit for the softmax,
+// and a V pair that is no number as zeros, with a bit of its group that makes
+// NaNs of the columns that see the key, and of no other.
 // The tiles hold a word's eight dimensions in the order of the unpacking, 0 4
-// 1 5 2 6 3 7; Q is read in that order and the output written back from it.
+// 1 5 2 6 3 7; Q is stored in that order and the output written back from it.
 
 struct RowItems {
     int qo[kMaxB + 1];        // query rows before request b
     int it[kMaxB + 1];        // items before request b
-    long long sum[8];
-    int sum_q[8];
+    long long sum[16];
+    int sum_q[16];
     int bad, next;
 };
+// An item, in shared memory (what a role uses of it would cost registers).
+struct RowsItem {
+    int b, hk, n, ql, v0, vlast, page0, end_page, n_st, part;
+};
 
+constexpr int kRowsThreads = 512;
 template <int D, int GROUP>
 struct RowsSmem {
-    static constexpr int NG = D / GROUP;
-    static constexpr int kCodes = kRowsKeys * D / 2;               // bytes of a stage's K or V codes
-    static constexpr int kRaw = 2 * kCodes + 2 * kRowsKeys * NG * 4;
-    static constexpr int kStages = 4;
-    struct alignas(256) Tiles {
-        __half k[kRowsKeys * D], v[kRowsKeys * D];
-        float kf[NG * kRowsKeys], vf[NG * kRowsKeys];      // scales of a group's keys: 2^24 s / 128, s
-        __half kz[kRowsKeys * 8];                          // a key's z of the groups, twice
-        __half vz[8 * kVzRow];                             // z + 8 s of group i, row NG + i: its remainder
-    };
-    Tiles t[2];
-    alignas(128) unsigned char raw[kStages * kRaw];
-    int e[4];                                              // largest scale_exp of stage i mod 4
+    static constexpr int NG = D / GROUP, KH = D / 64;      // KH: 64-dimension halves of a row
+    static constexpr int kQHalf = kRowsTile * 128, kKHalf = kRowsKeys * 128;
+    unsigned char q[KH * kQHalf];
+    unsigned char k[2][2][KH * kKHalf];      // stages 2i, 2i + 1: c s', c s"
+    unsigned char v[2][KH * kKHalf];
+    unsigned char qz[kRowsTile * 32];        // [16][2][8] pieces of 16 bytes: row, half of the 16 terms
+    unsigned char kz[2][kRowsKeys * 32];
+    unsigned long long bar[16];
+    // stage i mod 4: a bit a key (a byte eight of them); v_odd: 1 scaled, 2 no number
+    unsigned char kbig[4][8], vbig[4][8], vnan[4][NG][8], v_odd[4][8];
+    float2 ml[2][kRowsTile];                 // a column's reference and sum
+    unsigned nan[2][kRowsTile];              // its groups of V that are no numbers
     RowItems s;
+    RowsItem r;
+    unsigned tmem;
+    int abort;
 };
+template <int D, int GROUP>
+constexpr size_t kRowsSmem = sizeof(RowsSmem<D, GROUP>) + 1024;      // (from a 1024-byte boundary on)
+enum { ROWS_QFULL, ROWS_FIN, ROWS_KFULL, ROWS_VFULL = ROWS_KFULL + 2, ROWS_SFULL = ROWS_VFULL + 2,
+       ROWS_PREADY = ROWS_SFULL + 2, ROWS_PVDONE = ROWS_PREADY + 2 };
+constexpr unsigned kRowsTmem = 512, kRowsColS = 0, kRowsColO = 128;      // S (or P) of stage i: 64 (i & 1); O: 128 (i & 1)
+
+// descriptor of 8 x 16-byte pieces without swizzle: the row's next 16 bytes
+// 128 bytes on, the next eight rows 256
+__device__ __forceinline__ uint64_t plain_desc(unsigned saddr)
+{
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128u >> 4) << 16 | (uint64_t)(256u >> 4) << 32 | (uint64_t)1 << 46;
+}
+// a descriptor that is made where it is used (the many of a stage would be
+// kept in registers, and those in local memory)
+__device__ __forceinline__ uint64_t pinned(uint64_t d)
+{
+    uint64_t r;
+    asm volatile("mov.b64 %0, %1;" : "=l"(r) : "l"(d));
+    return r;
+}
 
 // Pages of a split: about three items an SM.
 __device__ __forceinline__ int split_pages(long long work, int grid, int least)
@@ -1684,7 +1726,7 @@ __device__ __forceinline__ int split_pages(long long work, int grid, int least)
 }
 __device__ __forceinline__ int rows_tiles(int cols) { return (cols + kRowsTile - 1) / kRowsTile; }
 
-// The items of the batch (256 threads): items prefix, and the split.
+// The items of the batch (at least 256 threads): items prefix, and the split.
 __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int least, int rows_max)
 {
     constexpr int PER = kMaxB / 256;
@@ -1758,466 +1800,625 @@ __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int leas
     return split;
 }
 
-// A stage's pieces of one thread: D / 64 pieces of codes, and a piece of the
-// pairs for the first 32 NG threads.
+__device__ __forceinline__ void sts128(unsigned a, unsigned x, unsigned y, unsigned z, unsigned w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+__device__ __forceinline__ void tmem_st16(unsigned taddr, const unsigned (&r)[16])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
+// What is rare stays out of the loops: four roles' code passes through a
+// scheduler's instruction cache, and what it does not hold runs at a tenth of
+// the rate.
+__device__ __noinline__ bool rows_wait_long(unsigned bar, unsigned parity, volatile int *abort) { return tc::mbar_wait(bar, parity, abort); }
+__device__ __forceinline__ bool rows_wait(unsigned bar, unsigned parity, volatile int *abort)
+{
+    return tc::mbar_try(bar, parity) || rows_wait_long(bar, parity, abort);
+}
+// Scores in TMEM: the keys of `big` times 2048, those from `seen` on hidden.
+__device__ __noinline__ void rows_fix_scores(unsigned tS, unsigned long long big, int seen)
+{
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+        unsigned x[32];
+        tc::tmem_ld32(tS + c, x);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k++) {
+            if (big >> c >> k & 1) x[k] = __float_as_uint(__uint_as_float(x[k]) * 2048.f);
+            if (c + k >= seen) x[k] = __float_as_uint(kNegInf);
+        }
+        tc::tmem_st32(tS + c, x);
+    }
+    tc::tmem_wait_st();
+}
+// Weights in TMEM (fp16): the keys of `big` times 32.
+__device__ __noinline__ void rows_fix_weights(unsigned tP, unsigned long long big)
+{
+    unsigned x[32];
+    tc::tmem_wait_st();
+    tc::tmem_ld32(tP, x);
+    tc::tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; k++) {
+        const __half2 f = __floats2half2_rn(big >> (2 * k) & 1 ? 32.f : 1.f, big >> (2 * k + 1) & 1 ? 32.f : 1.f);
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[k]), f);
+        x[k] = *reinterpret_cast<const unsigned *>(&y);
+    }
+    tc::tmem_st32(tP, x);
+}
+// An O of W columns times f.
+template <int W>
+__device__ __noinline__ void rows_scale(unsigned tO, float f)
+{
+#pragma unroll 1
+    for (int c = 0; c < W; c += 32) {
+        unsigned o[32];
+        tc::tmem_ld32(tO + c, o);
+        tc::tmem_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; k++) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+        tc::tmem_st32(tO + c, o);
+    }
+}
+
+// A thread's part of a stage on its way, of K or of V: 32 dimensions of N keys.
+// Eight lanes that store together are four keys and two neighbouring pieces: no
+// bank twice.
 template <int D, int GROUP>
 struct Pieces {
     using S = RowsSmem<D, GROUP>;
-    static constexpr int kN = D * 4 / 256;             // pieces of codes
-    static constexpr int kPerRow = D / 32;
-    // piece i: K or V, key of the stage, 32 dimensions
-    static __device__ __forceinline__ void where(int i, int &kv, int &key, int &ch)
+    static constexpr int NG = S::NG, N = D / 64;
+    static constexpr int kBytes = D == 128 ? 1 : 2;      // a warp's keys are eight, or 16
+    uint4 c[N];
+    unsigned sz[N];
+
+    static __device__ __forceinline__ int piece(int u) { return D == 128 ? (u & 1) | (u >> 2 & 2) : u & 1; }
+    static __device__ __forceinline__ int key(int u, int i)
     {
-        const int c = threadIdx.x + 256 * i;
-        kv = c / (kRowsKeys * kPerRow);
-        key = c / kPerRow % kRowsKeys;
-        ch = c % kPerRow;
+        return D == 128 ? (u >> 5) * 8 + (u >> 1 & 3) + (u >> 2 & 4) + 32 * i : u >> 1;
     }
-    static __device__ __forceinline__ void where_sz(int &kv, int &first)      // first pair, of 64 * NG
+    static __device__ __forceinline__ unsigned key_lanes(int first) { return (D == 128 ? 0x303u : 3u) << first; }
+    // the warp's keys of a ballot: byte `lane` of them
+    static __device__ __noinline__ unsigned char keys_of(unsigned b, int lane)
     {
-        kv = threadIdx.x / (16 * S::NG);
-        first = threadIdx.x % (16 * S::NG) * 4;
+        unsigned r = 0;
+#pragma unroll
+        for (int k = 0; k < 8 * kBytes; k++) r |= (b & key_lanes(D == 128 ? (k & 3) << 1 | (k & 4) << 2 : 2 * k)) ? 1u << k : 0u;
+        return (unsigned char)(r >> (8 * lane & 31));
     }
-    // block ids of its pieces in the stage from page `page` on (-1: none or bad)
-    int blk[kN], blk_sz;
-    __device__ __forceinline__ void ids(const Params &p, const int *table, int page, int end)
+    static __device__ __forceinline__ bool of_key(unsigned b, int lane) { return b & key_lanes(lane & (D == 128 ? ~9 : ~1)); }
+
+    static __device__ __forceinline__ void ids(const int *table, int u, int page0, int end, int (&blk)[N])
     {
 #pragma unroll
-        for (int i = 0; i < kN; i++) {
-            int kv, key, ch;
-            where(i, kv, key, ch);
-            blk[i] = id(p, table, page + key / kBlock, end);
+        for (int i = 0; i < N; i++) {
+            const int page = page0 + key(u, i) / kBlock;
+            blk[i] = -1;
+            if (page < end) blk[i] = __ldg(table + page);
         }
-        int kv, first;
-        where_sz(kv, first);
-        blk_sz = kv < 2 ? id(p, table, page + first / (kBlock * S::NG), end) : -1;
     }
-    static __device__ __forceinline__ int id(const Params &p, const int *table, int page, int end)
+    // codes, pairs: those of the thread's first key and piece in block 0
+    __device__ __forceinline__ void load(const Params &p, const unsigned char *codes, const unsigned char *pairs, int u, int page0, int end,
+                                         int n, const int (&blk)[N])
     {
-        int blk = -1;
-        if (page < end) {
-            blk = table[page];
-            if ((unsigned)blk >= (unsigned)p.num_blocks) {
-                atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
-                blk = -1;
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            c[i] = make_uint4(0u, 0u, 0u, 0u);
+            sz[i] = 0u;
+            if ((unsigned)blk[i] >= (unsigned)p.num_blocks) {
+                if (page0 + key(u, i) / kBlock < end) atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
+            } else {
+                c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)blk[i] * (unsigned)(p.Hkv * kBlock * (D / 2))));
+                // pairs of tokens behind the last one are zero
+                if (page0 * kBlock + key(u, i) < n)
+                    sz[i] = __ldg(reinterpret_cast<const unsigned *>(pairs + (size_t)blk[i] * (unsigned)(p.Hkv * kBlock * NG * 4)));
             }
         }
-        return blk;
     }
-    __device__ __forceinline__ void fetch(const Params &p, const Pool &pool, unsigned raw, int hk, int page, int n) const
+    static __device__ __forceinline__ const unsigned char *at_codes(const unsigned char *codes, int u, int hk)
+    {
+        return codes + ((size_t)hk * kBlock + key(u, 0) % kBlock) * (D / 2) + 16 * piece(u);
+    }
+    static __device__ __forceinline__ const unsigned char *at_pairs(const __half2 *pairs, int u, int hk)
+    {
+        return reinterpret_cast<const unsigned char *>(pairs + ((size_t)hk * kBlock + key(u, 0) % kBlock) * NG + piece(u) * 32 / GROUP);
+    }
+    // Codes of word w, dimensions k and k + 4, as halves 1024 + c (k even) and 64 + c.
+    static __device__ __forceinline__ void raised(unsigned w, __half2 (&c)[4])
     {
 #pragma unroll
-        for (int i = 0; i < kN; i++) {
-            int kv, key, ch;
-            where(i, kv, key, ch);
-            const size_t row = ((size_t)max(blk[i], 0) * p.Hkv + hk) * kBlock + key % kBlock;
-            copy16(raw + (threadIdx.x + 256 * i) * 16, (kv ? pool.v : pool.k) + row * (D / 2) + 16 * ch, blk[i] >= 0 ? 16 : 0, true);
+        for (int k = 0; k < 4; k += 2) {
+            const unsigned x = w >> (4 * k), lo = (x & kLoCodes) | 0x64006400u, hi = (x & kHiCodes) | 0x54005400u;
+            c[k] = *reinterpret_cast<const __half2 *>(&lo);
+            c[k + 1] = *reinterpret_cast<const __half2 *>(&hi);
         }
-        int kv, first;
-        where_sz(kv, first);
-        const int in = first % (kBlock * S::NG);
-        const __half2 *src = (kv ? pool.vsz : pool.ksz) + ((size_t)max(blk_sz, 0) * p.Hkv + hk) * kBlock * S::NG + in;
-        // pairs of tokens behind the last one read as zero
-        const int rows = n - (page + first / (kBlock * S::NG)) * kBlock;
-        const int bytes = blk_sz < 0 ? 0 : min(16, max(0, (rows * S::NG - in) * 4));
-        copy16(raw + 2 * S::kCodes + threadIdx.x * 16, src, bytes, kv < 2);
     }
-    // its pieces into the tiles
-    static __device__ __forceinline__ void unpack(typename S::Tiles &t, int *e, unsigned raw)
+    // Its first store into a tile at `tile`.
+    static __device__ __forceinline__ unsigned first(unsigned tile, int u)
     {
-        const __half2 bias = __floats2half2_rn(-1032.f, -1032.f);
+        const int ch = piece(u);
+        unsigned x;      // (not kept through the loop in 24 addresses)
+        asm volatile("add.u32 %0, %1, %2;" : "=r"(x) : "r"(tile), "r"((ch >> 1) * S::kKHalf + tc::sw_off(key(u, 0), 4 * (ch & 1))));
+        return x;
+    }
+    static __device__ __forceinline__ void put(unsigned at, int i, int j, const __half2 (&x)[4])
+    {
+        const unsigned *w = reinterpret_cast<const unsigned *>(x);
+        sts128((at ^ (j << 4)) + i * 4096, w[0], w[1], w[2], w[3]);      // (32 keys on)
+    }
+    static __device__ __forceinline__ float2 pair(unsigned w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
+    static __device__ __forceinline__ __half2 both(unsigned w, unsigned sel)
+    {
+        const unsigned x = __byte_perm(w, 0u, sel);
+        return *reinterpret_cast<const __half2 *>(&x);
+    }
+    static __device__ __forceinline__ bool number(unsigned w) { return (w & 0x7c00u) != 0x7c00u && (w & 0x7c000000u) != 0x7c000000u; }
+    static __device__ __forceinline__ void times(unsigned &w, float f)
+    {
+        const float2 x = pair(w);
+        const __half2 h = __floats2half2_rn(x.x * f, x.y * f);
+        w = *reinterpret_cast<const unsigned *>(&h);
+    }
+    // c s = (1024 + c) s - 1024 s, exact for a scale of at most seven bits
+    // whose 1024 s is a half, and the same with 64.
+    __device__ __forceinline__ void unpack_k(S &sm, int e, int slot, int u)
+    {
+        const int lane = u & 31, ch = piece(u);
+        const unsigned to = first(smem_u32(sm.k[e][0]), u);
 #pragma unroll
-        for (int i = 0; i < kN; i++) {
-            int kv, key, ch;
-            where(i, kv, key, ch);
-            const uint4 x = lds128(raw + (threadIdx.x + 256 * i) * 16);
-            const unsigned w[4] = {x.x, x.y, x.z, x.w};
-            __half *tile = kv ? t.v : t.k;
+        for (int i = 0; i < N; i++) {
+            const int kk = key(u, i);
+            const float2 f = pair(sz[i]);
+            const unsigned any = __ballot_sync(0xffffffffu, fabsf(f.x) >= 60.f || fabsf(f.y) >= 511.f);
+            if (lane < kBytes) sm.kbig[slot][kk / 8 + lane] = any ? keys_of(any, lane) : (unsigned char)0;
+            if (any && of_key(any, lane)) times(sz[i], 0x1p-11f);
+            const unsigned s1 = __byte_perm(sz[i], 0u, 0x1010), s1h = s1 & 0xfff0fff0u;
+            const __half2 sh = *reinterpret_cast<const __half2 *>(&s1h), sl = __hsub2(*reinterpret_cast<const __half2 *>(&s1), sh);
+            const __half2 k0 = __floats2half2_rn(-1024.f, -1024.f), k1 = __floats2half2_rn(-64.f, -64.f);
+            const __half2 sh0 = __hmul2(sh, k0), sh1 = __hmul2(sh, k1), sl0 = __hmul2(sl, k0), sl1 = __hmul2(sl, k1);
+            const unsigned w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                unsigned o[4];
+                __half2 x[4], h[4], l[4];
+                raised(w[j], x);
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
-                    const unsigned c = (w[j] >> (4 * k)) & kLoCodes;
-                    if (kv) {
-                        const unsigned m = c | 0x64006400u;
-                        const __half2 r = __hadd2(*reinterpret_cast<const __half2 *>(&m), bias);
-                        o[k] = *reinterpret_cast<const unsigned *>(&r);
-                    } else {
-                        o[k] = c;
-                    }
+                    h[k] = __hfma2(x[k], sh, k & 1 ? sh1 : sh0);
+                    l[k] = __hfma2(x[k], sl, k & 1 ? sl1 : sl0);
                 }
-                *reinterpret_cast<uint4 *>(tile + swz<D>(key, 4 * ch + j)) = make_uint4(o[0], o[1], o[2], o[3]);
+                put(to, i, j, h);
+                put(to + S::KH * S::kKHalf, i, j, l);
+            }
+            if (ch * 32 % GROUP == 0) {
+                const int gi = ch * 32 / GROUP;
+                const __half z = __hmul(__ushort_as_half((unsigned short)(sz[i] >> 16)), __float2half_rn(128.f));
+                __half *terms = reinterpret_cast<__half *>(sm.kz[e] + kk / 8 * 256 + kk % 8 * 16);
+                terms[gi] = z;
+                terms[NG + gi] = z;      // (at most eight terms: the first 16 bytes)
             }
         }
-        int kv, first, em = 0;
-        where_sz(kv, first);
-        if (kv < 2) {
-            const uint4 x = lds128(raw + 2 * S::kCodes + threadIdx.x * 16);
-            const unsigned w[4] = {x.x, x.y, x.z, x.w};
+    }
+    __device__ __forceinline__ void unpack_v(S &sm, int e, int slot, int u)
+    {
+        const int lane = u & 31, ch = piece(u);
+        const unsigned to = first(smem_u32(sm.v[e]), u);
+#pragma unroll
+        for (int i = 0; i < N; i++) {
+            const int at = key(u, i) / 8 + lane;
+            const float2 f = pair(sz[i]);
+            const bool odd = !(fmaf(15.f, fabsf(f.x), fabsf(f.y)) < 65504.f);
+            if (__any_sync(0xffffffffu, odd)) {
+                const bool num = number(sz[i]);
+                const unsigned any = __ballot_sync(0xffffffffu, num && odd), none = __ballot_sync(0xffffffffu, !num);
+                if (lane < kBytes) {
+                    sm.v_odd[slot][at] = (any ? 1 : 0) | (none ? 2 : 0);
+                    sm.vbig[slot][at] = keys_of(any, lane);
+                }
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++) {
+                    const unsigned g = __ballot_sync(0xffffffffu, !num && ch * 32 / GROUP == gi);
+                    if (lane < kBytes) sm.vnan[slot][gi][at] = keys_of(g, lane);
+                }
+                if (!num) sz[i] = 0u;
+                if (of_key(any, lane)) times(sz[i], 0x1p-5f);
+            } else if (lane < kBytes) {
+                sm.v_odd[slot][at] = sm.vbig[slot][at] = 0;
+#pragma unroll
+                for (int gi = 0; gi < NG; gi++) sm.vnan[slot][gi][at] = 0;
+            }
+            const __half2 s = both(sz[i], 0x1010), z = both(sz[i], 0x3232);
+            const __half2 k0 = __floats2half2_rn(-1024.f, -1024.f), k1 = __floats2half2_rn(-64.f, -64.f);
+            const unsigned w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const __half2 h = *reinterpret_cast<const __half2 *>(&w[j]);
-                const float2 f = __half22float2(h);
-                const int key = (first + j) / S::NG, gi = (first + j) % S::NG;
-                if (kv) {
-                    const float z = fmaf(8.f, f.x, f.y);
-                    const __half z16 = __float2half_rn(z);
-                    t.vf[gi * kRowsKeys + key] = f.x;
-                    t.vz[gi * kVzRow + key] = z16;
-                    t.vz[(S::NG + gi) * kVzRow + key] = __float2half_rn(z - __half2float(z16));
-                    em = max(em, scale_exp(h));
-                } else {
-                    t.kf[gi * kRowsKeys + key] = f.x * (0x1p24f * kQsScale);
-                    t.kz[key * 8 + gi] = t.kz[key * 8 + S::NG + gi] = __high2half(h);
-                }
+                __half2 x[4];
+                raised(w[j], x);
+#pragma unroll
+                for (int k = 0; k < 4; k++) x[k] = __hfma2(__hadd2(x[k], k & 1 ? k1 : k0), s, z);
+                put(to, i, j, x);
             }
         }
-        em = (int)__reduce_max_sync(0xffffffffu, (unsigned)em);
-        if (em > 0 && (threadIdx.x & 31) == 0) atomicMax(e, em);
     }
 };
 
-// A warp's 16 columns (rows g and g + 8 of its tiles).
-template <int D>
-struct RowsState {
-    float o[D / 8][4];
-    float z[4];               // columns 2t, 2t + 1: sum p hi(z + 8 s) of groups, then of the remainders
-    float m[2], l[2];
-    int e;
-};
-
-__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned a)
+__device__ __forceinline__ RowsItem rows_item(const Params &p, const RowItems &s, int item, int split)
 {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
-__device__ __forceinline__ void ldsm4_t(unsigned (&r)[4], unsigned a)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(a));
-}
-
-// One stage for one warp.  FULL: every column sees every key of it.
-template <int D, int GROUP, bool FULL>
-__device__ __forceinline__ void rows_stage(const typename RowsSmem<D, GROUP>::Tiles &T, int stage_e, int lane,
-                                           const unsigned (&qf)[D / 16][4], const unsigned (&qz)[2], const int (&end)[2],
-                                           int key0, RowsState<D> &s, float scale, float slack)
-{
-    constexpr int NG = D / GROUP, KN = kRowsKeys / 8, NT = D / 8;
-    const int g = lane >> 2, t = lane & 3;
-    // addresses of swz(row, chunk): the chunk is an exclusive or away from the row's first one
-    const int kr = (lane & 7) + ((lane >> 4) << 3), vr = (lane & 7) + (((lane >> 3) & 1) << 3);
-    const unsigned ka = smem_u32(T.k) + kr * (2 * D) + ((((lane >> 3) & 1) ^ (lane & 7)) << 4);
-    const unsigned va = smem_u32(T.v) + vr * (2 * D) + (((lane >> 4) ^ (lane & 7)) << 4);
-    float sc[KN][4];
-    const unsigned az[4] = {qz[0], qz[1], 0u, 0u};
-#pragma unroll
-    for (int nn = 0; nn < KN; nn++)
-        mma16816_first(sc[nn], az, *reinterpret_cast<const unsigned *>(&T.kz[(8 * nn + g) * 8 + 2 * t]), 0u);
-#pragma unroll
-    for (int gi = 0; gi < NG; gi++)
-#pragma unroll
-        for (int np = 0; np < KN / 2; np++) {
-            float acc[2][4];
-#pragma unroll
-            for (int kk = 0; kk < GROUP / 16; kk++) {
-                const int kt = gi * (GROUP / 16) + kk;
-                unsigned b[4];
-                ldsm4(b, (ka ^ (kt << 5)) + np * 16 * (2 * D));
-                if (kk == 0) {
-                    mma16816_first(acc[0], qf[kt], b[0], b[1]);
-                    mma16816_first(acc[1], qf[kt], b[2], b[3]);
-                } else {
-                    mma16816(acc[0], qf[kt], b[0], b[1]);
-                    mma16816(acc[1], qf[kt], b[2], b[3]);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const float2 f = *reinterpret_cast<const float2 *>(&T.kf[gi * kRowsKeys + 16 * np + 8 * h + 2 * t]);
-                float(&x)[4] = sc[2 * np + h];
-                x[0] = fmaf(acc[h][0], f.x, x[0]);
-                x[1] = fmaf(acc[h][1], f.y, x[1]);
-                x[2] = fmaf(acc[h][2], f.x, x[2]);
-                x[3] = fmaf(acc[h][3], f.y, x[3]);
-            }
-        }
-    if (!FULL) {
-#pragma unroll
-        for (int nn = 0; nn < KN; nn++)
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                if (key0 + 8 * nn + 2 * t + (e & 1) >= end[e >> 1]) sc[nn][e] = kNegInf;
-    }
-    bool moved = false;
-    float mn[2], mu[2];
-#pragma unroll
-    for (int r = 0; r < 2; r++) {
-        float mx = kNegInf;
-#pragma unroll
-        for (int nn = 0; nn < KN; nn++) mx = fmaxf(mx, fmaxf(sc[nn][2 * r], sc[nn][2 * r + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const bool move = mx > s.m[r] + slack;
-        mn[r] = move ? mx : s.m[r];
-        mu[r] = mn[r] == kNegInf ? 0.f : -mn[r] * scale;
-        moved = moved || move;
-    }
-    const int em = max(s.e, stage_e);
-    if (__any_sync(0xffffffffu, moved || em != s.e)) {
-        const float ae = __int_as_float((s.e - em + 127) << 23);
-        s.e = em;
-#pragma unroll
-        for (int r = 0; r < 2; r++) {
-            const float al = ex2(fmaf(s.m[r], scale, mu[r])), ao = al * ae;
-            s.m[r] = mn[r];
-            s.l[r] *= al;
-            s.z[2 * r] *= al;
-            s.z[2 * r + 1] *= al;
-#pragma unroll
-            for (int d = 0; d < NT; d++) {
-                s.o[d][2 * r] *= ao;
-                s.o[d][2 * r + 1] *= ao;
-            }
-        }
-    }
-    const float down = scale_down(em);
-#pragma unroll
-    for (int nn = 0; nn < KN; nn++)
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            sc[nn][e] = ex2(fmaf(sc[nn][e], scale, mu[e >> 1]));
-            s.l[e >> 1] += sc[nn][e];
-        }
-    // the group terms; an unseen key's may be a NaN, which must not meet its zero weight
-#pragma unroll
-    for (int ks = 0; ks < KN / 2; ks++) {
-        const unsigned pa[4] = {pack_half2(sc[2 * ks][0], sc[2 * ks][1]), pack_half2(sc[2 * ks][2], sc[2 * ks][3]),
-                                pack_half2(sc[2 * ks + 1][0], sc[2 * ks + 1][1]), pack_half2(sc[2 * ks + 1][2], sc[2 * ks + 1][3])};
-        unsigned bz[2];
-#pragma unroll
-        for (int h = 0; h < 2; h++) {
-            bz[h] = *reinterpret_cast<const unsigned *>(&T.vz[g * kVzRow + 16 * ks + 8 * h + 2 * t]);
-            if (!FULL) {
-                if ((bz[h] & 0x7c00u) == 0x7c00u) bz[h] &= 0xffff0000u;
-                if ((bz[h] & 0x7c000000u) == 0x7c000000u) bz[h] &= 0x0000ffffu;
-            }
-        }
-        mma16816(s.z, pa, bz[0], bz[1]);
-    }
-    if (FULL) {
-#pragma unroll
-        for (int nn = 0; nn < KN; nn++)
-#pragma unroll
-            for (int e = 0; e < 4; e++) sc[nn][e] *= down;
-    }
-#pragma unroll
-    for (int gi = 0; gi < NG; gi++)
-#pragma unroll
-        for (int ks = 0; ks < KN / 2; ks++) {
-            unsigned pa[4];
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                const int nn = 2 * ks + h, key = 8 * nn + 2 * t;
-                float2 f = *reinterpret_cast<const float2 *>(&T.vf[gi * kRowsKeys + key]);
-                float w[4];
-                if (FULL) {
-                    w[0] = sc[nn][0] * f.x;
-                    w[1] = sc[nn][1] * f.y;
-                    w[2] = sc[nn][2] * f.x;
-                    w[3] = sc[nn][3] * f.y;
-                } else {
-                    // a group whose z left the operand above has a NaN weight where the key is seen
-                    const unsigned b = *reinterpret_cast<const unsigned *>(&T.vz[gi * kVzRow + key]);
-                    if ((b & 0x7c00u) == 0x7c00u) f.x = __int_as_float(0x7fffffff);
-                    if ((b & 0x7c000000u) == 0x7c000000u) f.y = __int_as_float(0x7fffffff);
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        w[e] = key0 + key + (e & 1) < end[e >> 1] ? sc[nn][e] * ((e & 1 ? f.y : f.x) * down) : 0.f;
-                }
-                pa[2 * h] = pack_half2(w[0], w[1]);
-                pa[2 * h + 1] = pack_half2(w[2], w[3]);
-            }
-#pragma unroll
-            for (int dd = 0; dd < GROUP / 16; dd++) {
-                const int dp = gi * (GROUP / 16) + dd;
-                unsigned b[4];
-                ldsm4_t(b, (va ^ (dp << 5)) + ks * 16 * (2 * D));
-                mma16816(s.o[2 * dp], pa, b[0], b[1]);
-                mma16816(s.o[2 * dp + 1], pa, b[2], b[3]);
-            }
-        }
+    RowsItem r;
+    r.b = find_owner(s.it, p.B, item);
+    r.n = p.ctx_lens[r.b];
+    r.ql = s.qo[r.b + 1] - s.qo[r.b];
+    const int cols = r.ql * p.G, pages = (r.n + kBlock - 1) / kBlock, tiles = rows_tiles(cols);
+    int j = item - s.it[r.b];
+    r.hk = j % p.Hkv;      // (KV heads next to each other: they share the split's length)
+    j /= p.Hkv;
+    const int tile = j % tiles;
+    r.part = j / tiles;
+    r.v0 = tile * kRowsTile;
+    r.vlast = min(cols, r.v0 + kRowsTile) - 1;
+    r.page0 = r.part * split;
+    r.end_page = min(min(r.page0 + split, pages), (keys_seen(r.n, r.ql, r.vlast / p.G) + kBlock - 1) / kBlock);
+    r.n_st = r.end_page > r.page0 ? (r.end_page - r.page0 + 3) / 4 : 0;
+    return r;
 }
 
 template <int D, int GROUP>
-__global__ void __launch_bounds__(256, 1) rows_kernel(const __grid_constant__ Args a)
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ Args a)
 {
     using S = RowsSmem<D, GROUP>;
-    constexpr int NG = S::NG, KT = D / 16, NT = D / 8;
-    extern __shared__ __align__(256) unsigned char smem_rows[];
-    S &sm = *reinterpret_cast<S *>(smem_rows);
+    using X = Pieces<D, GROUP>;
+    constexpr int NG = S::NG, KH = S::KH;
+    constexpr uint32_t id_s = tc::idesc_f16(kRowsTile, kRowsKeys), id_o = tc::idesc_f16(kRowsTile, D, true);
+    extern __shared__ unsigned char smem_rows[];
+    S &sm = *reinterpret_cast<S *>(smem_rows + (-smem_u32(smem_rows) & 1023u));
     const Params &p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    for (int k = 0; k < 2; k++) {      // rows and columns that no group has
-        for (int i = tid; i < kRowsKeys * 8; i += 256) sm.t[k].kz[i] = __ushort_as_half(0);
-        for (int i = tid; i < 8 * kVzRow; i += 256) sm.t[k].vz[i] = __ushort_as_half(0);
-    }
+    auto bar = [&](int i) { return smem_u32(sm.bar) + 8u * (unsigned)i; };
+    volatile int *abort_p = &sm.abort;
     const int split = build_rows(p, sm.s, a.rows_least, a.rows_max);
     if (blockIdx.x == 0 && tid == 0) p.sched[2] = split;
     const bool run = !sm.s.bad && sm.s.qo[p.B] <= p.max_q_total;
     const int n_items = run ? sm.s.it[p.B] : 0;
-    const unsigned raw = smem_u32(sm.raw);
-    const float scale = p.scale_log2 * (1.f / kQsScale), slack = a.slack * kQsScale;
+    if ((int)blockIdx.x >= n_items) {
+        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        return;
+    }
+    if (warp == 8) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(&sm.tmem)), "n"(kRowsTmem)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n" ::: "memory");
+    }
+    if (tid == 0) {
+        sm.abort = 0;
+        tc::mbar_init(bar(ROWS_QFULL), 4);
+        tc::mbar_init(bar(ROWS_FIN), 2);
+        for (int i = 0; i < 2; i++) {
+            tc::mbar_init(bar(ROWS_KFULL + i), 4);
+            tc::mbar_init(bar(ROWS_VFULL + i), 4);
+            tc::mbar_init(bar(ROWS_SFULL + i), 1);
+            tc::mbar_init(bar(ROWS_PREADY + i), 4);
+            tc::mbar_init(bar(ROWS_PVDONE + i), 1);
+        }
+        sm.r = rows_item(p, sm.s, blockIdx.x, split);
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    }
+    for (int i = tid; i < kRowsKeys * 16; i += kRowsThreads) reinterpret_cast<unsigned *>(sm.kz)[i] = 0u;      // terms that no group has
+    tc::fence_async_smem();
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const unsigned tmem = sm.tmem;
+    const RowsItem &r = sm.r;
+    int J = 0;                 // stages before the item
+    unsigned q_items = 0;      // items with stages before it
 
     for (int item = blockIdx.x; item < n_items;) {
-        const int b = find_owner(sm.s.it, p.B, item);
-        const int n = p.ctx_lens[b], ql = sm.s.qo[b + 1] - sm.s.qo[b], cols = ql * p.G, pages = (n + kBlock - 1) / kBlock;
-        const int tiles = rows_tiles(cols);
-        int j = item - sm.s.it[b];
-        const int hk = j % p.Hkv;      // (KV heads next to each other: they share the split's length)
-        j /= p.Hkv;
-        const int tile = j % tiles, part = j / tiles;
-        const int v0 = tile * kRowsTile, vlast = min(cols, v0 + kRowsTile) - 1;
-        const int page0 = part * split;
-        const int end_page = min(min(page0 + split, pages), (keys_seen(n, ql, vlast / p.G) + kBlock - 1) / kBlock);
-        const int n_st = end_page > page0 ? (end_page - page0 + 3) / 4 : 0;
-        const int *table = p.block_tables + (size_t)b * p.max_blocks;
-        Pieces<D, GROUP> pc;
-        pc.ids(p, table, page0, end_page);
-        int fetched = 0;
-        auto fetch = [&]() {
-            if (fetched < n_st) {
-                pc.fetch(p, a.pool, raw + fetched % S::kStages * S::kRaw, hk, page0 + 4 * fetched, n);
-                fetched++;
-                if (fetched < n_st) pc.ids(p, table, page0 + 4 * fetched, end_page);
-            }
-            cp_async_commit();
-        };
-        for (int k = 0; k < S::kStages - 1; k++) fetch();
-
-        // the warp's 16 columns: rows g and g + 8 of its tiles
-        const int vw = v0 + 16 * warp;
-        const bool active = vw <= vlast;
-        unsigned qf[KT][4], qz[2];
-        int end[2];
-        const int key_end = end_page * kBlock;      // the split's keys end here
-        const int least = min(key_end, keys_seen(n, ql, min(vw, vlast) / p.G));
-        const int most = min(key_end, keys_seen(n, ql, min(vw + 15, vlast) / p.G));
-        {
-            const __half *q[2];
-            float sum[2][NG];
+        bool ok = true;
+        if (warp < 8) {
+            // ------------------------------------------------------------ softmax, Q and the output
+            const int e = warp >> 2, row = tid & 127;
+            const bool have = r.v0 + row <= r.vlast;
+            const unsigned lane_off = (unsigned)((warp & 3) * 32) << 16;
+            int end = 0;           // keys that the row sees, of the range
+            if (r.n_st > 0) {
+                const int v = have ? r.v0 + row : 0, i = v / p.G;
+                end = r.end_page * kBlock;      // (rows that are none hide nothing: what they come to is not written)
+                if (have) end = min(end, keys_seen(r.n, r.ql, i));
+                if (e == 0) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (((size_t)r.b * p.Lq + i) * p.H + r.hk * p.G + v - i * p.G) * D);
+                    float sum[NG];
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const int v = vw + g + 8 * r;
-                const int i = v / p.G, c = v - i * p.G;
-                q[r] = v <= vlast ? p.q + (((size_t)b * p.Lq + i) * p.H + hk * p.G + c) * D : nullptr;
-                end[r] = min(key_end, keys_seen(n, ql, min(v, vlast) / p.G));
+                    for (int gi = 0; gi < NG; gi++) sum[gi] = 0.f;
+                    unsigned to;
+                    asm volatile("add.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(sm.q)), "r"(tc::sw_off(row, 0)));
+#pragma unroll 1
+                    for (int c0 = 0; c0 < D / 8; c0 += 4) {      // 32 dimensions, of one group
+                        float f = 0.f;
 #pragma unroll
-                for (int gi = 0; gi < NG; gi++) sum[r][gi] = 0.f;
-            }
+                        for (int c = 0; c < 4; c++) {
+                            const uint4 x = have ? __ldg(src + c0 + c) : make_uint4(0u, 0u, 0u, 0u);
+                            const unsigned w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int kt = 0; kt < KT; kt++)
+                            for (int k = 0; k < 4; k++) {
+                                const float2 y = X::pair(w[k]);
+                                f += y.x + y.y;
+                            }
+                            sts128((to ^ (((c0 & 4) + c) << 4)) + (c0 >> 3) * S::kQHalf, __byte_perm(x.x, x.z, 0x5410),
+                                   __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+                        }
 #pragma unroll
-                for (int x = 0; x < 4; x++) {      // rows g, g + 8; words 2 kt, 2 kt + 1: dimensions t, t + 4
-                    const __half *src = q[x & 1];
-                    const int d = 16 * kt + 8 * (x >> 1) + t;
-                    __half2 h = __floats2half2_rn(0.f, 0.f);
-                    if (src) h = __halves2half2(src[d], src[d + 4]);
-                    qf[kt][x] = *reinterpret_cast<const unsigned *>(&h);
-                    const float2 f = __half22float2(h);
-                    sum[x & 1][16 * kt / GROUP] += f.x + f.y;
+                        for (int gi = 0; gi < NG; gi++)
+                            if (gi == 8 * c0 / GROUP) sum[gi] += f;
+                    }
+                    // the groups' sums, then their remainders
+                    __half t[8];
+#pragma unroll
+                    for (int gi = 0; gi < 8; gi++) t[gi] = __ushort_as_half(0);
+#pragma unroll
+                    for (int gi = 0; gi < NG; gi++) {
+                        const float f = sum[gi] * kQsScale;
+                        t[gi] = __float2half_rn(f);
+                        t[NG + gi] = __float2half_rn(f - __half2float(t[gi]));
+                    }
+                    unsigned w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const __half2 x = __halves2half2(t[2 * k], t[2 * k + 1]);
+                        w[k] = *reinterpret_cast<const unsigned *>(&x);
+                    }
+                    const unsigned terms = smem_u32(sm.qz) + row / 8 * 256 + row % 8 * 16;
+                    sts128(terms, w[0], w[1], w[2], w[3]);
+                    sts128(terms + 128, 0u, 0u, 0u, 0u);
+                    tc::fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(bar(ROWS_QFULL));
                 }
-            // the row's sums of the groups, then their remainders: columns 2t, 2t + 1 of the operand
+            }
+            auto issue_s = [&](int j) {      // S = Q K^T, by one thread
+                ok = rows_wait(bar(ROWS_KFULL + e), (j >> 1) & 1, abort_p);
+                if (!ok) return;
+                tc::tc_fence_after();
+                const unsigned d0 = tmem + kRowsColS + 64 * e;
+                tc::umma_ss(d0, pinned(plain_desc(smem_u32(sm.qz))), pinned(plain_desc(smem_u32(sm.kz[e]))), id_s, 0);
+                const uint64_t qd = pinned(tc::sw128_desc(smem_u32(sm.q))), kd = pinned(tc::sw128_desc(smem_u32(sm.k[e][0])));
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                __half w[2] = {__ushort_as_half(0), __ushort_as_half(0)};
+                for (int kk = 0; kk < 2 * D / 16; kk++) {
+                    const int d = kk % (D / 16);
+                    tc::umma_ss(d0, qd + (((d >> 2) * S::kQHalf + (d & 3) * 32) >> 4),
+                                kd + (((kk / (D / 16)) * KH * S::kKHalf + (d >> 2) * S::kKHalf + (d & 3) * 32) >> 4), id_s, 1);
+                }
+                tc::umma_commit(bar(ROWS_SFULL + e));
+            };
+            const int st0 = (J + e) & 1;      // its first stage of the item
+            if ((warp & 3) == 0 && lane == 0 && st0 < r.n_st) {
+                ok = rows_wait(bar(ROWS_QFULL), q_items & 1, abort_p);
+                if (ok) issue_s(J + st0);
+            }
+            __syncwarp();
+            float m = kNegInf, l = 0.f;
+            unsigned nan = 0;
+            const unsigned tS = tmem + kRowsColS + 64 * e + lane_off, tO = tmem + kRowsColO + 128 * e + lane_off;
+            for (int st = st0; st < r.n_st; st += 2) {
+                const int j = J + st, key0 = (r.page0 + 4 * st) * kBlock;
+                ok = ok && rows_wait(bar(ROWS_VFULL + e), (j >> 1) & 1, abort_p) && rows_wait(bar(ROWS_SFULL + e), (j >> 1) & 1, abort_p);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                tc::tc_fence_after();
+                const unsigned *flags = reinterpret_cast<const unsigned *>(sm.kbig[j & 3]);
+                const unsigned k0 = flags[0], k1 = flags[1];
+                flags = reinterpret_cast<const unsigned *>(sm.v_odd[j & 3]);
+                const unsigned v_odd = flags[0] | flags[1];
+                const int seen = end - key0;
+                if (__any_sync(0xffffffffu, seen < kRowsKeys || (k0 | k1))) rows_fix_scores(tS, (unsigned long long)k1 << 32 | k0, seen);
+                if (v_odd & 0x02020202u) {
+                    const unsigned long long mask = seen >= 64 ? ~0ull : seen <= 0 ? 0ull : (1ull << seen) - 1ull;
+#pragma unroll 1
+                    for (int gi = 0; gi < NG; gi++)
+                        if (*reinterpret_cast<const unsigned long long *>(sm.vnan[j & 3][gi]) & mask) nan |= 1u << gi;
+                }
+                unsigned y[2][32];
+                tc::tmem_ld32(tS, y[0]);
+                tc::tmem_ld32(tS + 32, y[1]);
+                tc::tmem_wait_ld();
+                float x[64];
 #pragma unroll
-                for (int gi = 0; gi < NG; gi++) {
-                    float f = sum[r][gi];
-                    f += __shfl_xor_sync(0xffffffffu, f, 1);
-                    f += __shfl_xor_sync(0xffffffffu, f, 2);
-                    f *= kQsScale;
-                    const __half hi = __float2half_rn(f), lo = __float2half_rn(f - __half2float(hi));
+                for (int k = 0; k < 64; k++) x[k] = __uint_as_float(y[k >> 5][k & 31]);
+                float mx[4];
 #pragma unroll
-                    for (int x = 0; x < 2; x++) {
-                        if (2 * t + x == gi) w[x] = hi;
-                        if (2 * t + x == NG + gi) w[x] = lo;
+                for (int k = 0; k < 4; k++) {
+                    mx[k] = fmaxf(x[k], x[4 + k]);
+#pragma unroll
+                    for (int c = 8; c < 64; c += 8) mx[k] = tc::max3f(mx[k], x[c + k], x[c + 4 + k]);
+                }
+                const float top = fmaxf(tc::max3f(mx[0], mx[1], mx[2]), mx[3]);
+                const bool move = top > m + a.slack;
+                const bool moved = __any_sync(0xffffffffu, move);
+                float al = 1.f;
+                if (moved) {
+                    const float mn = move ? top : m;
+                    al = move ? ex2((m - mn) * p.scale_log2) : 1.f;
+                    m = mn;
+                    l *= al;
+                }
+                const float mu = m == kNegInf ? 0.f : -m * p.scale_log2;
+                const unsigned long long sc2 = tc::f2_pack(p.scale_log2, p.scale_log2), mu2 = tc::f2_pack(mu, mu);
+                unsigned long long ls[2] = {0ull, 0ull};
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+#pragma unroll
+                    for (int k = 32 * h; k < 32 * h + 32; k += 2) {
+                        tc::f2_unpack(tc::f2_fma(tc::f2_pack(x[k], x[k + 1]), sc2, mu2), x[k], x[k + 1]);
+                        x[k] = ex2(x[k]);
+                        x[k + 1] = ex2(x[k + 1]);
+                        ls[k / 2 & 1] = tc::f2_add(ls[k / 2 & 1], tc::f2_pack(x[k], x[k + 1]));
+                    }
+                    unsigned pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; k++) pk[k] = pack_half2(x[32 * h + 2 * k], x[32 * h + 2 * k + 1]);
+                    tmem_st16(tS + 16 * h, pk);
+                }
+                float l0, l1;
+                tc::f2_unpack(tc::f2_add(ls[0], ls[1]), l0, l1);
+                l += l0 + l1;
+                if (v_odd & 0x01010101u) rows_fix_weights(tS, *reinterpret_cast<const unsigned long long *>(sm.vbig[j & 3]));
+                if (moved && st > 1) {      // O holds the stages before
+                    ok = rows_wait(bar(ROWS_PVDONE + e), ((j - 2) >> 1) & 1, abort_p);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    tc::tc_fence_after();
+                    rows_scale<D>(tO, al);
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {      // (the warp's others wait for the next S)
+                    tc::mbar_arrive(bar(ROWS_PREADY + e));
+                    if ((warp & 3) == 0) {      // O (+)= P V
+                        ok = rows_wait(bar(ROWS_PREADY + e), (j >> 1) & 1, abort_p);
+                        if (ok) {
+                            tc::tc_fence_after();
+                            const uint64_t vd = pinned(tc::sw128_desc(smem_u32(sm.v[e]), S::kKHalf));
+#pragma unroll
+                            for (int kk = 0; kk < kRowsKeys / 16; kk++)
+                                tc::umma_ts(tmem + kRowsColO + 128 * e, tmem + kRowsColS + 64 * e + 8 * kk, vd + kk * (2048 >> 4), id_o,
+                                            st > 1 || kk > 0);
+                            tc::umma_commit(bar(ROWS_PVDONE + e));
+                        }
+                        if (ok && st + 2 < r.n_st) {
+                            ok = rows_wait(bar(ROWS_PVDONE + e), (j >> 1) & 1, abort_p);
+                            if (ok) issue_s(j + 2);
+                        }
                     }
                 }
-                const __half2 h = __halves2half2(w[0], w[1]);
-                qz[r] = *reinterpret_cast<const unsigned *>(&h);
             }
-        }
-        RowsState<D> s;
-        s.e = 0;
-#pragma unroll
-        for (int e = 0; e < 4; e++) {
-            s.z[e] = 0.f;
-#pragma unroll
-            for (int d = 0; d < NT; d++) s.o[d][e] = 0.f;
-        }
-        s.m[0] = s.m[1] = kNegInf;
-        s.l[0] = s.l[1] = 0.f;
-        if (tid < 4) sm.e[tid] = 0;
-        __syncthreads();
-        if (n_st > 0) {
-            cp_async_wait<S::kStages - 2>();
-            Pieces<D, GROUP>::unpack(sm.t[0], &sm.e[0], raw);
-            fetch();
-        }
-        __syncthreads();
-        for (int st = 0; st < n_st; st++) {
-            if (st + 1 < n_st) {
-                cp_async_wait<S::kStages - 2>();
-                Pieces<D, GROUP>::unpack(sm.t[(st + 1) & 1], &sm.e[(st + 1) & 3], raw + (st + 1) % S::kStages * S::kRaw);
-                fetch();
-            }
-            const int key0 = (page0 + 4 * st) * kBlock;
-            if (tid == 0) sm.e[(st + 2) & 3] = 0;      // (last read two stages ago, written in the next one)
-            if (active && key0 < most) {
-                if (key0 + kRowsKeys <= least)
-                    rows_stage<D, GROUP, true>(sm.t[st & 1], sm.e[st & 3], lane, qf, qz, end, key0, s, scale, slack);
-                else
-                    rows_stage<D, GROUP, false>(sm.t[st & 1], sm.e[st & 3], lane, qf, qz, end, key0, s, scale, slack);
-            }
-            __syncthreads();
-        }
-        cp_async_wait<0>();
-        if (active) {
-            const float up = __int_as_float((s.e - 15 + 127) << 23);      // 1 / scale_down
-#pragma unroll
-            for (int r = 0; r < 2; r++) {
-                float L = s.l[r];
-                L += __shfl_xor_sync(0xffffffffu, L, 1);
-                L += __shfl_xor_sync(0xffffffffu, L, 2);
-                const float inv = L == 0.f ? 0.f : __fdividef(1.f, L), f = up * inv;
-                float zg[NG];
-#pragma unroll
-                for (int gi = 0; gi < NG; gi++) {
-                    // columns gi and NG + gi of the row, two to a lane
-                    const float hi = __shfl_sync(0xffffffffu, s.z[2 * r + gi % 2], (lane & ~3) + gi / 2);
-                    const float lo = __shfl_sync(0xffffffffu, s.z[2 * r + (NG + gi) % 2], (lane & ~3) + (NG + gi) / 2);
-                    zg[gi] = (hi + lo) * inv;
-                }
-                const int v = vw + g + 8 * r;
-                if (v > vlast) continue;
-                const int i = v / p.G, h = hk * p.G + v - i * p.G;
-                const size_t pr = (size_t)a.rows0 + ((size_t)part * p.max_q_total + sm.s.qo[b] + i) * p.H + h;
+            // the two halves of the stages together: half of the dimensions each
+            sm.ml[e][row] = make_float2(m, l);
+            sm.nan[e][row] = nan;
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+            const int first = J & 1;      // (the half that has the item's first stage)
+            if (r.n_st > 0) ok = ok && rows_wait(bar(ROWS_PVDONE + ((J + r.n_st - 1) & 1)), ((J + r.n_st - 1) >> 1) & 1, abort_p);
+            if (r.n_st > 1) ok = ok && rows_wait(bar(ROWS_PVDONE + ((J + r.n_st) & 1)), ((J + r.n_st - 2) >> 1) & 1, abort_p);
+            if (__all_sync(0xffffffffu, ok)) {
+                tc::tc_fence_after();
+                const float2 x0 = sm.ml[first][row], x1 = sm.ml[first ^ 1][row];
+                const float M = fmaxf(x0.x, x1.x), mu = M == kNegInf ? 0.f : M;
+                float f0 = ex2((x0.x - mu) * p.scale_log2), f1 = ex2((x1.x - mu) * p.scale_log2);
+                const float L = fmaf(x0.y, f0, x1.y * f1), inv = L == 0.f ? 0.f : __fdividef(1.f, L);      // (a NaN goes on)
+                f0 *= inv;
+                f1 *= inv;
+                nan = sm.nan[0][row] | sm.nan[1][row];
+                const int v = r.v0 + row, i = v / p.G;
+                const size_t pr = (size_t)a.rows0 + ((size_t)r.part * p.max_q_total + sm.s.qo[r.b] + i) * p.H + r.hk * p.G + v - i * p.G;
                 float *po = p.part_o + pr * D;
+                const unsigned t0 = tmem + kRowsColO + 128 * first + lane_off, t1 = tmem + kRowsColO + 128 * (first ^ 1) + lane_off;
+#pragma unroll 1
+                for (int c = e * (D / 2); c < (e + 1) * (D / 2); c += 32) {
+                    float y[32];
 #pragma unroll
-                for (int d = 0; d < NT; d++) {
-                    __stcg(po + 8 * d + t, s.o[d][2 * r] * f + zg[8 * d / GROUP]);
-                    __stcg(po + 8 * d + t + 4, s.o[d][2 * r + 1] * f + zg[8 * d / GROUP]);
+                    for (int k = 0; k < 32; k++) y[k] = 0.f;
+                    unsigned o[32];
+                    if (r.n_st > 0) {
+                        tc::tmem_ld32(t0 + c, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k++) y[k] = __uint_as_float(o[k]) * f0;
+                    }
+                    if (r.n_st > 1) {
+                        tc::tmem_ld32(t1 + c, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; k++) y[k] = fmaf(__uint_as_float(o[k]), f1, y[k]);
+                    }
+                    if (nan >> (c / GROUP) & 1) {
+#pragma unroll
+                        for (int k = 0; k < 32; k++) y[k] = __int_as_float(0x7fffffff);
+                    }
+                    if (!have) continue;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 8) {
+                        __stcg(reinterpret_cast<float4 *>(po + c + k), make_float4(y[k], y[k + 2], y[k + 4], y[k + 6]));
+                        __stcg(reinterpret_cast<float4 *>(po + c + k + 4), make_float4(y[k + 1], y[k + 3], y[k + 5], y[k + 7]));
+                    }
                 }
-                if (t == 0) __stcg(p.part_lse + pr, L == 0.f ? kNegInf : fmaf(s.m[r], scale, lg2(L)));
+                if (have && e == 0) __stcg(p.part_lse + pr, L == 0.f ? kNegInf : fmaf(M, p.scale_log2, lg2(L)));
+            }
+        } else if (warp < 12) {
+            // ------------------------------------------------------------ K
+            const int u = tid - 256;
+            const int *table = p.block_tables + (size_t)r.b * p.max_blocks;
+            const unsigned char *codes = X::at_codes(a.pool.k, u, r.hk), *pairs = X::at_pairs(a.pool.ksz, u, r.hk);
+            int blk[X::N];
+            X x, next;
+            X::ids(table, u, r.page0, r.end_page, blk);
+            next.load(p, codes, pairs, u, r.page0, r.end_page, r.n, blk);
+            X::ids(table, u, r.page0 + 4, r.end_page, blk);
+#pragma unroll 1
+            for (int st = 0; st < r.n_st; st++) {
+                const int j = J + st, e = j & 1, page = r.page0 + 4 * (st + 1);
+                x = next;      // (asked for a stage ago)
+                next.load(p, codes, pairs, u, page, r.end_page, r.n, blk);
+                X::ids(table, u, page + 4, r.end_page, blk);
+                // S(j - 2), the last reader of the K tiles
+                if (j > 1) ok = rows_wait(bar(ROWS_SFULL + e), ((j - 2) >> 1) & 1, abort_p);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                x.unpack_k(sm, e, j & 3, u);
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar(ROWS_KFULL + e));
+            }
+        } else {
+            // ------------------------------------------------------------ V
+            const int u = tid - 384;
+            const int *table = p.block_tables + (size_t)r.b * p.max_blocks;
+            const unsigned char *codes = X::at_codes(a.pool.v, u, r.hk), *pairs = X::at_pairs(a.pool.vsz, u, r.hk);
+            int blk[X::N];
+            X x, next;
+            X::ids(table, u, r.page0, r.end_page, blk);
+            next.load(p, codes, pairs, u, r.page0, r.end_page, r.n, blk);
+            X::ids(table, u, r.page0 + 4, r.end_page, blk);
+#pragma unroll 1
+            for (int st = 0; st < r.n_st; st++) {
+                const int j = J + st, e = j & 1, page = r.page0 + 4 * (st + 1);
+                x = next;      // (asked for a stage ago)
+                next.load(p, codes, pairs, u, page, r.end_page, r.n, blk);
+                X::ids(table, u, page + 4, r.end_page, blk);
+                // PV(j - 2), the last reader of the V tile
+                if (j > 1) ok = rows_wait(bar(ROWS_PVDONE + e), ((j - 2) >> 1) & 1, abort_p);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                x.unpack_v(sm, e, j & 3, u);
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar(ROWS_VFULL + e));
             }
         }
-        if (tid == 0) sm.s.next = (int)(gridDim.x + atomicAdd(&p.ctrl[CTRL_Q4_ROWS], 1u));
+        __syncwarp();
+        J += r.n_st;      // (before the barrier behind which r is another item)
+        q_items += r.n_st > 0;
+        tc::tc_fence_before();
+        __syncthreads();
+        tc::tc_fence_after();
+        if (tid == 0) {
+            const int next = (int)(gridDim.x + atomicAdd(&p.ctrl[CTRL_Q4_ROWS], 1u));
+            sm.s.next = *abort_p ? n_items : next;
+            if (next < n_items) sm.r = rows_item(p, sm.s, next, split);
+        }
         __syncthreads();
         item = sm.s.next;
-        __syncthreads();
+    }
+    // after a wait that gave up: the MMAs in flight, of the two threads that issue them
+    if (*abort_p && lane == 0 && (warp == 0 || warp == 4)) tc::umma_commit(bar(ROWS_FIN));
+    if (warp == 8) {
+        if (lane == 0 && *abort_p) {
+            atomicOr(&p.ctrl[CTRL_FLAGS], RELAY_FLAG_WAIT_TIMEOUT);
+            tc::mbar_drain(bar(ROWS_FIN), 0);
+        }
+        __syncwarp();
+        tc::tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "n"(kRowsTmem) : "memory");
     }
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }

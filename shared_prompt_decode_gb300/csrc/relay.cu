@@ -116,7 +116,7 @@ Q4Kernel q4_kernel(int D, int group, long long cols)
 template <int D, int GROUP>
 Q4Kernel rows_instance()
 {
-    return {q4::rows_kernel<D, GROUP>, 8, sizeof(q4::RowsSmem<D, GROUP>)};
+    return {q4::rows_kernel<D, GROUP>, q4::kRowsThreads / 32, q4::kRowsSmem<D, GROUP>};
 }
 Q4Kernel rows_kernel(int D, int group)
 {
@@ -1187,10 +1187,10 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(dev->sms);
     cfg.stream = s;
     cfg.attrs = attr;
-    auto launch = [&](const Q4Kernel &k) {
+    auto launch = [&](const Q4Kernel &k, int per_sm) {
+        cfg.gridDim = dim3(per_sm * dev->sms);
         cfg.blockDim = dim3(32 * k.warps);
         cfg.dynamicSmemBytes = k.smem;
         cfg.numAttrs = front ? 1 : 0;
@@ -1200,9 +1200,9 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     cudaError_t e = cudaSuccess;
     if (pl.rows_max < INT_MAX) {      // some request may be a prompt chunk
         a.queue = 1;
-        e = launch(rows_kernel(d->D, cache->group));
+        e = launch(rows_kernel(d->D, cache->group), 1);
     }
-    if (e == cudaSuccess) e = launch(q4_kernel(d->D, cache->group, pl.line_cols));
+    if (e == cudaSuccess) e = launch(q4_kernel(d->D, cache->group, pl.line_cols), 1);
     if (e == cudaSuccess) {
         const long long rows = (long long)p.max_q_total * d->H;
         // a few rows: four warps each; up to a GPU full of warps: one each, with all

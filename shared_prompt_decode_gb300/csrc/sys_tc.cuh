@@ -240,7 +240,7 @@ __device__ __forceinline__ uint64_t sw128_desc(unsigned saddr, unsigned lbo = 16
 
 // Instruction descriptor, kind::f16: fp16 A and B, fp32 accumulator, shape
 // M x N, A K-major, B K-major or (b_mn) MN-major.
-__device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn = false)
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn = false)
 {
     return (1u << 4)                          // D: fp32
          | (0u << 7) | (0u << 10)             // A, B: fp16
