@@ -1642,17 +1642,15 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
 // ----------------------------------------------------------------------------- attention: prompt chunks
 // Requests of more columns than the line takes: a dense contraction, on the
 // 5th-generation tensor cores.  A CTA takes 128 columns of one KV head (a TMEM
-// lane each) against a range of the context, 64 keys a stage, two stages at a
-// time.  Its warps:
+// lane each) against a range of the context, 64 keys a stage.  Its warps:
 //   0-3, 4-7   softmax of the even and of the odd stages, each with a reference,
 //              a sum and an O of its own (joined at the item's end): thread t of
 //              them has column t, so a maximum needs no other lane.  One thread
 //              of each issues the products: a stage's P V, then, when P has been
 //              read, the Q K^T of the stage after the next in its place.
-//   8-11       unpack K: codes and pairs come from global memory to registers
-//              a stage ahead, and go to shared memory as fp16 tiles (128-byte
-//              swizzle).
-//   12-15      unpack V.
+//   8-15       unpack: codes and pairs come from global memory to registers a
+//              stage ahead, and go to shared memory as fp16 tiles (128-byte
+//              swizzle), three stages of them.
 // With c the codes and s = s' + s" a scale cut after 7 bits, c s' and c s" are
 // exact in fp16, and so is S but for its fp32 sums:
 //     S = Q (c s')^T + Q (c s")^T + sum(q) z^T      (M 128, N 64, K 2 D + 16)
@@ -1684,10 +1682,11 @@ struct RowsSmem {
     static constexpr int NG = D / GROUP, KH = D / 64;      // KH: 64-dimension halves of a row
     static constexpr int kQHalf = kRowsTile * 128, kKHalf = kRowsKeys * 128;
     unsigned char q[KH * kQHalf];
-    unsigned char k[2][2][KH * kKHalf];      // stages 2i, 2i + 1: c s', c s"
-    unsigned char v[2][KH * kKHalf];
+    static constexpr int kStages = 3;
+    unsigned char k[kStages][2][KH * kKHalf];      // c s', c s"
+    unsigned char v[kStages][KH * kKHalf];
     unsigned char qz[kRowsTile * 32];        // [16][2][8] pieces of 16 bytes: row, half of the 16 terms
-    unsigned char kz[2][kRowsKeys * 32];
+    unsigned char kz[kStages][kRowsKeys * 32];
     unsigned long long bar[16];
     // stage i mod 4: a bit a key (a byte eight of them); v_odd: 1 scaled, 2 no number
     unsigned char kbig[4][8], vbig[4][8], vnan[4][NG][8], v_odd[4][8];
@@ -1700,8 +1699,9 @@ struct RowsSmem {
 };
 template <int D, int GROUP>
 constexpr size_t kRowsSmem = sizeof(RowsSmem<D, GROUP>) + 1024;      // (from a 1024-byte boundary on)
-enum { ROWS_QFULL, ROWS_FIN, ROWS_KFULL, ROWS_VFULL = ROWS_KFULL + 2, ROWS_SFULL = ROWS_VFULL + 2,
-       ROWS_PREADY = ROWS_SFULL + 2, ROWS_PVDONE = ROWS_PREADY + 2 };
+// full, free: of a stage's tiles; the others of the even and the odd stages
+enum { ROWS_QFULL, ROWS_FIN, ROWS_SFULL, ROWS_PREADY = ROWS_SFULL + 2, ROWS_PVDONE = ROWS_PREADY + 2, ROWS_FULL = ROWS_PVDONE + 2,
+       ROWS_FREE = ROWS_FULL + 3 };
 constexpr unsigned kRowsTmem = 512, kRowsColS = 0, kRowsColO = 128;      // S (or P) of stage i: 64 (i & 1); O: 128 (i & 1)
 
 // descriptor of 8 x 16-byte pieces without swizzle: the row's next 16 bytes
@@ -1820,6 +1820,8 @@ __device__ __forceinline__ bool rows_wait(unsigned bar, unsigned parity, volatil
 {
     return tc::mbar_try(bar, parity) || rows_wait_long(bar, parity, abort);
 }
+// All ones in the bytes of x that have bit `b`.
+__device__ __forceinline__ unsigned rows_bytes(unsigned x, unsigned b) { return (x & 0x01010101u * b) / b * 255u; }
 // Scores in TMEM: the keys of `big` times 2048, those from `seen` on hidden.
 __device__ __noinline__ void rows_fix_scores(unsigned tS, unsigned long long big, int seen)
 {
@@ -1867,21 +1869,23 @@ __device__ __noinline__ void rows_scale(unsigned tO, float f)
     }
 }
 
-// A thread's part of a stage on its way, of K or of V: 32 dimensions of N keys.
-// Eight lanes that store together are four keys and two neighbouring pieces: no
-// bank twice.
+// A thread's part of a stage on its way: 32 dimensions of a key, of K and of V
+// (D = 128; D = 64: the first four warps have K, the others V).  Eight lanes
+// that store together are four keys and two neighbouring pieces: no bank twice.
 template <int D, int GROUP>
 struct Pieces {
     using S = RowsSmem<D, GROUP>;
-    static constexpr int NG = S::NG, N = D / 64;
+    static constexpr int NG = S::NG;
     static constexpr int kBytes = D == 128 ? 1 : 2;      // a warp's keys are eight, or 16
-    uint4 c[N];
-    unsigned sz[N];
+    uint4 k, v;
+    unsigned ksz, vsz;
 
+    static __device__ __forceinline__ bool has_k(int u) { return D == 128 || u < 128; }
+    static __device__ __forceinline__ bool has_v(int u) { return D == 128 || u >= 128; }
     static __device__ __forceinline__ int piece(int u) { return D == 128 ? (u & 1) | (u >> 2 & 2) : u & 1; }
-    static __device__ __forceinline__ int key(int u, int i)
+    static __device__ __forceinline__ int key(int u)
     {
-        return D == 128 ? (u >> 5) * 8 + (u >> 1 & 3) + (u >> 2 & 4) + 32 * i : u >> 1;
+        return D == 128 ? (u >> 5) * 8 + (u >> 1 & 3) + (u >> 2 & 4) : u >> 1 & 63;
     }
     static __device__ __forceinline__ unsigned key_lanes(int first) { return (D == 128 ? 0x303u : 3u) << first; }
     // the warp's keys of a ballot: byte `lane` of them
@@ -1889,45 +1893,38 @@ struct Pieces {
     {
         unsigned r = 0;
 #pragma unroll
-        for (int k = 0; k < 8 * kBytes; k++) r |= (b & key_lanes(D == 128 ? (k & 3) << 1 | (k & 4) << 2 : 2 * k)) ? 1u << k : 0u;
+        for (int i = 0; i < 8 * kBytes; i++) r |= (b & key_lanes(D == 128 ? (i & 3) << 1 | (i & 4) << 2 : 2 * i)) ? 1u << i : 0u;
         return (unsigned char)(r >> (8 * lane & 31));
     }
     static __device__ __forceinline__ bool of_key(unsigned b, int lane) { return b & key_lanes(lane & (D == 128 ? ~9 : ~1)); }
 
-    static __device__ __forceinline__ void ids(const int *table, int u, int page0, int end, int (&blk)[N])
+    static __device__ __forceinline__ int id(const int *table, int u, int page0, int end)
     {
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int page = page0 + key(u, i) / kBlock;
-            blk[i] = -1;
-            if (page < end) blk[i] = __ldg(table + page);
-        }
+        const int page = page0 + key(u) / kBlock;
+        return page < end ? __ldg(table + page) : -1;
     }
-    // codes, pairs: those of the thread's first key and piece in block 0
-    __device__ __forceinline__ void load(const Params &p, const unsigned char *codes, const unsigned char *pairs, int u, int page0, int end,
-                                         int n, const int (&blk)[N])
+    // codes, pairs: places of the thread's key and piece in a block
+    __device__ __forceinline__ void load(const Params &p, const Pool &pool, unsigned codes, unsigned pairs, int u, int page0, int end,
+                                         int n, int blk)
     {
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            c[i] = make_uint4(0u, 0u, 0u, 0u);
-            sz[i] = 0u;
-            if ((unsigned)blk[i] >= (unsigned)p.num_blocks) {
-                if (page0 + key(u, i) / kBlock < end) atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
-            } else {
-                c[i] = __ldg(reinterpret_cast<const uint4 *>(codes + (size_t)blk[i] * (unsigned)(p.Hkv * kBlock * (D / 2))));
-                // pairs of tokens behind the last one are zero
-                if (page0 * kBlock + key(u, i) < n)
-                    sz[i] = __ldg(reinterpret_cast<const unsigned *>(pairs + (size_t)blk[i] * (unsigned)(p.Hkv * kBlock * NG * 4)));
+        k = v = make_uint4(0u, 0u, 0u, 0u);
+        ksz = vsz = 0u;
+        if ((unsigned)blk >= (unsigned)p.num_blocks) {
+            if (page0 + key(u) / kBlock < end) atomicOr(&p.ctrl[CTRL_FLAGS], FLAG_BAD_BLOCK);
+        } else {
+            const size_t at = (size_t)blk * (unsigned)(p.Hkv * kBlock * (D / 2)) + codes;
+            const size_t at_sz = (size_t)blk * (unsigned)(p.Hkv * kBlock * NG) + pairs;
+            // pairs of tokens behind the last one are zero
+            const bool in = page0 * kBlock + key(u) < n;
+            if (has_k(u)) {
+                k = __ldg(reinterpret_cast<const uint4 *>(pool.k + at));
+                if (in) ksz = __ldg(reinterpret_cast<const unsigned *>(pool.ksz) + at_sz);
+            }
+            if (has_v(u)) {
+                v = __ldg(reinterpret_cast<const uint4 *>(pool.v + at));
+                if (in) vsz = __ldg(reinterpret_cast<const unsigned *>(pool.vsz) + at_sz);
             }
         }
-    }
-    static __device__ __forceinline__ const unsigned char *at_codes(const unsigned char *codes, int u, int hk)
-    {
-        return codes + ((size_t)hk * kBlock + key(u, 0) % kBlock) * (D / 2) + 16 * piece(u);
-    }
-    static __device__ __forceinline__ const unsigned char *at_pairs(const __half2 *pairs, int u, int hk)
-    {
-        return reinterpret_cast<const unsigned char *>(pairs + ((size_t)hk * kBlock + key(u, 0) % kBlock) * NG + piece(u) * 32 / GROUP);
     }
     // Codes of word w, dimensions k and k + 4, as halves 1024 + c (k even) and 64 + c.
     static __device__ __forceinline__ void raised(unsigned w, __half2 (&c)[4])
@@ -1944,13 +1941,13 @@ struct Pieces {
     {
         const int ch = piece(u);
         unsigned x;      // (not kept through the loop in 24 addresses)
-        asm volatile("add.u32 %0, %1, %2;" : "=r"(x) : "r"(tile), "r"((ch >> 1) * S::kKHalf + tc::sw_off(key(u, 0), 4 * (ch & 1))));
+        asm volatile("add.u32 %0, %1, %2;" : "=r"(x) : "r"(tile), "r"((ch >> 1) * S::kKHalf + tc::sw_off(key(u), 4 * (ch & 1))));
         return x;
     }
-    static __device__ __forceinline__ void put(unsigned at, int i, int j, const __half2 (&x)[4])
+    static __device__ __forceinline__ void put(unsigned at, int j, const __half2 (&x)[4])
     {
         const unsigned *w = reinterpret_cast<const unsigned *>(x);
-        sts128((at ^ (j << 4)) + i * 4096, w[0], w[1], w[2], w[3]);      // (32 keys on)
+        sts128(at ^ (j << 4), w[0], w[1], w[2], w[3]);
     }
     static __device__ __forceinline__ float2 pair(unsigned w) { return __half22float2(*reinterpret_cast<const __half2 *>(&w)); }
     static __device__ __forceinline__ __half2 both(unsigned w, unsigned sel)
@@ -1967,82 +1964,75 @@ struct Pieces {
     }
     // c s = (1024 + c) s - 1024 s, exact for a scale of at most seven bits
     // whose 1024 s is a half, and the same with 64.
-    __device__ __forceinline__ void unpack_k(S &sm, int e, int slot, int u)
+    __device__ __forceinline__ void unpack_k(S &sm, int at, int slot, int u)
     {
-        const int lane = u & 31, ch = piece(u);
-        const unsigned to = first(smem_u32(sm.k[e][0]), u);
+        const int lane = u & 31, ch = piece(u), kk = key(u);
+        const unsigned to = first(smem_u32(sm.k[at][0]), u);
+        const float2 f = pair(ksz);
+        const unsigned any = __ballot_sync(0xffffffffu, fabsf(f.x) >= 60.f || fabsf(f.y) >= 511.f);
+        unsigned char bits = 0;
+        if (any) {
+            bits = keys_of(any, lane);
+            if (of_key(any, lane)) times(ksz, 0x1p-11f);
+        }
+        if (lane < kBytes) sm.kbig[slot][kk / 8 + lane] = bits;
+        const unsigned s1 = __byte_perm(ksz, 0u, 0x1010), s1h = s1 & 0xfff0fff0u;
+        const __half2 sh = *reinterpret_cast<const __half2 *>(&s1h), sl = __hsub2(*reinterpret_cast<const __half2 *>(&s1), sh);
+        const __half2 k0 = __floats2half2_rn(-1024.f, -1024.f), k1 = __floats2half2_rn(-64.f, -64.f);
+        const __half2 sh0 = __hmul2(sh, k0), sh1 = __hmul2(sh, k1), sl0 = __hmul2(sl, k0), sl1 = __hmul2(sl, k1);
+        const unsigned w[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int kk = key(u, i);
-            const float2 f = pair(sz[i]);
-            const unsigned any = __ballot_sync(0xffffffffu, fabsf(f.x) >= 60.f || fabsf(f.y) >= 511.f);
-            if (lane < kBytes) sm.kbig[slot][kk / 8 + lane] = any ? keys_of(any, lane) : (unsigned char)0;
-            if (any && of_key(any, lane)) times(sz[i], 0x1p-11f);
-            const unsigned s1 = __byte_perm(sz[i], 0u, 0x1010), s1h = s1 & 0xfff0fff0u;
-            const __half2 sh = *reinterpret_cast<const __half2 *>(&s1h), sl = __hsub2(*reinterpret_cast<const __half2 *>(&s1), sh);
-            const __half2 k0 = __floats2half2_rn(-1024.f, -1024.f), k1 = __floats2half2_rn(-64.f, -64.f);
-            const __half2 sh0 = __hmul2(sh, k0), sh1 = __hmul2(sh, k1), sl0 = __hmul2(sl, k0), sl1 = __hmul2(sl, k1);
-            const unsigned w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+        for (int j = 0; j < 4; j++) {
+            __half2 x[4], h[4], l[4];
+            raised(w[j], x);
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                __half2 x[4], h[4], l[4];
-                raised(w[j], x);
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    h[k] = __hfma2(x[k], sh, k & 1 ? sh1 : sh0);
-                    l[k] = __hfma2(x[k], sl, k & 1 ? sl1 : sl0);
-                }
-                put(to, i, j, h);
-                put(to + S::KH * S::kKHalf, i, j, l);
+            for (int i = 0; i < 4; i++) {
+                h[i] = __hfma2(x[i], sh, i & 1 ? sh1 : sh0);
+                l[i] = __hfma2(x[i], sl, i & 1 ? sl1 : sl0);
             }
-            if (ch * 32 % GROUP == 0) {
-                const int gi = ch * 32 / GROUP;
-                const __half z = __hmul(__ushort_as_half((unsigned short)(sz[i] >> 16)), __float2half_rn(128.f));
-                __half *terms = reinterpret_cast<__half *>(sm.kz[e] + kk / 8 * 256 + kk % 8 * 16);
-                terms[gi] = z;
-                terms[NG + gi] = z;      // (at most eight terms: the first 16 bytes)
-            }
+            put(to, j, h);
+            put(to + S::KH * S::kKHalf, j, l);
+        }
+        if (ch * 32 % GROUP == 0) {
+            const int gi = ch * 32 / GROUP;
+            const __half z = __hmul(__ushort_as_half((unsigned short)(ksz >> 16)), __float2half_rn(128.f));
+            __half *terms = reinterpret_cast<__half *>(sm.kz[at] + kk / 8 * 256 + kk % 8 * 16);
+            terms[gi] = z;
+            terms[NG + gi] = z;      // (at most eight terms: the first 16 bytes)
         }
     }
-    __device__ __forceinline__ void unpack_v(S &sm, int e, int slot, int u)
+    __device__ __forceinline__ void unpack_v(S &sm, int at, int slot, int u)
     {
-        const int lane = u & 31, ch = piece(u);
-        const unsigned to = first(smem_u32(sm.v[e]), u);
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int at = key(u, i) / 8 + lane;
-            const float2 f = pair(sz[i]);
-            const bool odd = !(fmaf(15.f, fabsf(f.x), fabsf(f.y)) < 65504.f);
-            if (__any_sync(0xffffffffu, odd)) {
-                const bool num = number(sz[i]);
-                const unsigned any = __ballot_sync(0xffffffffu, num && odd), none = __ballot_sync(0xffffffffu, !num);
-                if (lane < kBytes) {
-                    sm.v_odd[slot][at] = (any ? 1 : 0) | (none ? 2 : 0);
-                    sm.vbig[slot][at] = keys_of(any, lane);
-                }
-#pragma unroll
-                for (int gi = 0; gi < NG; gi++) {
-                    const unsigned g = __ballot_sync(0xffffffffu, !num && ch * 32 / GROUP == gi);
-                    if (lane < kBytes) sm.vnan[slot][gi][at] = keys_of(g, lane);
-                }
-                if (!num) sz[i] = 0u;
-                if (of_key(any, lane)) times(sz[i], 0x1p-5f);
-            } else if (lane < kBytes) {
-                sm.v_odd[slot][at] = sm.vbig[slot][at] = 0;
-#pragma unroll
-                for (int gi = 0; gi < NG; gi++) sm.vnan[slot][gi][at] = 0;
+        const int lane = u & 31, ch = piece(u), byte = key(u) / 8 + lane;
+        const unsigned to = first(smem_u32(sm.v[at]), u);
+        const float2 f = pair(vsz);
+        const bool odd = !(fmaf(15.f, fabsf(f.x), fabsf(f.y)) < 65504.f);
+        unsigned char bits = 0;
+        if (__any_sync(0xffffffffu, odd)) {
+            const bool num = number(vsz);
+            const unsigned any = __ballot_sync(0xffffffffu, num && odd), none = __ballot_sync(0xffffffffu, !num);
+            const unsigned char b = keys_of(any, lane);
+            if (lane < kBytes) sm.vbig[slot][byte] = b;
+#pragma unroll 1
+            for (int gi = 0; gi < NG; gi++) {
+                const unsigned char g = keys_of(__ballot_sync(0xffffffffu, !num && ch * 32 / GROUP == gi), lane);
+                if (lane < kBytes) sm.vnan[slot][gi][byte] = g;
             }
-            const __half2 s = both(sz[i], 0x1010), z = both(sz[i], 0x3232);
-            const __half2 k0 = __floats2half2_rn(-1024.f, -1024.f), k1 = __floats2half2_rn(-64.f, -64.f);
-            const unsigned w[4] = {c[i].x, c[i].y, c[i].z, c[i].w};
+            bits = (any ? 1 : 0) | (none ? 2 : 0);
+            if (!num) vsz = 0u;
+            if (of_key(any, lane)) times(vsz, 0x1p-5f);
+        }
+        if (lane < kBytes) sm.v_odd[slot][byte] = bits;
+        const __half2 s = both(vsz, 0x1010), z = both(vsz, 0x3232);
+        const __half2 k0 = __floats2half2_rn(-1024.f, -1024.f), k1 = __floats2half2_rn(-64.f, -64.f);
+        const unsigned w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                __half2 x[4];
-                raised(w[j], x);
+        for (int j = 0; j < 4; j++) {
+            __half2 x[4];
+            raised(w[j], x);
 #pragma unroll
-                for (int k = 0; k < 4; k++) x[k] = __hfma2(__hadd2(x[k], k & 1 ? k1 : k0), s, z);
-                put(to, i, j, x);
-            }
+            for (int i = 0; i < 4; i++) x[i] = __hfma2(__hadd2(x[i], i & 1 ? k1 : k0), s, z);
+            put(to, j, x);
         }
     }
 };
@@ -2098,9 +2088,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         sm.abort = 0;
         tc::mbar_init(bar(ROWS_QFULL), 4);
         tc::mbar_init(bar(ROWS_FIN), 2);
+        for (int i = 0; i < S::kStages; i++) {
+            tc::mbar_init(bar(ROWS_FULL + i), 8);
+            tc::mbar_init(bar(ROWS_FREE + i), 1);
+        }
         for (int i = 0; i < 2; i++) {
-            tc::mbar_init(bar(ROWS_KFULL + i), 4);
-            tc::mbar_init(bar(ROWS_VFULL + i), 4);
             tc::mbar_init(bar(ROWS_SFULL + i), 1);
             tc::mbar_init(bar(ROWS_PREADY + i), 4);
             tc::mbar_init(bar(ROWS_PVDONE + i), 1);
@@ -2108,7 +2100,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         sm.r = rows_item(p, sm.s, blockIdx.x, split);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    for (int i = tid; i < kRowsKeys * 16; i += kRowsThreads) reinterpret_cast<unsigned *>(sm.kz)[i] = 0u;      // terms that no group has
+    for (int i = tid; i < (int)sizeof(sm.kz) / 4; i += kRowsThreads) reinterpret_cast<unsigned *>(sm.kz)[i] = 0u;      // terms that no group has
     tc::fence_async_smem();
     tc::tc_fence_before();
     __syncthreads();
@@ -2181,12 +2173,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 }
             }
             auto issue_s = [&](int j) {      // S = Q K^T, by one thread
-                ok = rows_wait(bar(ROWS_KFULL + e), (j >> 1) & 1, abort_p);
+                const int at = j % S::kStages;
+                ok = rows_wait(bar(ROWS_FULL + at), (j / S::kStages) & 1, abort_p);
                 if (!ok) return;
                 tc::tc_fence_after();
                 const unsigned d0 = tmem + kRowsColS + 64 * e;
-                tc::umma_ss(d0, pinned(plain_desc(smem_u32(sm.qz))), pinned(plain_desc(smem_u32(sm.kz[e]))), id_s, 0);
-                const uint64_t qd = pinned(tc::sw128_desc(smem_u32(sm.q))), kd = pinned(tc::sw128_desc(smem_u32(sm.k[e][0])));
+                tc::umma_ss(d0, pinned(plain_desc(smem_u32(sm.qz))), pinned(plain_desc(smem_u32(sm.kz[at]))), id_s, 0);
+                const uint64_t qd = pinned(tc::sw128_desc(smem_u32(sm.q))), kd = pinned(tc::sw128_desc(smem_u32(sm.k[at][0])));
 #pragma unroll
                 for (int kk = 0; kk < 2 * D / 16; kk++) {
                     const int d = kk % (D / 16);
@@ -2206,20 +2199,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             const unsigned tS = tmem + kRowsColS + 64 * e + lane_off, tO = tmem + kRowsColO + 128 * e + lane_off;
             for (int st = st0; st < r.n_st; st += 2) {
                 const int j = J + st, key0 = (r.page0 + 4 * st) * kBlock;
-                ok = ok && rows_wait(bar(ROWS_VFULL + e), (j >> 1) & 1, abort_p) && rows_wait(bar(ROWS_SFULL + e), (j >> 1) & 1, abort_p);
+                ok = ok && rows_wait(bar(ROWS_SFULL + e), (j >> 1) & 1, abort_p);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 tc::tc_fence_after();
                 const unsigned *flags = reinterpret_cast<const unsigned *>(sm.kbig[j & 3]);
                 const unsigned k0 = flags[0], k1 = flags[1];
                 flags = reinterpret_cast<const unsigned *>(sm.v_odd[j & 3]);
-                const unsigned v_odd = flags[0] | flags[1];
+                const unsigned v0 = flags[0], v1 = flags[1], v_odd = v0 | v1;
                 const int seen = end - key0;
                 if (__any_sync(0xffffffffu, seen < kRowsKeys || (k0 | k1))) rows_fix_scores(tS, (unsigned long long)k1 << 32 | k0, seen);
                 if (v_odd & 0x02020202u) {
+                    const unsigned long long odd = (unsigned long long)rows_bytes(v1, 2) << 32 | rows_bytes(v0, 2);
                     const unsigned long long mask = seen >= 64 ? ~0ull : seen <= 0 ? 0ull : (1ull << seen) - 1ull;
 #pragma unroll 1
                     for (int gi = 0; gi < NG; gi++)
-                        if (*reinterpret_cast<const unsigned long long *>(sm.vnan[j & 3][gi]) & mask) nan |= 1u << gi;
+                        if (*reinterpret_cast<const unsigned long long *>(sm.vnan[j & 3][gi]) & mask & odd) nan |= 1u << gi;
                 }
                 unsigned y[2][32];
                 tc::tmem_ld32(tS, y[0]);
@@ -2265,7 +2259,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 float l0, l1;
                 tc::f2_unpack(tc::f2_add(ls[0], ls[1]), l0, l1);
                 l += l0 + l1;
-                if (v_odd & 0x01010101u) rows_fix_weights(tS, *reinterpret_cast<const unsigned long long *>(sm.vbig[j & 3]));
+                if (v_odd & 0x01010101u)
+                    rows_fix_weights(tS, *reinterpret_cast<const unsigned long long *>(sm.vbig[j & 3]) &
+                                             ((unsigned long long)rows_bytes(v1, 1) << 32 | rows_bytes(v0, 1)));
                 if (moved && st > 1) {      // O holds the stages before
                     ok = rows_wait(bar(ROWS_PVDONE + e), ((j - 2) >> 1) & 1, abort_p);
                     if (!__all_sync(0xffffffffu, ok)) break;
@@ -2281,12 +2277,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                         ok = rows_wait(bar(ROWS_PREADY + e), (j >> 1) & 1, abort_p);
                         if (ok) {
                             tc::tc_fence_after();
-                            const uint64_t vd = pinned(tc::sw128_desc(smem_u32(sm.v[e]), S::kKHalf));
+                            const uint64_t vd = pinned(tc::sw128_desc(smem_u32(sm.v[j % S::kStages]), S::kKHalf));
 #pragma unroll
                             for (int kk = 0; kk < kRowsKeys / 16; kk++)
                                 tc::umma_ts(tmem + kRowsColO + 128 * e, tmem + kRowsColS + 64 * e + 8 * kk, vd + kk * (2048 >> 4), id_o,
                                             st > 1 || kk > 0);
                             tc::umma_commit(bar(ROWS_PVDONE + e));
+                            tc::umma_commit(bar(ROWS_FREE + j % S::kStages));
                         }
                         if (ok && st + 2 < r.n_st) {
                             ok = rows_wait(bar(ROWS_PVDONE + e), (j >> 1) & 1, abort_p);
@@ -2346,53 +2343,28 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 }
                 if (have && e == 0) __stcg(p.part_lse + pr, L == 0.f ? kNegInf : fmaf(M, p.scale_log2, lg2(L)));
             }
-        } else if (warp < 12) {
-            // ------------------------------------------------------------ K
+        } else {
+            // ------------------------------------------------------------ unpack
             const int u = tid - 256;
             const int *table = p.block_tables + (size_t)r.b * p.max_blocks;
-            const unsigned char *codes = X::at_codes(a.pool.k, u, r.hk), *pairs = X::at_pairs(a.pool.ksz, u, r.hk);
-            int blk[X::N];
+            const unsigned row = (unsigned)r.hk * kBlock + X::key(u) % kBlock;
+            const unsigned codes = row * (D / 2) + 16 * X::piece(u), pairs = row * NG + X::piece(u) * 32 / GROUP;
             X x, next;
-            X::ids(table, u, r.page0, r.end_page, blk);
-            next.load(p, codes, pairs, u, r.page0, r.end_page, r.n, blk);
-            X::ids(table, u, r.page0 + 4, r.end_page, blk);
+            next.load(p, a.pool, codes, pairs, u, r.page0, r.end_page, r.n, X::id(table, u, r.page0, r.end_page));
+            int blk = X::id(table, u, r.page0 + 4, r.end_page);
 #pragma unroll 1
             for (int st = 0; st < r.n_st; st++) {
-                const int j = J + st, e = j & 1, page = r.page0 + 4 * (st + 1);
+                const int j = J + st, at = j % S::kStages, page = r.page0 + 4 * (st + 1);
                 x = next;      // (asked for a stage ago)
-                next.load(p, codes, pairs, u, page, r.end_page, r.n, blk);
-                X::ids(table, u, page + 4, r.end_page, blk);
-                // S(j - 2), the last reader of the K tiles
-                if (j > 1) ok = rows_wait(bar(ROWS_SFULL + e), ((j - 2) >> 1) & 1, abort_p);
+                next.load(p, a.pool, codes, pairs, u, page, r.end_page, r.n, blk);
+                blk = X::id(table, u, page + 4, r.end_page);
+                if (j >= S::kStages) ok = rows_wait(bar(ROWS_FREE + at), (j / S::kStages - 1) & 1, abort_p);
                 if (!__all_sync(0xffffffffu, ok)) break;
-                x.unpack_k(sm, e, j & 3, u);
+                if (X::has_k(u)) x.unpack_k(sm, at, j & 3, u);
+                if (X::has_v(u)) x.unpack_v(sm, at, j & 3, u);
                 tc::fence_async_smem();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar(ROWS_KFULL + e));
-            }
-        } else {
-            // ------------------------------------------------------------ V
-            const int u = tid - 384;
-            const int *table = p.block_tables + (size_t)r.b * p.max_blocks;
-            const unsigned char *codes = X::at_codes(a.pool.v, u, r.hk), *pairs = X::at_pairs(a.pool.vsz, u, r.hk);
-            int blk[X::N];
-            X x, next;
-            X::ids(table, u, r.page0, r.end_page, blk);
-            next.load(p, codes, pairs, u, r.page0, r.end_page, r.n, blk);
-            X::ids(table, u, r.page0 + 4, r.end_page, blk);
-#pragma unroll 1
-            for (int st = 0; st < r.n_st; st++) {
-                const int j = J + st, e = j & 1, page = r.page0 + 4 * (st + 1);
-                x = next;      // (asked for a stage ago)
-                next.load(p, codes, pairs, u, page, r.end_page, r.n, blk);
-                X::ids(table, u, page + 4, r.end_page, blk);
-                // PV(j - 2), the last reader of the V tile
-                if (j > 1) ok = rows_wait(bar(ROWS_PVDONE + e), ((j - 2) >> 1) & 1, abort_p);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                x.unpack_v(sm, e, j & 3, u);
-                tc::fence_async_smem();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(bar(ROWS_VFULL + e));
+                if (lane == 0) tc::mbar_arrive(bar(ROWS_FULL + at));
             }
         }
         __syncwarp();
