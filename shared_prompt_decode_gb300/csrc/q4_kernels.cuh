@@ -1009,16 +1009,16 @@ __device__ __forceinline__ void wide_q(const Params &p, int lane, const Share &s
                          "r"(__byte_perm(x.x, x.z, 0x7632)), "r"(__byte_perm(x.y, x.w, 0x7632))
                          : "memory");
         }
-        // row k of the operand: sums of groups k, then their remainders
+        // row k of the operand: sums of groups k 2^-7 of themselves, then their
+        // remainders as they are (2^-7 of them would fall below fp16 where q is small)
         __half v16[2 * NG];
 #pragma unroll
         for (int gi = 0; gi < NG; gi++) {
             float f = sum[gi];
             f += __shfl_xor_sync(0xffffffffu, f, 1);
             f += __shfl_xor_sync(0xffffffffu, f, 2);
-            f *= kQsScale;
-            v16[gi] = __float2half_rn(f);
-            v16[NG + gi] = __float2half_rn(f - __half2float(v16[gi]));
+            v16[gi] = __float2half_rn(f * kQsScale);
+            v16[NG + gi] = __float2half_rn(f - __half2float(v16[gi]) * (1.f / kQsScale));
         }
         unsigned w = 0;
 #pragma unroll
@@ -1043,7 +1043,8 @@ __device__ __forceinline__ void wide_page(unsigned st, const Lane<D, GROUP> &ln,
     const __half2 zero = __floats2half2_rn(0.f, 0.f);
     float sc[NT][4];
     {
-        // z sum(q): rows keys, columns of the operand groups (twice: sums and remainders)
+        // z sum(q): rows keys, columns of the operand groups (z for the sums, 2^-7 z for their remainders)
+        const __half2 by = __floats2half2_rn(2 * t < NG ? 1.f : kQsScale, 2 * t + 1 < NG ? 1.f : kQsScale);
         __half2 h[2][NG];
         load_pairs<NG>(st + ln.sz, h[0]);
         load_pairs<NG>(st + ln.sz + 8 * NG * 4, h[1]);
@@ -1052,6 +1053,7 @@ __device__ __forceinline__ void wide_page(unsigned st, const Lane<D, GROUP> &ln,
         for (int r = 0; r < 2; r++) {
             __half2 z = NG == 1 ? __highs2half2(h[r][0], h[r][0]) : __highs2half2(h[r][0], h[r][NG > 1 ? 1 : 0]);
             if (NG == 4 && (t & 1)) z = __highs2half2(h[r][NG > 2 ? 2 : 0], h[r][NG > 2 ? 3 : 0]);
+            z = __hmul2(z, by);
             a[r] = *reinterpret_cast<const unsigned *>(&z);
         }
 #pragma unroll
@@ -1655,8 +1657,8 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
 // exact in fp16, and so is S but for its fp32 sums:
 //     S = Q (c s')^T + Q (c s")^T + sum(q) z^T      (M 128, N 64, K 2 D + 16)
 //     O += P V                                      (V = fma(c, s, z): one fp16 rounding, as P has)
-// sum(q) of a group is two halves and 2^-7 of itself, z 2^7 of itself.  P (fp16)
-// takes the place of its S in TMEM.
+// sum(q) of a group is two halves, the first 2^-7 of itself against 2^7 z, the
+// second what that leaves.  P (fp16) takes the place of its S in TMEM.
 // What fp16 does not hold is kept out of the tiles: a key whose K or V would
 // leave its range is stored 2^-11 or 2^-5 of itself, with a bit for the softmax,
 // and a V pair that is no number as zeros, with a bit of its group that makes
@@ -1719,10 +1721,12 @@ __device__ __forceinline__ uint64_t pinned(uint64_t d)
     return r;
 }
 
-// Pages of a split: about three items an SM.
+// Pages of a split: about two items an SM (an item costs 5 us apart from its
+// stages: its first loads, its output; with three or four 8 and 15 us more for
+// 600 rows over 3700 keys, 40 heads).
 __device__ __forceinline__ int split_pages(long long work, int grid, int least)
 {
-    return ((int)max((long long)least, min(256ll, (work + 3 * grid - 1) / (3 * grid))) + 3) / 4 * 4;      // whole stages
+    return ((int)max((long long)least, min(256ll, (work + 2 * grid - 1) / (2 * grid))) + 3) / 4 * 4;      // whole stages
 }
 __device__ __forceinline__ int rows_tiles(int cols) { return (cols + kRowsTile - 1) / kRowsTile; }
 
@@ -1995,9 +1999,9 @@ struct Pieces {
         }
         if (ch * 32 % GROUP == 0) {
             const int gi = ch * 32 / GROUP;
-            const __half z = __hmul(__ushort_as_half((unsigned short)(ksz >> 16)), __float2half_rn(128.f));
+            const __half z = __ushort_as_half((unsigned short)(ksz >> 16));
             __half *terms = reinterpret_cast<__half *>(sm.kz[at] + kk / 8 * 256 + kk % 8 * 16);
-            terms[gi] = z;
+            terms[gi] = __hmul(z, __float2half_rn(1.f / kQsScale));
             terms[NG + gi] = z;      // (at most eight terms: the first 16 bytes)
         }
     }
@@ -2057,6 +2061,13 @@ __device__ __forceinline__ RowsItem rows_item(const Params &p, const RowItems &s
     return r;
 }
 
+// Partial row of a column.
+__device__ __forceinline__ size_t rows_slot(const Args &a, const RowItems &s, const RowsItem &r, int v)
+{
+    const int i = v / a.p.G;
+    return (size_t)a.rows0 + ((size_t)r.part * a.p.max_q_total + s.qo[r.b] + i) * a.p.H + r.hk * a.p.G + v - i * a.p.G;
+}
+
 template <int D, int GROUP>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ Args a)
 {
@@ -2086,7 +2097,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     }
     if (tid == 0) {
         sm.abort = 0;
-        tc::mbar_init(bar(ROWS_QFULL), 4);
+        tc::mbar_init(bar(ROWS_QFULL), 8);
         tc::mbar_init(bar(ROWS_FIN), 2);
         for (int i = 0; i < S::kStages; i++) {
             tc::mbar_init(bar(ROWS_FULL + i), 8);
@@ -2100,7 +2111,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
         sm.r = rows_item(p, sm.s, blockIdx.x, split);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
-    for (int i = tid; i < (int)sizeof(sm.kz) / 4; i += kRowsThreads) reinterpret_cast<unsigned *>(sm.kz)[i] = 0u;      // terms that no group has
+    // terms that no group has
+    for (int i = tid; i < (int)sizeof(sm.kz) / 4; i += kRowsThreads) reinterpret_cast<unsigned *>(sm.kz)[i] = 0u;
+    for (int i = tid; i < (int)sizeof(sm.qz) / 4; i += kRowsThreads) reinterpret_cast<unsigned *>(sm.qz)[i] = 0u;
     tc::fence_async_smem();
     tc::tc_fence_before();
     __syncthreads();
@@ -2117,60 +2130,42 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             const int e = warp >> 2, row = tid & 127;
             const bool have = r.v0 + row <= r.vlast;
             const unsigned lane_off = (unsigned)((warp & 3) * 32) << 16;
-            int end = 0;           // keys that the row sees, of the range
+            // keys that the row sees, of the range (rows that are none hide
+            // nothing: what they come to is not written)
+            int end = r.end_page * kBlock;
+            if (have) end = min(end, keys_seen(r.n, r.ql, (r.v0 + row) / p.G));
             if (r.n_st > 0) {
-                const int v = have ? r.v0 + row : 0, i = v / p.G;
-                end = r.end_page * kBlock;      // (rows that are none hide nothing: what they come to is not written)
-                if (have) end = min(end, keys_seen(r.n, r.ql, i));
-                if (e == 0) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + (((size_t)r.b * p.Lq + i) * p.H + r.hk * p.G + v - i * p.G) * D);
-                    float sum[NG];
+                // Q: a warp has kR rows at a time, 16 bytes a lane
+                constexpr int kL = D / 8, kR = 32 / kL, kT = kRowsTile / (8 * kR);
+                const int c = lane % kL;
+                uint4 x[kT];
 #pragma unroll
-                    for (int gi = 0; gi < NG; gi++) sum[gi] = 0.f;
-                    unsigned to;
-                    asm volatile("add.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(sm.q)), "r"(tc::sw_off(row, 0)));
-#pragma unroll 1
-                    for (int c0 = 0; c0 < D / 8; c0 += 4) {      // 32 dimensions, of one group
-                        float f = 0.f;
-#pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            const uint4 x = have ? __ldg(src + c0 + c) : make_uint4(0u, 0u, 0u, 0u);
-                            const unsigned w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                const float2 y = X::pair(w[k]);
-                                f += y.x + y.y;
-                            }
-                            sts128((to ^ (((c0 & 4) + c) << 4)) + (c0 >> 3) * S::kQHalf, __byte_perm(x.x, x.z, 0x5410),
-                                   __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
-                        }
-#pragma unroll
-                        for (int gi = 0; gi < NG; gi++)
-                            if (gi == 8 * c0 / GROUP) sum[gi] += f;
-                    }
-                    // the groups' sums, then their remainders
-                    __half t[8];
-#pragma unroll
-                    for (int gi = 0; gi < 8; gi++) t[gi] = __ushort_as_half(0);
-#pragma unroll
-                    for (int gi = 0; gi < NG; gi++) {
-                        const float f = sum[gi] * kQsScale;
-                        t[gi] = __float2half_rn(f);
-                        t[NG + gi] = __float2half_rn(f - __half2float(t[gi]));
-                    }
-                    unsigned w[4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const __half2 x = __halves2half2(t[2 * k], t[2 * k + 1]);
-                        w[k] = *reinterpret_cast<const unsigned *>(&x);
-                    }
-                    const unsigned terms = smem_u32(sm.qz) + row / 8 * 256 + row % 8 * 16;
-                    sts128(terms, w[0], w[1], w[2], w[3]);
-                    sts128(terms + 128, 0u, 0u, 0u, 0u);
-                    tc::fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(bar(ROWS_QFULL));
+                for (int k = 0; k < kT; k++) {
+                    const int v = r.v0 + (warp * kT + k) * kR + lane / kL, i = v / p.G;
+                    x[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (v <= r.vlast)
+                        x[k] = __ldg(reinterpret_cast<const uint4 *>(p.q + (((size_t)r.b * p.Lq + i) * p.H + r.hk * p.G + v - i * p.G) * D) + c);
                 }
+#pragma unroll
+                for (int k = 0; k < kT; k++) {
+                    const int at = (warp * kT + k) * kR + lane / kL;
+                    sts128(smem_u32(sm.q) + (c >> 3) * S::kQHalf + tc::sw_off(at, c & 7), __byte_perm(x[k].x, x[k].z, 0x5410),
+                           __byte_perm(x[k].x, x[k].z, 0x7632), __byte_perm(x[k].y, x[k].w, 0x5410), __byte_perm(x[k].y, x[k].w, 0x7632));
+                    // the groups' sums, then their remainders
+                    const float2 y0 = X::pair(x[k].x), y1 = X::pair(x[k].y), y2 = X::pair(x[k].z), y3 = X::pair(x[k].w);
+                    float f = ((y0.x + y0.y) + (y1.x + y1.y)) + ((y2.x + y2.y) + (y3.x + y3.y));
+#pragma unroll
+                    for (int off = 1; off < GROUP / 8; off <<= 1) f += __shfl_xor_sync(0xffffffffu, f, off);
+                    if (c % (GROUP / 8) == 0) {
+                        const __half hi = __float2half_rn(f * kQsScale);
+                        __half *terms = reinterpret_cast<__half *>(sm.qz + at / 8 * 256 + at % 8 * 16) + c / (GROUP / 8);
+                        terms[0] = hi;
+                        terms[NG] = __float2half_rn(f - __half2float(hi) * (1.f / kQsScale));
+                    }
+                }
+                tc::fence_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(bar(ROWS_QFULL));
             }
             auto issue_s = [&](int j) {      // S = Q K^T, by one thread
                 const int at = j % S::kStages;
@@ -2299,7 +2294,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             const int first = J & 1;      // (the half that has the item's first stage)
             if (r.n_st > 0) ok = ok && rows_wait(bar(ROWS_PVDONE + ((J + r.n_st - 1) & 1)), ((J + r.n_st - 1) >> 1) & 1, abort_p);
             if (r.n_st > 1) ok = ok && rows_wait(bar(ROWS_PVDONE + ((J + r.n_st) & 1)), ((J + r.n_st - 2) >> 1) & 1, abort_p);
-            if (__all_sync(0xffffffffu, ok)) {
+            if (!__all_sync(0xffffffffu, ok)) sm.abort = 1;      // (set, or about to be: all eight warps take the same way)
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+            if (!*abort_p) {
                 tc::tc_fence_after();
                 const float2 x0 = sm.ml[first][row], x1 = sm.ml[first ^ 1][row];
                 const float M = fmaxf(x0.x, x1.x), mu = M == kNegInf ? 0.f : M;
@@ -2308,9 +2305,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 f0 *= inv;
                 f1 *= inv;
                 nan = sm.nan[0][row] | sm.nan[1][row];
-                const int v = r.v0 + row, i = v / p.G;
-                const size_t pr = (size_t)a.rows0 + ((size_t)r.part * p.max_q_total + sm.s.qo[r.b] + i) * p.H + r.hk * p.G + v - i * p.G;
-                float *po = p.part_o + pr * D;
+                // rows through the K tiles (every product has been taken), so that a
+                // warp writes whole rows
+                constexpr int kRow = D * 4 + 16;
+                static_assert(kRowsTile * kRow <= (int)sizeof(sm.k), "room for the output");
+                const unsigned to = smem_u32(sm.k) + row * kRow;
                 const unsigned t0 = tmem + kRowsColO + 128 * first + lane_off, t1 = tmem + kRowsColO + 128 * (first ^ 1) + lane_off;
 #pragma unroll 1
                 for (int c = e * (D / 2); c < (e + 1) * (D / 2); c += 32) {
@@ -2334,14 +2333,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 #pragma unroll
                         for (int k = 0; k < 32; k++) y[k] = __int_as_float(0x7fffffff);
                     }
-                    if (!have) continue;
+                    const unsigned *z = reinterpret_cast<const unsigned *>(y);
 #pragma unroll
                     for (int k = 0; k < 32; k += 8) {
-                        __stcg(reinterpret_cast<float4 *>(po + c + k), make_float4(y[k], y[k + 2], y[k + 4], y[k + 6]));
-                        __stcg(reinterpret_cast<float4 *>(po + c + k + 4), make_float4(y[k + 1], y[k + 3], y[k + 5], y[k + 7]));
+                        sts128(to + 4 * (c + k), z[k], z[k + 2], z[k + 4], z[k + 6]);
+                        sts128(to + 4 * (c + k) + 16, z[k + 1], z[k + 3], z[k + 5], z[k + 7]);
                     }
                 }
-                if (have && e == 0) __stcg(p.part_lse + pr, L == 0.f ? kNegInf : fmaf(M, p.scale_log2, lg2(L)));
+                if (have && e == 0) __stcg(p.part_lse + rows_slot(a, sm.s, r, r.v0 + row), L == 0.f ? kNegInf : fmaf(M, p.scale_log2, lg2(L)));
+                asm volatile("bar.sync 1, 256;\n" ::: "memory");
+                constexpr int kL = D / 4, kR = 32 / kL;      // lanes of a row, rows at a time
+#pragma unroll 4
+                for (int k = warp * kR + lane / kL; k < kRowsTile && r.v0 + k <= r.vlast; k += 8 * kR) {
+                    const uint4 x = lds128(smem_u32(sm.k) + k * kRow + lane % kL * 16);
+                    __stcg(reinterpret_cast<uint4 *>(p.part_o + rows_slot(a, sm.s, r, r.v0 + k) * D) + lane % kL, x);
+                }
             }
         } else {
             // ------------------------------------------------------------ unpack

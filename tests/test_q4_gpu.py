@@ -329,6 +329,50 @@ def test_prompt_chunks_over_long_contexts():
     check(c, run(c, "ctx"), "ctx")
 
 
+@pytest.mark.parametrize("D,group", [(128, 128), (128, 32), (64, 64), (64, 32)])
+@pytest.mark.parametrize("what", ["s", "z"])
+@pytest.mark.parametrize("rows", [1, 5, 12, 40])
+def test_large_keys(D, group, what, rows):
+    """Keys of one group that are 2^10 times the others, against queries 2^-10 of the usual: their products with a scale
+    leave fp16's range as the tiles would hold them.  Two neighbouring keys of a page, and a page."""
+    c = Case([130, 90], [rows, 1], 4, 2, D, group, 30, seed=30)
+    c.q = (c.q.astype(np.float32) * 2.0 ** -10).astype(np.float16)
+    for blk, t in ((c.table[0, 2], slice(5, 7)), (c.table[0, 5], slice(0, 16)), (c.table[1, 1], slice(15, 16))):
+        x = c.sz["k"][blk, :, t, -1, 0 if what == "s" else 1]
+        c.sz["k"][blk, :, t, -1, 0 if what == "s" else 1] = x.astype(np.float32) * 2.0 ** 10
+    check(c, run(c))
+
+
+@pytest.mark.parametrize("D,group", [(128, 128), (128, 64), (64, 32)])
+def test_prompt_chunks_over_values_behind_fp16(D, group):
+    """Values s * 15 + z of up to 95,000, of some keys and of one of their groups: fp32 results."""
+    c = Case([150, 90], [48, 1], 2, 2, D, group, 0, seed=31)
+    for t in (3, 64, 65, 149):
+        c.sz["v"][c.table[0, t // 16], :, t % 16, 0] = [6000.0, 5000.0]
+        c.sz["v"][c.table[0, t // 16], :, t % 16, -1, 1] = -60000.0
+    check(c, run(c, "ctx"), "ctx")
+
+
+@pytest.mark.parametrize("D,group", [(128, 128), (128, 32), (64, 32)])
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_one_group_of_a_seen_value_is_no_number(D, group, bad):
+    """The group's dimensions are NaN in the rows that see the key; its other dimensions, and the rows before, are what
+    they were."""
+    c = Case([100], [40], 2, 2, D, group, 20, seed=32)
+    t = 80      # seen by rows 20 and up
+    clean = c.reference()
+    at = D // group - 1
+    c.sz["v"][c.table[0, t // 16], 1, t % 16, at, 1] = bad
+    out, lse, flags = run(c)
+    assert flags == 0
+    hit = np.zeros(out.shape, bool)
+    hit[0, 20:, 1, at * group:] = True
+    assert np.isnan(out[hit]).all()
+    keep = ~hit
+    within(out[keep], clean[0][keep], clean[2][keep], "out")
+    within(lse, clean[1], clean[3], "lse")
+
+
 def test_many_requests():
     r = np.random.default_rng(8)
     c = Case(list(r.integers(0, 60, 512)), [1] * 512, 2, 1, 64, 32, 40, seed=9)
