@@ -1655,7 +1655,7 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
 //              swizzle), three stages of them.
 // With c the codes and s = s' + s" a scale cut after 7 bits, c s' and c s" are
 // exact in fp16, and so is S but for its fp32 sums:
-//     S = Q (c s')^T + Q (c s")^T + sum(q) z^T      (M 128, N 64, K 2 D + 16)
+//     S = Q (c s')^T + sum(q) z^T, and Q (c s")^T   (M 128, N 2 x 64, K D and 16; the softmax adds them)
 //     O += P V                                      (V = fma(c, s, z): one fp16 rounding, as P has)
 // sum(q) of a group is two halves, the first 2^-7 of itself against 2^7 z, the
 // second what that leaves.  P (fp16) takes the place of its S in TMEM.
@@ -1685,7 +1685,7 @@ struct RowsSmem {
     static constexpr int kQHalf = kRowsTile * 128, kKHalf = kRowsKeys * 128;
     unsigned char q[KH * kQHalf];
     static constexpr int kStages = 3;
-    unsigned char k[kStages][2][KH * kKHalf];      // c s', c s"
+    unsigned char k[kStages][KH][2 * kKHalf];      // 64 keys c s', 64 keys c s"
     unsigned char v[kStages][KH * kKHalf];
     unsigned char qz[kRowsTile * 32];        // [16][2][8] pieces of 16 bytes: row, half of the 16 terms
     unsigned char kz[kStages][kRowsKeys * 32];
@@ -1704,7 +1704,7 @@ constexpr size_t kRowsSmem = sizeof(RowsSmem<D, GROUP>) + 1024;      // (from a 
 // full, free: of a stage's tiles; the others of the even and the odd stages
 enum { ROWS_QFULL, ROWS_FIN, ROWS_SFULL, ROWS_PREADY = ROWS_SFULL + 2, ROWS_PVDONE = ROWS_PREADY + 2, ROWS_FULL = ROWS_PVDONE + 2,
        ROWS_FREE = ROWS_FULL + 3 };
-constexpr unsigned kRowsTmem = 512, kRowsColS = 0, kRowsColO = 128;      // S (or P) of stage i: 64 (i & 1); O: 128 (i & 1)
+constexpr unsigned kRowsTmem = 512, kRowsColS = 0, kRowsColO = 256;      // S (its two parts; or P) of stage i: 128 (i & 1); O: 128 (i & 1)
 
 // descriptor of 8 x 16-byte pieces without swizzle: the row's next 16 bytes
 // 128 bytes on, the next eight rows 256
@@ -1826,18 +1826,20 @@ __device__ __forceinline__ bool rows_wait(unsigned bar, unsigned parity, volatil
 }
 // All ones in the bytes of x that have bit `b`.
 __device__ __forceinline__ unsigned rows_bytes(unsigned x, unsigned b) { return (x & 0x01010101u * b) / b * 255u; }
-// Scores in TMEM: the keys of `big` times 2048, those from `seen` on hidden.
+// Scores in TMEM, two parts: the keys of `big` times 2048, those from `seen` on
+// hidden.
 __device__ __noinline__ void rows_fix_scores(unsigned tS, unsigned long long big, int seen)
 {
 #pragma unroll 1
-    for (int c = 0; c < 64; c += 32) {
+    for (int c = 0; c < 128; c += 32) {
+        const int key = c & 63;
         unsigned x[32];
         tc::tmem_ld32(tS + c, x);
         tc::tmem_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; k++) {
-            if (big >> c >> k & 1) x[k] = __float_as_uint(__uint_as_float(x[k]) * 2048.f);
-            if (c + k >= seen) x[k] = __float_as_uint(kNegInf);
+            if (big >> key >> k & 1) x[k] = __float_as_uint(__uint_as_float(x[k]) * 2048.f);
+            if (key + k >= seen) x[k] = c < 64 ? __float_as_uint(kNegInf) : 0u;
         }
         tc::tmem_st32(tS + c, x);
     }
@@ -1941,11 +1943,12 @@ struct Pieces {
         }
     }
     // Its first store into a tile at `tile`.
+    template <int HALF>      // bytes of a tile of 64 dimensions
     static __device__ __forceinline__ unsigned first(unsigned tile, int u)
     {
         const int ch = piece(u);
         unsigned x;      // (not kept through the loop in 24 addresses)
-        asm volatile("add.u32 %0, %1, %2;" : "=r"(x) : "r"(tile), "r"((ch >> 1) * S::kKHalf + tc::sw_off(key(u), 4 * (ch & 1))));
+        asm volatile("add.u32 %0, %1, %2;" : "=r"(x) : "r"(tile), "r"((ch >> 1) * HALF + tc::sw_off(key(u), 4 * (ch & 1))));
         return x;
     }
     static __device__ __forceinline__ void put(unsigned at, int j, const __half2 (&x)[4])
@@ -1971,7 +1974,7 @@ struct Pieces {
     __device__ __forceinline__ void unpack_k(S &sm, int at, int slot, int u)
     {
         const int lane = u & 31, ch = piece(u), kk = key(u);
-        const unsigned to = first(smem_u32(sm.k[at][0]), u);
+        const unsigned to = first<2 * S::kKHalf>(smem_u32(sm.k[at][0]), u);
         const float2 f = pair(ksz);
         const unsigned any = __ballot_sync(0xffffffffu, fabsf(f.x) >= 60.f || fabsf(f.y) >= 511.f);
         unsigned char bits = 0;
@@ -1995,7 +1998,7 @@ struct Pieces {
                 l[i] = __hfma2(x[i], sl, i & 1 ? sl1 : sl0);
             }
             put(to, j, h);
-            put(to + S::KH * S::kKHalf, j, l);
+            put(to + S::kKHalf, j, l);
         }
         if (ch * 32 % GROUP == 0) {
             const int gi = ch * 32 / GROUP;
@@ -2008,7 +2011,7 @@ struct Pieces {
     __device__ __forceinline__ void unpack_v(S &sm, int at, int slot, int u)
     {
         const int lane = u & 31, ch = piece(u), byte = key(u) / 8 + lane;
-        const unsigned to = first(smem_u32(sm.v[at]), u);
+        const unsigned to = first<S::kKHalf>(smem_u32(sm.v[at]), u);
         const float2 f = pair(vsz);
         const bool odd = !(fmaf(15.f, fabsf(f.x), fabsf(f.y)) < 65504.f);
         unsigned char bits = 0;
@@ -2074,7 +2077,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     using S = RowsSmem<D, GROUP>;
     using X = Pieces<D, GROUP>;
     constexpr int NG = S::NG, KH = S::KH;
-    constexpr uint32_t id_s = tc::idesc_f16(kRowsTile, kRowsKeys), id_o = tc::idesc_f16(kRowsTile, D, true);
+    constexpr uint32_t id_s = tc::idesc_f16(kRowsTile, 2 * kRowsKeys), id_z = tc::idesc_f16(kRowsTile, kRowsKeys), id_o = tc::idesc_f16(kRowsTile, D, true);
     extern __shared__ unsigned char smem_rows[];
     S &sm = *reinterpret_cast<S *>(smem_rows + (-smem_u32(smem_rows) & 1023u));
     const Params &p = a.p;
@@ -2172,15 +2175,13 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 ok = rows_wait(bar(ROWS_FULL + at), (j / S::kStages) & 1, abort_p);
                 if (!ok) return;
                 tc::tc_fence_after();
-                const unsigned d0 = tmem + kRowsColS + 64 * e;
-                tc::umma_ss(d0, pinned(plain_desc(smem_u32(sm.qz))), pinned(plain_desc(smem_u32(sm.kz[at]))), id_s, 0);
+                const unsigned d0 = tmem + kRowsColS + 128 * e;
                 const uint64_t qd = pinned(tc::sw128_desc(smem_u32(sm.q))), kd = pinned(tc::sw128_desc(smem_u32(sm.k[at][0])));
 #pragma unroll
-                for (int kk = 0; kk < 2 * D / 16; kk++) {
-                    const int d = kk % (D / 16);
-                    tc::umma_ss(d0, qd + (((d >> 2) * S::kQHalf + (d & 3) * 32) >> 4),
-                                kd + (((kk / (D / 16)) * KH * S::kKHalf + (d >> 2) * S::kKHalf + (d & 3) * 32) >> 4), id_s, 1);
-                }
+                for (int kk = 0; kk < D / 16; kk++)
+                    tc::umma_ss(d0, qd + (((kk >> 2) * S::kQHalf + (kk & 3) * 32) >> 4),
+                                kd + (((kk >> 2) * 2 * S::kKHalf + (kk & 3) * 32) >> 4), id_s, kk > 0);
+                tc::umma_ss(d0, pinned(plain_desc(smem_u32(sm.qz))), pinned(plain_desc(smem_u32(sm.kz[at]))), id_z, 1);
                 tc::umma_commit(bar(ROWS_SFULL + e));
             };
             const int st0 = (J + e) & 1;      // its first stage of the item
@@ -2191,7 +2192,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             __syncwarp();
             float m = kNegInf, l = 0.f;
             unsigned nan = 0;
-            const unsigned tS = tmem + kRowsColS + 64 * e + lane_off, tO = tmem + kRowsColO + 128 * e + lane_off;
+            const unsigned tS = tmem + kRowsColS + 128 * e + lane_off, tO = tmem + kRowsColO + 128 * e + lane_off;
             for (int st = st0; st < r.n_st; st += 2) {
                 const int j = J + st, key0 = (r.page0 + 4 * st) * kBlock;
                 ok = ok && rows_wait(bar(ROWS_SFULL + e), (j >> 1) & 1, abort_p);
@@ -2210,13 +2211,19 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                     for (int gi = 0; gi < NG; gi++)
                         if (*reinterpret_cast<const unsigned long long *>(sm.vnan[j & 3][gi]) & mask & odd) nan |= 1u << gi;
                 }
-                unsigned y[2][32];
-                tc::tmem_ld32(tS, y[0]);
-                tc::tmem_ld32(tS + 32, y[1]);
-                tc::tmem_wait_ld();
                 float x[64];
 #pragma unroll
-                for (int k = 0; k < 64; k++) x[k] = __uint_as_float(y[k >> 5][k & 31]);
+                for (int h = 0; h < 2; h++) {      // the two parts together
+                    unsigned y[2][32];
+                    tc::tmem_ld32(tS + 32 * h, y[0]);
+                    tc::tmem_ld32(tS + 32 * h + 64, y[1]);
+                    tc::tmem_wait_ld();
+#pragma unroll
+                    for (int k = 0; k < 32; k += 2)
+                        tc::f2_unpack(tc::f2_add(tc::f2_pack(__uint_as_float(y[0][k]), __uint_as_float(y[0][k + 1])),
+                                                 tc::f2_pack(__uint_as_float(y[1][k]), __uint_as_float(y[1][k + 1]))),
+                                      x[32 * h + k], x[32 * h + k + 1]);
+                }
                 float mx[4];
 #pragma unroll
                 for (int k = 0; k < 4; k++) {
@@ -2275,7 +2282,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                             const uint64_t vd = pinned(tc::sw128_desc(smem_u32(sm.v[j % S::kStages]), S::kKHalf));
 #pragma unroll
                             for (int kk = 0; kk < kRowsKeys / 16; kk++)
-                                tc::umma_ts(tmem + kRowsColO + 128 * e, tmem + kRowsColS + 64 * e + 8 * kk, vd + kk * (2048 >> 4), id_o,
+                                tc::umma_ts(tmem + kRowsColO + 128 * e, tmem + kRowsColS + 128 * e + 8 * kk, vd + kk * (2048 >> 4), id_o,
                                             st > 1 || kk > 0);
                             tc::umma_commit(bar(ROWS_PVDONE + e));
                             tc::umma_commit(bar(ROWS_FREE + j % S::kStages));
