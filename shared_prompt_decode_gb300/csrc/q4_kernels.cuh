@@ -1671,7 +1671,7 @@ struct RowItems {
     int it[kMaxB + 1];        // items before request b
     long long sum[16];
     int sum_q[16];
-    int bad, next;
+    int bad, next[2];
 };
 // An item, in shared memory (what a role uses of it would cost registers).
 struct RowsItem {
@@ -1695,7 +1695,7 @@ struct RowsSmem {
     float2 ml[2][kRowsTile];                 // a column's reference and sum
     unsigned nan[2][kRowsTile];              // its groups of V that are no numbers
     RowItems s;
-    RowsItem r;
+    RowsItem r[2];
     unsigned tmem;
     int abort;
 };
@@ -1909,7 +1909,15 @@ struct Pieces {
         const int page = page0 + key(u) / kBlock;
         return page < end ? __ldg(table + page) : -1;
     }
-    // codes, pairs: places of the thread's key and piece in a block
+    // places of the thread's key and piece in a block
+    static __device__ __forceinline__ unsigned codes_at(int u, int hk)
+    {
+        return ((unsigned)hk * kBlock + key(u) % kBlock) * (D / 2) + 16 * piece(u);
+    }
+    static __device__ __forceinline__ unsigned pairs_at(int u, int hk)
+    {
+        return ((unsigned)hk * kBlock + key(u) % kBlock) * NG + piece(u) * 32 / GROUP;
+    }
     __device__ __forceinline__ void load(const Params &p, const Pool &pool, unsigned codes, unsigned pairs, int u, int page0, int end,
                                          int n, int blk)
     {
@@ -2111,7 +2119,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
             tc::mbar_init(bar(ROWS_PREADY + i), 4);
             tc::mbar_init(bar(ROWS_PVDONE + i), 1);
         }
-        sm.r = rows_item(p, sm.s, blockIdx.x, split);
+        sm.r[0] = rows_item(p, sm.s, blockIdx.x, split);
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     }
     // terms that no group has
@@ -2122,13 +2130,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     __syncthreads();
     tc::tc_fence_after();
     const unsigned tmem = sm.tmem;
-    const RowsItem &r = sm.r;
-    int J = 0;                 // stages before the item
-    unsigned q_items = 0;      // items with stages before it
-
-    for (int item = blockIdx.x; item < n_items;) {
-        bool ok = true;
-        if (warp < 8) {
+    // Both halves of the CTA go through the same items; J: stages before the item.
+    if (warp < 8) {
+        unsigned q_items = 0;      // items with stages before it
+        for (int item = blockIdx.x, turn = 0, J = 0; item < n_items; turn ^= 1) {
+            const RowsItem &r = sm.r[turn];
+            bool ok = true;
             // ------------------------------------------------------------ softmax, Q and the output
             const int e = warp >> 2, row = tid & 127;
             const bool have = r.v0 + row <= r.vlast;
@@ -2356,19 +2363,35 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                     __stcg(reinterpret_cast<uint4 *>(p.part_o + rows_slot(a, sm.s, r, r.v0 + k) * D) + lane % kL, x);
                 }
             }
-        } else {
-            // ------------------------------------------------------------ unpack
-            const int u = tid - 256;
+            __syncwarp();
+            J += r.n_st;      // (before the barrier: behind it r may become another item)
+            q_items += r.n_st > 0;
+            tc::tc_fence_before();
+            __syncthreads();
+            tc::tc_fence_after();
+            item = sm.s.next[turn];
+        }
+    } else {
+        // ------------------------------------------------------------ unpack
+        const int u = tid - 256;
+        X next;           // a stage on its way
+        int blk;          // the block of the one behind it
+        auto begin = [&](const RowsItem &r) {
             const int *table = p.block_tables + (size_t)r.b * p.max_blocks;
-            const unsigned row = (unsigned)r.hk * kBlock + X::key(u) % kBlock;
-            const unsigned codes = row * (D / 2) + 16 * X::piece(u), pairs = row * NG + X::piece(u) * 32 / GROUP;
-            X x, next;
-            next.load(p, a.pool, codes, pairs, u, r.page0, r.end_page, r.n, X::id(table, u, r.page0, r.end_page));
-            int blk = X::id(table, u, r.page0 + 4, r.end_page);
+            next.load(p, a.pool, X::codes_at(u, r.hk), X::pairs_at(u, r.hk), u, r.page0, r.end_page, r.n,
+                      X::id(table, u, r.page0, r.end_page));
+            blk = X::id(table, u, r.page0 + 4, r.end_page);
+        };
+        begin(sm.r[0]);
+        for (int item = blockIdx.x, turn = 0, J = 0; item < n_items; turn ^= 1) {
+            const RowsItem &r = sm.r[turn];
+            bool ok = true;
+            const int *table = p.block_tables + (size_t)r.b * p.max_blocks;
+            const unsigned codes = X::codes_at(u, r.hk), pairs = X::pairs_at(u, r.hk);
 #pragma unroll 1
             for (int st = 0; st < r.n_st; st++) {
                 const int j = J + st, at = j % S::kStages, page = r.page0 + 4 * (st + 1);
-                x = next;      // (asked for a stage ago)
+                X x = next;      // (asked for a stage ago)
                 next.load(p, a.pool, codes, pairs, u, page, r.end_page, r.n, blk);
                 blk = X::id(table, u, page + 4, r.end_page);
                 if (j >= S::kStages) ok = rows_wait(bar(ROWS_FREE + at), (j / S::kStages - 1) & 1, abort_p);
@@ -2379,20 +2402,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(bar(ROWS_FULL + at));
             }
+            // the next item, and its first stage, beside the end of this one
+            if (u == 0) {
+                const int to = *abort_p ? n_items : (int)(gridDim.x + atomicAdd(&p.ctrl[CTRL_Q4_ROWS], 1u));
+                sm.s.next[turn] = to;
+                if (to < n_items) sm.r[turn ^ 1] = rows_item(p, sm.s, to, split);
+            }
+            asm volatile("bar.sync 2, 256;\n" ::: "memory");
+            if (sm.s.next[turn] < n_items) begin(sm.r[turn ^ 1]);
+            __syncwarp();
+            J += r.n_st;      // (before the barrier: behind it r may become another item)
+            tc::tc_fence_before();
+            __syncthreads();
+            tc::tc_fence_after();
+            item = sm.s.next[turn];
         }
-        __syncwarp();
-        J += r.n_st;      // (before the barrier behind which r is another item)
-        q_items += r.n_st > 0;
-        tc::tc_fence_before();
-        __syncthreads();
-        tc::tc_fence_after();
-        if (tid == 0) {
-            const int next = (int)(gridDim.x + atomicAdd(&p.ctrl[CTRL_Q4_ROWS], 1u));
-            sm.s.next = *abort_p ? n_items : next;
-            if (next < n_items) sm.r = rows_item(p, sm.s, next, split);
-        }
-        __syncthreads();
-        item = sm.s.next;
     }
     // after a wait that gave up: the MMAs in flight, of the two threads that issue them
     if (*abort_p && lane == 0 && (warp == 0 || warp == 4)) tc::umma_commit(bar(ROWS_FIN));
