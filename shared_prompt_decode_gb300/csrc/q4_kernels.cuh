@@ -1656,9 +1656,11 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
 // With c the codes and s = s' + s" a scale cut after 7 bits, c s' and c s" are
 // exact in fp16, and so is S but for its fp32 sums:
 //     S = Q (c s')^T + sum(q) z^T, and Q (c s")^T   (M 128, N 2 x 64, K D and 16; the softmax adds them)
-//     O += P V                                      (V = fma(c, s, z): one fp16 rounding, as P has)
+//     O += P V                                      (V = fma(c, s, z), one fp16 rounding; P in two halves, which
+//                                                    have 22 bits of it: with P in one, too, the error of the
+//                                                    results would be half as large again)
 // sum(q) of a group is two halves, the first 2^-7 of itself against 2^7 z, the
-// second what that leaves.  P (fp16) takes the place of its S in TMEM.
+// second what that leaves.  P takes the place of its S in TMEM.
 // What fp16 does not hold is kept out of the tiles: a key whose K or V would
 // leave its range is stored 2^-11 or 2^-5 of itself, with a bit for the softmax,
 // and a V pair that is no number as zeros, with a bit of its group that makes
@@ -1808,11 +1810,10 @@ __device__ __forceinline__ void sts128(unsigned a, unsigned x, unsigned y, unsig
 {
     asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
-__device__ __forceinline__ void tmem_st16(unsigned taddr, const unsigned (&r)[16])
+__device__ __forceinline__ void tmem_st8(unsigned taddr, const unsigned (&r)[8])
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};\n" ::"r"(taddr),
-                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
 
@@ -1845,20 +1846,23 @@ __device__ __noinline__ void rows_fix_scores(unsigned tS, unsigned long long big
     }
     tc::tmem_wait_st();
 }
-// Weights in TMEM (fp16): the keys of `big` times 32.
+// Weights in TMEM, two halves each: the keys of `big` times 32.
 __device__ __noinline__ void rows_fix_weights(unsigned tP, unsigned long long big)
 {
-    unsigned x[32];
     tc::tmem_wait_st();
-    tc::tmem_ld32(tP, x);
-    tc::tmem_wait_ld();
+#pragma unroll 1
+    for (int c = 0; c < 64; c += 32) {
+        unsigned x[32];
+        tc::tmem_ld32(tP + c, x);
+        tc::tmem_wait_ld();
 #pragma unroll
-    for (int k = 0; k < 32; k++) {
-        const __half2 f = __floats2half2_rn(big >> (2 * k) & 1 ? 32.f : 1.f, big >> (2 * k + 1) & 1 ? 32.f : 1.f);
-        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[k]), f);
-        x[k] = *reinterpret_cast<const unsigned *>(&y);
+        for (int k = 0; k < 32; k++) {
+            const __half2 f = __floats2half2_rn(big >> (2 * k) & 1 ? 32.f : 1.f, big >> (2 * k + 1) & 1 ? 32.f : 1.f);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&x[k]), f);
+            x[k] = *reinterpret_cast<const unsigned *>(&y);
+        }
+        tc::tmem_st32(tP + c, x);
     }
-    tc::tmem_st32(tP, x);
 }
 // An O of W columns times f.
 template <int W>
@@ -2252,18 +2256,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                 const unsigned long long sc2 = tc::f2_pack(p.scale_log2, p.scale_log2), mu2 = tc::f2_pack(mu, mu);
                 unsigned long long ls[2] = {0ull, 0ull};
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
+                for (int i = 0; i < 64; i += 16) {
+                    unsigned pk[8], rest[8];
 #pragma unroll
-                    for (int k = 32 * h; k < 32 * h + 32; k += 2) {
-                        tc::f2_unpack(tc::f2_fma(tc::f2_pack(x[k], x[k + 1]), sc2, mu2), x[k], x[k + 1]);
-                        x[k] = ex2(x[k]);
-                        x[k + 1] = ex2(x[k + 1]);
-                        ls[k / 2 & 1] = tc::f2_add(ls[k / 2 & 1], tc::f2_pack(x[k], x[k + 1]));
+                    for (int k = 0; k < 16; k += 2) {
+                        float y0, y1;
+                        tc::f2_unpack(tc::f2_fma(tc::f2_pack(x[i + k], x[i + k + 1]), sc2, mu2), y0, y1);
+                        y0 = ex2(y0);
+                        y1 = ex2(y1);
+                        ls[k / 2 & 1] = tc::f2_add(ls[k / 2 & 1], tc::f2_pack(y0, y1));
+                        pk[k / 2] = pack_half2(y0, y1);
+                        const float2 y = X::pair(pk[k / 2]);
+                        rest[k / 2] = pack_half2(y0 - y.x, y1 - y.y);
                     }
-                    unsigned pk[16];
-#pragma unroll
-                    for (int k = 0; k < 16; k++) pk[k] = pack_half2(x[32 * h + 2 * k], x[32 * h + 2 * k + 1]);
-                    tmem_st16(tS + 16 * h, pk);
+                    tmem_st8(tS + i / 2, pk);
+                    tmem_st8(tS + 32 + i / 2, rest);
                 }
                 float l0, l1;
                 tc::f2_unpack(tc::f2_add(ls[0], ls[1]), l0, l1);
@@ -2288,9 +2295,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
                             tc::tc_fence_after();
                             const uint64_t vd = pinned(tc::sw128_desc(smem_u32(sm.v[j % S::kStages]), S::kKHalf));
 #pragma unroll
-                            for (int kk = 0; kk < kRowsKeys / 16; kk++)
-                                tc::umma_ts(tmem + kRowsColO + 128 * e, tmem + kRowsColS + 128 * e + 8 * kk, vd + kk * (2048 >> 4), id_o,
-                                            st > 1 || kk > 0);
+                            for (int kk = 0; kk < 2 * kRowsKeys / 16; kk++)
+                                tc::umma_ts(tmem + kRowsColO + 128 * e, tmem + kRowsColS + 128 * e + 8 * kk,
+                                            vd + kk % (kRowsKeys / 16) * (2048 >> 4), id_o, st > 1 || kk > 0);
                             tc::umma_commit(bar(ROWS_PVDONE + e));
                             tc::umma_commit(bar(ROWS_FREE + j % S::kStages));
                         }
