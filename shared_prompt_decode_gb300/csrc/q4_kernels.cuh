@@ -19,6 +19,7 @@
 //     sum w_t (c_t - 8) + sum p_t (z_t + 8 s_t),   w_t = fp16(p_t s_t),
 // whose - 8 sum w_t is one more product with the same weights (a row of
 // codes 8).  Without it the error is three times as large on normal data.
+// (Prompt chunks on the tensor cores are the exception: rows_kernel.)
 #pragma once
 
 #include <cuda_fp16.h>
@@ -42,7 +43,10 @@ struct Pool {
 // 0..15, in fp32 with IEEE divisions; s = 0 has code 0, and a group with a NaN
 // or an infinity stores s = z = NaN.  D / 32 lanes take one row of one KV
 // head, K or V: with the instructions of a row's address, group and scale
-// spread over 32 elements the kernel is [APPEND].
+// spread over 32 elements the kernel takes 38.6 us for K and V of 8192 rows of
+// 32 heads (D = 128, groups of 64; 149 MB, 22 us at the copy rate): what is
+// left is the codes' arithmetic, ten instructions an element pair.  A row of
+// 8 elements a lane took 112 us.  A decode step's 32 rows are one launch.
 //
 // The quotient's code comes from a product with 1 / s: t = (x - z) * (1 / s)
 // is off by less than 1e-5 (15 times a few roundings of 2^-24), so unless t
@@ -404,7 +408,8 @@ struct Smem4 {
 };
 
 // Shape of a CTA: warps, pages of a step (their keys share one round of the
-// softmax), steps in a warp's ring.  One CTA per SM.
+// softmax), steps in a warp's ring.  One CTA per SM.  (12 warps: 10, 14 and 16
+// were no faster at D = 128; nor were three or four pages a step.)
 constexpr size_t kMaxSmem = 227 * 1024;
 template <int D, int GROUP, int NT>
 struct Geo {
@@ -1555,7 +1560,14 @@ __device__ __forceinline__ void run_wide(const Args &a, Smem4 &sm, const Lane<D,
 
 // ----------------------------------------------------------------------------- attention: kernels
 // The context kernel: one CTA per SM, every warp on its own through chunks of
-// the line.  NT: tensor-core tiles of columns that a sequence may have; E as
+// the line.  Bound by memory on long contexts: 64 requests x 4096 keys x 32
+// heads (D = 128, groups of 128, 1.14 GB) take 197 us with the merge, 5.8 TB/s
+// of 6.7 for a copy; a call has about 12 us besides (the line, the first
+// loads, the last partials and their merge), which is what remains of short
+// ones: 16 us at the copy rate and 39 us for 32 requests of 64 to 1024 keys with
+// a prompt of 2048.  With eight query heads a KV head and groups of 64 the
+// arithmetic comes near: 86 us, 49 at the copy rate (32 requests, 1000 to 8192 keys).
+//  NT: tensor-core tiles of columns that a sequence may have; E as
 // in State.  It starts beside a grid in front of it that computes the prompt's
 // partials (whichever SMs that leaves) and ends only after it.
 template <int D, int GROUP, int NT, int E>
@@ -1572,11 +1584,12 @@ __global__ void __launch_bounds__(Geo<D, GROUP, NT>::kW * 32, 1) ctx_kernel(cons
     if (a.queue) ch.ask(p);
     build_line<G::kW>(p, s, a.rows_max);
     const long long total = s.pre[p.B], workers = (long long)gridDim.x * G::kW;
-    // pages of a chunk: one chunk a warp up to 24 pages (two where the warps
-    // do not start together), then two or three: finer ones balance better,
-    // and cost partials
-    const long long per = (total + workers - 1) / workers;
-    const int parts = per <= 24 ? 1 + a.queue : 2 + a.queue;
+    // Pages of a chunk: one chunk a warp where the warps start together (two
+    // only cost partials and starts: 32 x 32768 keys of 8 heads 69 -> 77 us, 64 x
+    // 4096 of 32 heads 197 -> 199), four where the CTAs follow a grid in front
+    // of them as its CTAs leave (prompt chunks beside twelve decode requests:
+    // 236, 204, 196, 193 and 194 us with one, two, three, four and six)
+    const int parts = a.queue ? 4 : 1;
     const int Q = (int)max((long long)a.q_min, (total + workers * parts - 1) / (workers * parts));
     const unsigned bad = (unsigned)s.bad | (s.qo[p.B] > p.max_q_total ? FLAG_Q_TOTAL : 0u);
     if (blockIdx.x == 0) {
@@ -2083,6 +2096,14 @@ __device__ __forceinline__ size_t rows_slot(const Args &a, const RowItems &s, co
     return (size_t)a.rows0 + ((size_t)r.part * a.p.max_q_total + s.qo[r.b] + i) * a.p.H + r.hk * a.p.G + v - i * a.p.G;
 }
 
+// What bounds it: 482 rows against 3300 to 4100 keys of 40 heads (D = 128, groups
+// of 32) are 24 us of products at the measured dense rate, and take 95 us of
+// the SMs.  A stage is 1.2 us: unpacking (24 stores of 16 bytes and their
+// arithmetic a thread and stage, 0.9 us), the softmax (0.5) and the products
+// (0.6) overlap, but a scheduler's instruction cache passes three kinds of code,
+// and an item has 7 us apart from its stages.  The form before it (mma.sync,
+// eight warps of 16 columns over codes in shared memory) was bound by the
+// shared-memory reads of its operands and took 215 us.
 template <int D, int GROUP>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ Args a)
 {
@@ -2479,6 +2500,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 // context's partials by their log-sum-exps, as merge_kernel of the fp16 path
 // does.  With few rows it is one memory round trip after another, so four
 // warps share a row's parts; with many rows one warp a row moves the bytes.
+// About 5 us of a decode step, 27 us for 494 rows of 40 heads.
 template <int D, int WPR, int CH>
 __global__ void __launch_bounds__(256, CH > 8 ? 2 : 3) merge_kernel(const __grid_constant__ Args a)
 {

@@ -5,14 +5,18 @@ Tolerance of the attention, per element, from the roundings that the kernels
 make: the output is rounded to fp16 (2^-11 of it, or 2^-25), the weights to
 fp16 before the product with the values: sum_j d_j w_j x_j / sum_j w_j with
 |d_j| <= 2^-11 is at most 2^-11 max |x|, x the fp16 system values or s (c - 8)
-of the 4-bit ones; weights below fp16's normal numbers are off by 2^-25 of the
+of the 4-bit ones (prompt chunks on the tensor cores round the values s c + z
+instead, by 2^-11 of them, and keep the weights); weights below fp16's normal numbers are off by 2^-25 of the
 common scale at most, which counts only through n keys.  fp32 sums add 2e-5 of
 the largest value."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
 
 import shared_prompt_decode_gb300 as relay
+from shared_prompt_decode_gb300 import build
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -21,7 +25,6 @@ GROUPS = [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128)]
 
 @pytest.fixture(scope="module", autouse=True)
 def _built():
-    from shared_prompt_decode_gb300 import build
     build.build()
     assert torch.cuda.is_available()
 
@@ -527,3 +530,29 @@ def test_serving_loop(D, group, H, Hkv):
     fill(chunk, ql)
     step(chunk)
     verify(chunk, ql, before)
+
+
+def test_wait_that_gives_up_is_reported():
+    """Prompt chunks run on a pipeline whose waits are bounded in time.  In a build whose limit is zero the first wait that
+    is not met at once gives up: the call ends, reports it, and leaves the context and the workspace usable."""
+    path = build.build(variant="wait0", defines=["RELAY_WAIT_LIMIT_NS=0ull"])
+    short = ctypes.CDLL(path).relay_ctx_attn_q4
+    full = relay.lib().relay_ctx_attn_q4
+    short.restype, short.argtypes = full.restype, full.argtypes
+    c = Case([900, 700, 350], [128, 1, 60], 4, 4, 128, 64, 0, seed=40)
+    q, pool, table, ctx, ql = torch.from_numpy(c.q).to(DEV), c.pool(), i32(c.table), i32(c.ctx), i32(c.q_lens)
+    dims = relay.make_dims(q, 0, c.num, c.max_blocks, max_q_total=sum(c.q_lens), Hkv=c.Hkv)
+    w = relay.make_workspace_q4(dims)
+    out, lse = torch.zeros(c.q.shape, device=DEV), torch.zeros(c.q.shape[:3], device=DEV)
+    seen = 0
+    for _ in range(3):
+        rc = short(ctypes.byref(dims), q.data_ptr(), ctypes.byref(pool._struct), table.data_ptr(), ctx.data_ptr(), ql.data_ptr(),
+                   out.data_ptr(), lse.data_ptr(), w.data_ptr(), w.numel(), torch.cuda.current_stream().cuda_stream)
+        assert rc == relay.OK
+        torch.cuda.synchronize()
+        seen |= relay.device_status(w)
+    assert seen == relay.FLAG_WAIT_TIMEOUT
+    out, lse = relay.relay_ctx_attn_q4(q, pool, table, ctx, ql, workspace=w, dims=dims)
+    ref, ref_lse, tol, ltol = c.reference("ctx")
+    for b, r in enumerate(c.q_lens):
+        within(out[b, :r].double().cpu().numpy(), ref[b, :r], tol[b, :r], f"out of request {b}")
