@@ -335,7 +335,6 @@ struct Args {
     long long part0;          // first partial row of the contexts
     float slack;              // kSlack in units of q . k
     long long rows0;          // first partial row of the prompt chunks: (split * max_q_total + row) * H + head
-    int rows_least;           // pages of a chunk's split, at least
     int rows_max;             // columns of a request on the line, at most
 };
 
@@ -1566,7 +1565,7 @@ __device__ __forceinline__ void run_wide(const Args &a, Smem4 &sm, const Lane<D,
 // loads, the last partials and their merge), which is what remains of short
 // ones: 16 us at the copy rate and 39 us for 32 requests of 64 to 1024 keys with
 // a prompt of 2048.  With eight query heads a KV head and groups of 64 the
-// arithmetic comes near: 86 us, 49 at the copy rate (32 requests, 1000 to 8192 keys).
+// arithmetic comes near: 86 us, 49 at the copy rate (32 requests, 1000 to 16384 keys).
 //  NT: tensor-core tiles of columns that a sequence may have; E as
 // in State.  It starts beside a grid in front of it that computes the prompt's
 // partials (whichever SMs that leaves) and ends only after it.
@@ -1685,7 +1684,7 @@ struct RowItems {
     int qo[kMaxB + 1];        // query rows before request b
     int it[kMaxB + 1];        // items before request b
     long long sum[16];
-    int sum_q[16];
+    int sum_q[16], most[16];
     int bad, next[2];
 };
 // An item, in shared memory (what a role uses of it would cost registers).
@@ -1736,21 +1735,24 @@ __device__ __forceinline__ uint64_t pinned(uint64_t d)
     return r;
 }
 
-// Pages of a split: about two items an SM (an item costs 5 us apart from its
-// stages: its first loads, its output; with three or four 8 and 15 us more for
-// 600 rows over 3700 keys, 40 heads).
-__device__ __forceinline__ int split_pages(long long work, int grid, int least)
+// Pages of a split, from the batch's pages of all items and of its longest
+// context: about two items an SM (an item costs 7 us apart from its stages; with
+// three or four 7 and 15 us more for 482 rows over 3700 keys, 40 heads), at
+// most kRowsParts of a context, whole stages.
+constexpr int kRowsParts = 8, kRowsPages = 32;
+__device__ __forceinline__ int split_pages(long long work, int most, int grid)
 {
-    return ((int)max((long long)least, min(256ll, (work + 2 * grid - 1) / (2 * grid))) + 3) / 4 * 4;      // whole stages
+    const long long even = min(256ll, (work + 2 * grid - 1) / (2 * grid));
+    return ((int)max((long long)max(kRowsPages, (most + kRowsParts - 1) / kRowsParts), even) + 3) / 4 * 4;
 }
 __device__ __forceinline__ int rows_tiles(int cols) { return (cols + kRowsTile - 1) / kRowsTile; }
 
 // The items of the batch (at least 256 threads): items prefix, and the split.
-__device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int least, int rows_max)
+__device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int rows_max)
 {
     constexpr int PER = kMaxB / 256;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int ql[PER], pages[PER], sum_q = 0, bad = 0;
+    int ql[PER], pages[PER], sum_q = 0, most = 0, bad = 0;
     long long work = 0;
     if (tid == 0) s.bad = 0;
 #pragma unroll
@@ -1764,7 +1766,10 @@ __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int leas
             else pages[k] = (n + kBlock - 1) / kBlock;
         }
         sum_q += ql[k];
-        if (ql[k] * p.G > rows_max) work += (long long)p.Hkv * rows_tiles(ql[k] * p.G) * pages[k];
+        if (ql[k] * p.G > rows_max) {
+            work += (long long)p.Hkv * rows_tiles(ql[k] * p.G) * pages[k];
+            most = max(most, pages[k]);
+        }
     }
     int iq = sum_q;
     long long iw = work;
@@ -1774,9 +1779,11 @@ __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int leas
         const long long tw = __shfl_up_sync(0xffffffffu, iw, off);
         if (lane >= off) { iq += t; iw += tw; }
     }
+    most = __reduce_max_sync(0xffffffffu, most);
     if (lane == 31) {
         s.sum_q[warp] = iq;
         s.sum[warp] = iw;
+        s.most[warp] = most;
     }
     __syncthreads();
     if (bad) s.bad = 1;
@@ -1785,8 +1792,9 @@ __device__ __forceinline__ int build_rows(const Params &p, RowItems &s, int leas
     for (int j = 0; j < 8; j++) {
         if (j < warp) bq += s.sum_q[j];
         total += s.sum[j];
+        most = max(most, s.most[j]);
     }
-    const int split = split_pages(total, gridDim.x, least);
+    const int split = split_pages(total, most, gridDim.x);
     int n_it[PER], sum_i = 0;
 #pragma unroll
     for (int k = 0; k < PER; k++) {
@@ -1833,10 +1841,16 @@ __device__ __forceinline__ void tmem_st8(unsigned taddr, const unsigned (&r)[8])
 // What is rare stays out of the loops: four roles' code passes through a
 // scheduler's instruction cache, and what it does not hold runs at a tenth of
 // the rate.
-__device__ __noinline__ bool rows_wait_long(unsigned bar, unsigned parity, volatile int *abort) { return tc::mbar_wait(bar, parity, abort); }
+__device__ __noinline__ bool rows_wait_long(unsigned bar, unsigned parity, volatile int *abort)
+{
+    if (tc::kWaitNs > 0) return tc::mbar_wait(bar, parity, abort);
+    *abort = 1;
+    return false;
+}
+// (a limit of 0: a wait that is not met at once gives up)
 __device__ __forceinline__ bool rows_wait(unsigned bar, unsigned parity, volatile int *abort)
 {
-    return tc::mbar_try(bar, parity) || rows_wait_long(bar, parity, abort);
+    return (tc::kWaitNs > 0 ? tc::mbar_try(bar, parity) : tc::mbar_test(bar, parity)) || rows_wait_long(bar, parity, abort);
 }
 // All ones in the bytes of x that have bit `b`.
 __device__ __forceinline__ unsigned rows_bytes(unsigned x, unsigned b) { return (x & 0x01010101u * b) / b * 255u; }
@@ -2098,8 +2112,8 @@ __device__ __forceinline__ size_t rows_slot(const Args &a, const RowItems &s, co
 
 // What bounds it: 482 rows against 3300 to 4100 keys of 40 heads (D = 128, groups
 // of 32) are 24 us of products at the measured dense rate, and take 95 us of
-// the SMs.  A stage is 1.2 us: unpacking (24 stores of 16 bytes and their
-// arithmetic a thread and stage, 0.9 us), the softmax (0.5) and the products
+// the SMs.  A stage is 1.2 us: unpacking (12 stores of 16 bytes and their
+// arithmetic a thread, 0.9 us), the softmax (0.6) and the products
 // (0.6) overlap, but a scheduler's instruction cache passes three kinds of code,
 // and an item has 7 us apart from its stages.  The form before it (mma.sync,
 // eight warps of 16 columns over codes in shared memory) was bound by the
@@ -2118,7 +2132,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     auto bar = [&](int i) { return smem_u32(sm.bar) + 8u * (unsigned)i; };
     volatile int *abort_p = &sm.abort;
-    const int split = build_rows(p, sm.s, a.rows_least, a.rows_max);
+    const int split = build_rows(p, sm.s, a.rows_max);
     if (blockIdx.x == 0 && tid == 0) p.sched[2] = split;
     const bool run = !sm.s.bad && sm.s.qo[p.B] <= p.max_q_total;
     const int n_items = run ? sm.s.it[p.B] : 0;

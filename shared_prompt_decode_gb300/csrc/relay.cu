@@ -1080,7 +1080,7 @@ relay_status_t check_q4(const relay_dims_t *d, const relay_q4_cache_t *c)
 // plan, then room for every chunk and every sequence of the line (q4::Args).
 struct PlanQ4 {
     Plan sys;
-    int nc = 0, q_min = 0, rows_least = 0;
+    int nc = 0, q_min = 0;
     int rows_max = INT_MAX;               // columns of a request on the line, at most
     long long line_cols = 0;              // ... that this shape has
     size_t rows0 = 0;
@@ -1088,8 +1088,6 @@ struct PlanQ4 {
 };
 constexpr int kQ4MinPages = 4;        // pages of a chunk, at least (a partial row is 1/16 of their bytes)
 constexpr int kQ4MaxWarps = 16;       // warps of a context CTA, at most
-constexpr int kQ4RowsParts = 8;       // splits of a prompt chunk's context, at most
-constexpr int kQ4RowsPages = 32;      // pages of a split, at least
 
 PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
 {
@@ -1121,8 +1119,8 @@ PlanQ4 make_plan_q4(const relay_dims_t *d, int mode, int sms)
     const double line = (double)seqs * d->max_blocks_per_seq;
     const long long chunks = (long long)std::min(line / kQ4MinPages + 1, 4.0 * kQ4MaxWarps * sms + 1);
     pl.rows0 = pl.sys.dec_base + (size_t)(chunks + seqs) * pl.nc;
-    pl.rows_least = std::max(kQ4RowsPages, (d->max_blocks_per_seq + kQ4RowsParts - 1) / kQ4RowsParts);
-    const size_t parts = cols > pl.rows_max ? (d->max_blocks_per_seq + pl.rows_least - 1) / pl.rows_least : 0;
+    const size_t parts =      // of a prompt chunk's context
+        cols > pl.rows_max ? std::min(q4::kRowsParts, (d->max_blocks_per_seq + q4::kRowsPages - 1) / q4::kRowsPages) : 0;
     const size_t rows = pl.rows0 + parts * pl.sys.Mtot * d->H;
     pl.off_part_o = pl.sys.off_sched + (q4::sched_bytes(d->B) + 255) / 256 * 256;
     pl.off_part_lse = pl.off_part_o + (rows * d->D * sizeof(float) + 255) / 256 * 256;
@@ -1167,7 +1165,6 @@ relay_status_t launch_q4(const relay_dims_t *d, int mode, Params p, const relay_
     a.q_min = pl.q_min;
     a.part0 = (long long)pl.sys.dec_base;
     a.rows0 = (long long)pl.rows0;
-    a.rows_least = pl.rows_least;
     a.rows_max = pl.rows_max;
     a.slack = q4::kSlack / p.scale_log2;
 

@@ -324,6 +324,14 @@ def test_long_contexts_of_one_request():
     check(c, run(c))
 
 
+def test_prompt_chunks_with_room_for_more():
+    """Contexts far shorter than the block tables allow: their splits follow the contexts."""
+    c = Case([1500, 20, 900], [130, 1, 40], 2, 1, 128, 128, 10, seed=7)
+    c.max_blocks = 3000
+    c.table = np.pad(c.table, ((0, 0), (0, 3000 - c.table.shape[1])), constant_values=-1)
+    check(c, run(c))
+
+
 def test_prompt_chunks_over_long_contexts():
     """Prompt chunks whose contexts go to several splits, of a length that is no multiple of the kernel's stage."""
     c = Case([4400, 700, 2100], [40, 1, 140], 2, 2, 128, 128, 20, seed=5)
