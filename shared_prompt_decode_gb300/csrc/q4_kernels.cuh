@@ -1843,14 +1843,18 @@ __device__ __forceinline__ void tmem_st8(unsigned taddr, const unsigned (&r)[8])
 // the rate.
 __device__ __noinline__ bool rows_wait_long(unsigned bar, unsigned parity, volatile int *abort)
 {
-    if (tc::kWaitNs > 0) return tc::mbar_wait(bar, parity, abort);
-    *abort = 1;
-    return false;
+    if constexpr (tc::kWaitNs > 0) {
+        return tc::mbar_wait(bar, parity, abort);
+    } else {
+        *abort = 1;
+        return false;
+    }
 }
 // (a limit of 0: a wait that is not met at once gives up)
 __device__ __forceinline__ bool rows_wait(unsigned bar, unsigned parity, volatile int *abort)
 {
-    return (tc::kWaitNs > 0 ? tc::mbar_try(bar, parity) : tc::mbar_test(bar, parity)) || rows_wait_long(bar, parity, abort);
+    if constexpr (tc::kWaitNs > 0) return tc::mbar_try(bar, parity) || rows_wait_long(bar, parity, abort);
+    return tc::mbar_test(bar, parity) || rows_wait_long(bar, parity, abort);
 }
 // All ones in the bytes of x that have bit `b`.
 __device__ __forceinline__ unsigned rows_bytes(unsigned x, unsigned b) { return (x & 0x01010101u * b) / b * 255u; }
