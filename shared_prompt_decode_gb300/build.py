@@ -34,7 +34,7 @@ def build(force: bool = False, verbose: bool = False, variant: str = "", defines
         if all(os.path.getmtime(f) <= t for f in DEPS):
             return lib
     tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc(), ARCH, "-O3", "--split-compile=0", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-o", tmp] + [f"-D{d}" for d in defines] + SOURCES
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -2127,7 +2127,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 {
     using S = RowsSmem<D, GROUP>;
     using X = Pieces<D, GROUP>;
-    constexpr int NG = S::NG, KH = S::KH;
+    constexpr int NG = S::NG;
     constexpr uint32_t id_s = tc::idesc_f16(kRowsTile, 2 * kRowsKeys), id_z = tc::idesc_f16(kRowsTile, kRowsKeys), id_o = tc::idesc_f16(kRowsTile, D, true);
     extern __shared__ unsigned char smem_rows[];
     S &sm = *reinterpret_cast<S *>(smem_rows + (-smem_u32(smem_rows) & 1023u));
