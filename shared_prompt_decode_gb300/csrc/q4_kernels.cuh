@@ -1292,6 +1292,25 @@ __device__ __forceinline__ void write_column(const Args &a, int lane, size_t pr,
     if (g == 0) __stcg(a.p.part_lse + pr, lse);
 }
 
+// Takes the product with eights off the output, as the end does.  The tensor
+// cores cut what falls below the accumulator's last bit, and codes that are
+// all positive grow it with the number of keys: taken off every kCentre pages
+// the error against fp64 is 3.0e-4 of the result for 32 x 16384 keys, 4.2e-4
+// without it (a result rounded once: 2.1e-4), for 1 us in 84.
+constexpr int kCentre = 32;
+template <int D, int GROUP, int E>
+__device__ __forceinline__ void centre(State<D, GROUP, 1, E> &s)
+{
+#pragma unroll
+    for (int d = 0; d < D / 16; d++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) s.o[0][d][i] = fmaf(s.c[0][d * 16 / GROUP][i & 1], d & 1 ? -16.f : -1.f, s.o[0][d][i]);
+#pragma unroll
+    for (int gi = 0; gi < D / GROUP; gi++)
+#pragma unroll
+        for (int i = 0; i < 4; i++) s.c[0][gi][i] = 0.f;
+}
+
 // Writes the partial of a share, rows pr0 + column.
 template <int D, int GROUP, int NT, int E>
 __device__ __forceinline__ void write_partial(const Args &a, int lane, int nv, State<D, GROUP, NT, E> &s, size_t pr0)
@@ -1496,6 +1515,7 @@ __device__ __forceinline__ void run_share(const Args &a, Smem4 &sm, const Lane<D
                     end[nt][e] = (ql == 1 ? n : keys_seen(n, ql, min(v0 + 8 * nt + 2 * t + e, vlast) / p.G)) - page * kBlock;
             step<D, GROUP, NT, E, KP, false>(at, ln, sh.end - page, qb, qs, s, end, p.scale_log2, a.slack);
         }
+        if ((page - sh.page) % kCentre == kCentre - KP) centre<D, GROUP, E>(s);
         __syncwarp();
         at = at + KP * P::kPage == ring + STAGES * KP * P::kPage ? ring : at + KP * P::kPage;
         ld.fill(a, sm, ln, warp, ch, ring, ++done, closed);

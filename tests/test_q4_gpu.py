@@ -324,6 +324,38 @@ def test_long_contexts_of_one_request():
     check(c, run(c))
 
 
+@pytest.mark.parametrize("D,group,G", [(128, 128, 1), (128, 64, 8), (128, 32, 4), (64, 32, 2)])
+def test_long_shares(D, group, G):
+    """So many keys that a warp goes through far more pages of one head than in the other tests: the sums' last bits.  The
+    reference is formed on the device, in 64 bits."""
+    torch.manual_seed(41)
+    B, Hkv, n = 4, 16, 24000
+    blocks = n // 16
+    codes = [torch.randint(0, 256, (B * blocks, Hkv, 16, D // 2), dtype=torch.uint8, device=DEV) for _ in "kv"]
+    sz = [torch.stack([0.2 + 0.05 * torch.rand(B * blocks, Hkv, 16, D // group, device=DEV),
+                       -1.7 + 0.1 * torch.randn(B * blocks, Hkv, 16, D // group, device=DEV)], -1).half() for _ in "kv"]
+    pool = relay.Q4Cache(codes[0], sz[0], codes[1], sz[1])
+    table = torch.randperm(B * blocks, device=DEV).int().view(B, blocks)
+    q = torch.randn(B, 1, Hkv * G, D, device=DEV).half()
+    out, lse = relay.relay_ctx_attn_q4(q, pool, table, i32([n] * B))
+    for b in range(B):
+        for h in range(0, Hkv, 5):
+            x = []
+            for c, s in zip(codes, sz):
+                ids = table[b].long()
+                w = torch.stack([c[ids, h] & 15, c[ids, h] >> 4], -1).flatten(-2).double().unflatten(-1, (-1, group))
+                x.append((w * s[ids, h, :, :, :1].double() + s[ids, h, :, :, 1:].double()).flatten(-2).flatten(0, 1))
+            p = q[b, 0, h * G:(h + 1) * G].double() @ x[0].T / D ** 0.5
+            ref = torch.softmax(p, -1) @ x[1]
+            got = out[b, 0, h * G:(h + 1) * G].double()
+            # weights rounded by 2^-11 at random, sqrt(sum w^2) of them: their error, and that of n fp32 sums as large
+            # as the values (5 sigma of D G elements' rms)
+            w2 = torch.softmax(p, -1).square().sum(-1, keepdim=True).sqrt()
+            rms = float(((got - ref) / (2.0 ** -11 * w2 * x[1].square().mean().sqrt())).square().mean().sqrt())
+            assert rms < 1.0, f"request {b}, head {h}: {rms:.2f} of the weights' rounding"
+            assert torch.allclose(lse[b, 0, h * G:(h + 1) * G].double(), torch.logsumexp(p, -1), atol=2e-5)
+
+
 def test_prompt_chunks_with_room_for_more():
     """Contexts far shorter than the block tables allow: their splits follow the contexts."""
     c = Case([1500, 20, 900], [130, 1, 40], 2, 1, 128, 128, 10, seed=7)
