@@ -100,7 +100,7 @@ typedef enum {
 #define RELAY_FLAG_BAD_CTX_LEN  2u  /* ctx_lens[b] outside [0, 16*max_blocks_per_seq] */
 #define RELAY_FLAG_BAD_BLOCK    4u  /* a block id outside [0, num_blocks) */
 #define RELAY_FLAG_Q_TOTAL      8u  /* sum of q_lens above max_q_total */
-#define RELAY_FLAG_WAIT_TIMEOUT 16u  /* a bounded wait inside the tensor-core kernel gave up;
+#define RELAY_FLAG_WAIT_TIMEOUT 16u  /* a bounded wait inside a tensor-core kernel gave up;
                                        that call's outputs are not valid */
 
 #define RELAY_FLAG_POOL         32u  /* relay_block_plan: the free list is too short for a request (or its
@@ -411,8 +411,11 @@ size_t relay_workspace_size_q4(const relay_dims_t *dims);
 /* relay_attention_decode and relay_ctx_attn with the contexts in a 4-bit
  * pool.  Scores and sums are held in fp32 and the codes enter the products
  * exactly; the softmax weights times the value scales are rounded to fp16
- * (the fp16 path rounds the weights).  A key that a row does not see has no
- * part in it even where its scales are NaN. */
+ * (the fp16 path rounds the weights), or, for requests with more rows than
+ * stream (a prompt chunk), the values s * c + z.  A key that a row does not see
+ * has no part in it even where its pairs are NaN; a pair that is not finite
+ * makes what is not finite of the rows that see it (of its own dimensions, if
+ * it is a value's).  A chunk may raise RELAY_FLAG_WAIT_TIMEOUT. */
 relay_status_t relay_attention_decode_q4(const relay_dims_t *dims, const void *q, const void *sys_k, const void *sys_v,
                                          const relay_q4_cache_t *cache, const int32_t *block_tables,
                                          const int32_t *ctx_lens, const int32_t *q_lens, void *out, float *lse_out,
