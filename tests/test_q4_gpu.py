@@ -356,6 +356,59 @@ def test_long_shares(D, group, G):
             assert torch.allclose(lse[b, 0, h * G:(h + 1) * G].double(), torch.logsumexp(p, -1), atol=2e-5)
 
 
+@pytest.mark.parametrize("D,group", [(128, 32), (128, 128), (64, 64)])
+@pytest.mark.parametrize("ctx,q_lens,H,Hkv", [
+    ([10, 300, 0], [40, 1, 64], 4, 4),              # rows that see no key; a chunk without a context
+    ([100, 700, 0, 1], [1, 1, 1, 1], 64, 1),        # single rows of 64 heads a group
+    ([500, 130, 64], [60, 0, 33], 10, 2),           # tiles that end inside a row's heads; no rows at all
+    ([63, 64, 65, 128, 129], [63, 64, 65, 33, 34], 2, 2),
+    ([40] * 40, [40] * 40, 1, 1),                   # more requests than columns of one
+    ([2000], [1], 200, 1),
+])
+def test_prompt_chunk_edges(ctx, q_lens, H, Hkv, D, group):
+    c = Case(ctx, q_lens, H, Hkv, D, group, 17, seed=50)
+    check(c, run(c))
+    check(c, run(c, "ctx"), "ctx")
+
+
+def test_two_graphs_of_prompt_chunks_share_a_workspace():
+    """Captured one after the other over one workspace and replayed in turn, with lengths changed in between."""
+    cs = [Case([300, 50], [64, 1], 4, 2, 128, 64, 33, seed=51), Case([80, 400], [1, 64], 4, 2, 128, 64, 33, seed=52)]
+    f = lambda a: torch.from_numpy(a).to(DEV)
+    blocks, num = max(c.max_blocks for c in cs), max(c.num for c in cs)
+    for c in cs:
+        c.table = np.pad(c.table, ((0, 0), (0, blocks - c.max_blocks)), constant_values=-1)
+        c.max_blocks = blocks
+    dims = [relay.make_dims(f(c.q), c.Ls, c.num, blocks, max_q_total=80, Hkv=c.Hkv) for c in cs]
+    w = relay.make_workspace_q4(dims[0])
+    ins = [(f(c.q), f(c.sys_k), f(c.sys_v), c.pool(), i32(c.table), i32(c.ctx), i32(c.q_lens)) for c in cs]
+    outs = [torch.full(c.q.shape, 7.0, dtype=torch.float16, device=DEV) for c in cs]
+    graphs = []
+    s = torch.cuda.Stream()
+    for d, x, o in zip(dims, ins, outs):
+        with torch.cuda.stream(s):
+            relay.relay_attention_decode_q4(*x, out=o, workspace=w, dims=d)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            relay.relay_attention_decode_q4(*x, out=o, workspace=w, dims=d)
+        graphs.append(g)
+    for turn in range(3):
+        if turn == 2:      # the chunks one row shorter
+            for c, x in zip(cs, ins):
+                c.q_lens = [max(1, n - 1) for n in c.q_lens]
+                x[6].copy_(i32(c.q_lens))
+        for c, g, o in zip(cs, graphs, outs):
+            o.fill_(7.0)
+            g.replay()
+        for c, o in zip(cs, outs):
+            ref, _, tol, _ = c.reference()
+            for b, n in enumerate(c.q_lens):
+                within(o[b, :n].double().cpu().numpy(), ref[b, :n], tol[b, :n], f"turn {turn}, request {b}")
+                assert (o[b, n:] == 7.0).all()
+    assert relay.device_status(w) == 0
+
+
 def test_prompt_chunks_with_room_for_more():
     """Contexts far shorter than the block tables allow: their splits follow the contexts."""
     c = Case([1500, 20, 900], [130, 1, 40], 2, 1, 128, 128, 10, seed=7)
