@@ -409,6 +409,20 @@ def test_two_graphs_of_prompt_chunks_share_a_workspace():
     assert relay.device_status(w) == 0
 
 
+@pytest.mark.parametrize("scale", [0.01, 0.6])
+@pytest.mark.parametrize("rows", [1, 5, 40])
+def test_given_scale(scale, rows):
+    c = Case([200, 90], [rows, 1], 4, 2, 128, 64, 30, seed=60)
+    f = lambda a: torch.from_numpy(a).to(DEV)
+    out, lse = relay.relay_ctx_attn_q4(f(c.q), c.pool(), i32(c.table), i32(c.ctx), i32(c.q_lens), scale=scale)
+    c.q = c.q.astype(np.float64) * (scale * np.sqrt(128))      # (the reference takes 1 / sqrt(D))
+    ref, ref_lse, tol, ltol = c.reference("ctx")
+    for b, n in enumerate(c.q_lens):
+        within(out[b, :n].double().cpu().numpy(), ref[b, :n], tol[b, :n], f"out of request {b}")
+        seen = ~np.isinf(ref_lse[b, :n])
+        within(lse[b, :n].double().cpu().numpy()[seen], ref_lse[b, :n][seen], ltol[b, :n][seen], f"lse of request {b}")
+
+
 def test_prompt_chunks_with_room_for_more():
     """Contexts far shorter than the block tables allow: their splits follow the contexts."""
     c = Case([1500, 20, 900], [130, 1, 40], 2, 1, 128, 128, 10, seed=7)
