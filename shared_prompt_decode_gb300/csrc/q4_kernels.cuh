@@ -43,7 +43,7 @@ struct Pool {
 // 0..15, in fp32 with IEEE divisions; s = 0 has code 0, and a group with a NaN
 // or an infinity stores s = z = NaN.  D / 32 lanes take one row of one KV
 // head, K or V: with the instructions of a row's address, group and scale
-// spread over 32 elements the kernel takes 38.6 us for K and V of 6872 rows of
+// spread over 32 elements the kernel takes 39.6 us for K and V of 6872 rows of
 // 32 heads (D = 128, groups of 64; 149 MB, 22 us at the copy rate): what is
 // left is the codes' arithmetic, ten instructions an element pair.  A row of
 // 8 elements a lane took 112 us.  A decode step's 32 rows are one launch.
@@ -1583,9 +1583,9 @@ __device__ __forceinline__ void run_wide(const Args &a, Smem4 &sm, const Lane<D,
 // heads (D = 128, groups of 128, 1.14 GB) take 197 us with the merge, 5.8 TB/s
 // of 6.7 for a copy; a call has about 12 us besides (the line, the first
 // loads, the last partials and their merge), which is what remains of short
-// ones: 16 us at the copy rate and 39 us for 32 requests of 64 to 1024 keys with
+// ones: 16 us at the copy rate and 37 us for 32 requests of 64 to 1024 keys with
 // a prompt of 2048.  With eight query heads a KV head and groups of 64 the
-// arithmetic comes near: 86 us, 49 at the copy rate (32 requests, 1000 to 16384 keys).
+// arithmetic comes near: 85 us, 49 at the copy rate (32 requests, 1000 to 16384 keys).
 //  NT: tensor-core tiles of columns that a sequence may have; E as
 // in State.  It starts beside a grid in front of it that computes the prompt's
 // partials (whichever SMs that leaves) and ends only after it.

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kStepThreads) block_release_kernel(const __gri
 // token and `hpw` of its heads: it forms the D / 2 sines and cosines once,
 // passes them through shared memory, and a lane then holds the eight pairs
 // that it turns in every head (D / 16 lanes a head, two 16-byte loads each,
-// kUnroll heads in flight).  Bound by memory: 44.5 us for 6872 tokens of 64 + 8
+// kUnroll heads in flight).  Bound by memory: 45 us for 6872 tokens of 64 + 8
 // heads (265 MB, 39.6 us at the copy rate); a decode step is a launch and two
 // dependent reads.
 struct RopeAxes {
